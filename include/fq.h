@@ -269,6 +269,135 @@ fq_status fq_linear_heads(const void* x_bf16, int32_t M, int32_t K, int64_t ldx,
                           int32_t head_dim, void* y_bf16,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ FP8 sites with block scales
+ *
+ * A second kind of linear site: both operands hold OCP E4M3 codes (8-bit
+ * floating point, largest value 448) with float32 scales, one for every 128
+ * consecutive k of a token and one for every 128 x 128 block of the weight
+ * (rows 128 b .. 128 b + 127, the last block may be short in rows):
+ *   prologue  h = x, or RMSNorm(x) * gamma as in fq_prologue (no rotation, no smoothing)
+ *             s_a[g][m] = max|h[m][128 g .. +127]| / 448;  q_a = e4m3(h / s_a)
+ *   GEMM      y[m][n] = bf16_rne(sum_g s_a[g][m] s_w[n / 128][g] sum_{k in g} q_a q_w
+ *                                [+ bias[n]] [+ residual[m][n]])
+ * Scales and quotients are float32 (IEEE divide); codes round to nearest, ties
+ * to even, clamped to +-448; a group whose scale is zero has zero codes.  Sums
+ * are float32, of products that the matrix instruction adds in eights after
+ * dropping what lies 2^-13 below the largest exponent among the eight.  The conventions above hold; K is a multiple of
+ * 128, N of 8.  Where an input is not finite, the outputs of its token are not.
+ *   act_codes  [M][K] bytes
+ *   act_scale  float32 [K / 128][ld], ld = M rounded up to a multiple of 4
+ *              (fq_fp8_ascale_count floats; the pad is neither read nor written)
+ *   w_codes    [N][K] bytes;  wscale float32 [ceil(N / 128)][K / 128], 4-byte aligned */
+
+/* Floats of an activation scale matrix and of a weight scale matrix; 0 on bad arguments. */
+size_t fq_fp8_ascale_count(int32_t M, int32_t K);
+size_t fq_fp8_wscale_count(int32_t N, int32_t K);
+
+/* Host packer: W float32 [N][K] (finite) to codes [N][K] and block scales
+ * s = (float)(max|w| / 448); codes are rounded in float64 against the stored scale. */
+fq_status fq_fp8_pack_weights(const float* W, int32_t N, int32_t K, void* codes_out, float* wscale_out);
+
+/* Host: W_out[n][k] = (float)(wscale * code); the NaN codes give NaN. */
+fq_status fq_fp8_dequant_rows(const void* codes, const float* wscale, int32_t N, int32_t K, float* W_out);
+
+/* Device: quantise M bf16 tokens (gamma NULL: no norm). */
+fq_status fq_fp8_prologue(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, const float* gamma, float eps,
+                          void* act_codes, float* act_scale, void* stream);
+
+/* Device: the GEMM and its epilogue.  head_dim 0: y is [M][ldy]; a positive
+ * multiple of 8 dividing N: y is [N / head_dim][M][head_dim] (ldy unused).
+ * M <= 32 streams the weights through a GEMV, whose sums run in another order. */
+fq_status fq_fp8_gemm(const void* act_codes, const float* act_scale, int32_t M, const void* w_codes,
+                      const float* wscale, int32_t N, int32_t K, const float* bias, const void* residual_bf16,
+                      int64_t ldr, int32_t head_dim, void* y_bf16, int64_t ldy, void* stream);
+
+/* Device: prologue then GEMM on one stream.  workspace: at least
+ * fq_fp8_linear_workspace_bytes(M, K) bytes, 256-byte aligned; it holds the
+ * codes and, at the next 256-byte boundary, the scales after the call. */
+size_t fq_fp8_linear_workspace_bytes(int32_t M, int32_t K);
+fq_status fq_fp8_linear(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, const float* gamma, float eps,
+                        const void* w_codes, const float* wscale, int32_t N, const float* bias,
+                        const void* residual_bf16, int64_t ldr, int32_t head_dim, void* y_bf16, int64_t ldy,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ norms around a block
+ *
+ * The norm after a block, its gate and residual scale, the update of the
+ * residual stream and the norm before the next block, in one pass:
+ *   p  = x * (1/sqrt(mean(x^2) + post_eps)) * post_gamma        post_gamma NULL: p = x
+ *   p  = p * gate[m / rows_per_cond]                            gate NULL: 1
+ *   r' = stream_in + res_scale * p                              rounded to the stream's type
+ *   h  = r' * (1/sqrt(mean(r'^2) + pre_eps)) * pre_gamma        of the rounded r'; pre_gamma NULL: unit gain
+ *   h  = h * (1 + mod_scale[m / rows_per_cond]) + mod_shift[m / rows_per_cond]   (either NULL: left out)
+ * float32 arithmetic with the prologue's rules (float64 sums of squares).
+ *   x_bf16      device bf16 [M][ldx], the block's output, or NULL: the stream
+ *               stays as it is (no post_gamma, gate, stream_out) and only h is made
+ *   stream_in/out  device [M][ld] bf16, or float32 with stream_f32 = 1 (ld a
+ *               multiple of 4); they may be the same rows (with equal ld), other
+ *               overlaps are not allowed
+ *   gate, mod_scale, mod_shift  device bf16 [ceil(M / rows_per_cond)][ld_gate / ld_mod]:
+ *               one row for rows_per_cond consecutive rows of x (a sequence's condition)
+ *   h_bf16      device bf16 [M][ld_h] or NULL
+ *   act_codes, act_scale  device, as fq_fp8_prologue writes them (K a multiple
+ *               of 128), made from the float32 h, for fq_fp8_gemm; or both NULL
+ * With neither h_bf16 nor act_codes only the stream is updated.  K is a
+ * multiple of 8, at most 65536. */
+fq_status fq_block_norm(int32_t M, int32_t K, const void* x_bf16, int64_t ldx, const float* post_gamma, float post_eps,
+                        const void* gate_bf16, int64_t ld_gate, float res_scale, const void* stream_in,
+                        int64_t ld_in, void* stream_out, int64_t ld_out, int32_t stream_f32, const float* pre_gamma,
+                        float pre_eps, const void* mod_scale_bf16, const void* mod_shift_bf16, int64_t ld_mod,
+                        int32_t rows_per_cond, void* h_bf16, int64_t ld_h, void* act_codes, float* act_scale,
+                        void* stream);
+
+/* ------------------------------------------------------------------ rotary positions
+ *
+ * Pair i of rot_dim / 2 turns by theta_i = base^(-2 i / rot_dim) radians per
+ * position.  Rules for contexts longer than the trained one:
+ *   FQ_ROPE_PLAIN   theta_i
+ *   FQ_ROPE_LINEAR  theta_i / factor
+ *   FQ_ROPE_BASE    base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   FQ_ROPE_BANDS   theta_i (keep + (1 - keep) / factor), keep = clamp((t_i - low) / (high - low), 0, 1),
+ *                   t_i = trained_len theta_i / (2 pi) turns over the trained length
+ *   FQ_ROPE_RAMP    theta_i (1 - ramp) + theta_i / factor ramp, ramp = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *                   lo = max(floor(at(high)), 0), hi = min(ceil(at(low)), rot_dim - 1),
+ *                   at(n) = rot_dim ln(trained_len / (2 pi n)) / (2 ln base); cos and sin times 0.1 ln(factor) + 1
+ *   FQ_ROPE_PAIRS   theta_i / pair_factors[i]
+ */
+#define FQ_ROPE_PLAIN 0
+#define FQ_ROPE_LINEAR 1
+#define FQ_ROPE_BASE 2
+#define FQ_ROPE_BANDS 3
+#define FQ_ROPE_RAMP 4
+#define FQ_ROPE_PAIRS 5
+
+/* Host plan: freq_out[i], i < rot_dim / 2 (even rot_dim >= 2), the turns per
+ * position of pair i as a 64-bit fraction of a turn (a whole turn = 2^64), and
+ * the factor on cos and sin.  factor, trained_len, low, high and pair_factors
+ * (float32 [rot_dim / 2]) are read by the rules above that name them. */
+fq_status fq_rope_freqs(int32_t rot_dim, double base, int32_t kind, double factor, int32_t trained_len, double low,
+                        double high, const float* pair_factors, uint64_t* freq_out, float* attn_scale_out);
+
+/* Device: rotate heads 0 .. rot_heads - 1 of every token and copy the others
+ * (heads <= 65535, each head_dim values, a multiple of 8).  Element d of head h
+ * of token m is x[m * x_token + h * x_head + d] and y[m * y_token + h * y_head + d]:
+ * a row-major qkv output has x_token = ld, x_head = head_dim, the head layout
+ * x_token = head_dim, x_head = M * head_dim.  Strides are multiples of 8 and at
+ * least head_dim; the heads of y do not overlap.  y may be x with the same
+ * strides (copied heads are then not touched); other overlaps are not allowed.
+ *   (a, b) -> (a c - b s, b c + a s), c = attn_scale cos, s = attn_scale sin of
+ *   the pair's angle, a and b elements i and i + rot_dim / 2 of the head, or
+ *   2 i and 2 i + 1 with interleaved = 1; elements from rot_dim on are copied.
+ * inverse = 1 applies the transposed map: it undoes a rotation made with
+ * attn_scale 1, and it is the gradient of the rotation.
+ *   freq       device uint64 [rot_dim / 2] (fq_rope_freqs), 16-byte aligned
+ *   positions  device int32 [M], any value, or NULL: token m is at pos0 + m
+ * Angles are exact to 2^-32 turns at every position; float32 arithmetic, one
+ * rounding to bf16. */
+fq_status fq_rope(const void* x_bf16, int64_t x_token, int64_t x_head, int32_t M, int32_t heads, int32_t rot_heads,
+                  int32_t head_dim, int32_t rot_dim, int32_t interleaved, const uint64_t* freq, float attn_scale,
+                  const int32_t* positions, int32_t pos0, int32_t inverse, void* y_bf16, int64_t y_token,
+                  int64_t y_head, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

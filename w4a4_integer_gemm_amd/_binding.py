@@ -19,6 +19,9 @@ LIB_PATH = os.environ.get("FQ_LIB") or os.path.join(HERE, "libfq.so")
 
 E2M3 = 6  # FQ_CODES_E2M3: the 4-bit codes stored as FP6 E2M3 (include/fq.h)
 
+# scaling rules of fq_rope_freqs (include/fq.h)
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDS, ROPE_RAMP, ROPE_PAIRS = range(6)
+
 FQ_OK = 0
 _STATUS = {0: "FQ_OK", 1: "FQ_ERR_ARG", 2: "FQ_ERR_SHAPE", 3: "FQ_ERR_UNSUPPORTED", 4: "FQ_ERR_ALIGN",
            5: "FQ_ERR_DEVICE"}
@@ -47,6 +50,21 @@ SIGNATURES = {
     "fq_linear_noalloc_max_bytes": ([], _SZ),
     "fq_linear_heads": ([_P, _I32, _I32, _I64, _P, _F, _P, _I32, _I32, _I32, _P, _P, _I32, _I32, _P, _P, _I64,
                          _I32, _P, _P, _SZ, _P], ctypes.c_int),
+    "fq_fp8_ascale_count": ([_I32, _I32], _SZ),
+    "fq_fp8_wscale_count": ([_I32, _I32], _SZ),
+    "fq_fp8_pack_weights": ([_P, _I32, _I32, _P, _P], ctypes.c_int),
+    "fq_fp8_dequant_rows": ([_P, _P, _I32, _I32, _P], ctypes.c_int),
+    "fq_fp8_prologue": ([_P, _I32, _I32, _I64, _P, _F, _P, _P, _P], ctypes.c_int),
+    "fq_fp8_gemm": ([_P, _P, _I32, _P, _P, _I32, _I32, _P, _P, _I64, _I32, _P, _I64, _P], ctypes.c_int),
+    "fq_fp8_linear_workspace_bytes": ([_I32, _I32], _SZ),
+    "fq_fp8_linear": ([_P, _I32, _I32, _I64, _P, _F, _P, _P, _I32, _P, _P, _I64, _I32, _P, _I64, _P, _SZ, _P],
+                      ctypes.c_int),
+    "fq_block_norm": ([_I32, _I32, _P, _I64, _P, _F, _P, _I64, _F, _P, _I64, _P, _I64, _I32, _P, _F, _P, _P, _I64, _I32,
+                       _P, _I64, _P, _P, _P], ctypes.c_int),
+    "fq_rope_freqs": ([_I32, ctypes.c_double, _I32, ctypes.c_double, _I32, ctypes.c_double, ctypes.c_double, _P, _P, _P],
+                      ctypes.c_int),
+    "fq_rope": ([_P, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _P, _F, _P, _I32, _I32, _P, _I64, _I64, _P],
+                ctypes.c_int),
 }
 
 
@@ -152,6 +170,54 @@ def fq_dequant_rows(codes: np.ndarray, wscale: np.ndarray, K: int, ascale: Optio
     return out
 
 
+def fq_fp8_ascale_count(M: int, K: int) -> int:
+    return lib().fq_fp8_ascale_count(M, K)
+
+
+def fq_fp8_wscale_count(N: int, K: int) -> int:
+    return lib().fq_fp8_wscale_count(N, K)
+
+
+def fq_fp8_linear_workspace_bytes(M: int, K: int) -> int:
+    return lib().fq_fp8_linear_workspace_bytes(M, K)
+
+
+def fq_fp8_pack_weights(W: np.ndarray):
+    """Host packer; returns (codes uint8 [N][K], wscale float32 [ceil(N / 128)][K / 128])."""
+    W = np.ascontiguousarray(W, dtype=np.float32)
+    N, K = W.shape
+    codes = np.zeros((N, K), np.uint8)
+    ws = np.zeros((-(-N // 128), max(K // 128, 0)), np.float32)
+    _check(lib().fq_fp8_pack_weights(_np_ptr(W), N, K, _np_ptr(codes), _np_ptr(ws)))
+    return codes, ws
+
+
+def fq_fp8_dequant_rows(codes: np.ndarray, wscale: np.ndarray) -> np.ndarray:
+    """Host dequantisation; returns float32 [N][K]."""
+    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    ws = np.ascontiguousarray(wscale, dtype=np.float32)
+    N, K = codes.shape
+    if ws.size != fq_fp8_wscale_count(N, K):
+        raise ValueError(f"wscale has {ws.size} values, not {fq_fp8_wscale_count(N, K)} for N={N} K={K}")
+    out = np.empty((N, K), np.float32)
+    _check(lib().fq_fp8_dequant_rows(_np_ptr(codes), _np_ptr(ws), N, K, _np_ptr(out)))
+    return out
+
+
+def fq_rope_freqs(rot_dim: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0,
+                  trained_len: int = 1, low: float = 1.0, high: float = 32.0,
+                  pair_factors: Optional[np.ndarray] = None):
+    """Host plan; returns (freq uint64 [rot_dim / 2], factor on cos and sin)."""
+    pf = None if pair_factors is None else np.ascontiguousarray(pair_factors, dtype=np.float32)
+    if pf is not None and pf.size != rot_dim // 2:
+        raise ValueError(f"pair_factors has {pf.size} values, not {rot_dim // 2}")
+    freq = np.zeros(max(rot_dim // 2, 1), np.uint64)
+    scale = ctypes.c_float()
+    _check(lib().fq_rope_freqs(rot_dim, base, kind, factor, trained_len, low, high, _np_ptr(pf), _np_ptr(freq),
+                               ctypes.byref(scale)))
+    return freq, scale.value
+
+
 # ------------------------------------------------------------------ device entry points
 def _dptr(t) -> Optional[int]:
     if t is None:
@@ -223,3 +289,38 @@ def fq_linear_heads(x, M: int, K: int, ldx: int, gamma_folded, eps: float, ascal
 
 def fq_geglu(gateup, M: int, F: int, ld_in: int, h, ld_out: int, stream=None):
     _check(lib().fq_geglu(_dptr(gateup), M, F, ld_in, _dptr(h), ld_out, _stream(stream)))
+
+
+def fq_fp8_prologue(x, M: int, K: int, ldx: int, gamma, eps: float, act_codes, act_scale, stream=None):
+    _check(lib().fq_fp8_prologue(_dptr(x), M, K, ldx, _dptr(gamma), eps, _dptr(act_codes), _dptr(act_scale),
+                                 _stream(stream)))
+
+
+def fq_fp8_gemm(act_codes, act_scale, M: int, w_codes, wscale, N: int, K: int, bias, residual, ldr: int,
+                head_dim: int, y, ldy: int, stream=None):
+    _check(lib().fq_fp8_gemm(_dptr(act_codes), _dptr(act_scale), M, _dptr(w_codes), _dptr(wscale), N, K, _dptr(bias),
+                             _dptr(residual), ldr, head_dim, _dptr(y), ldy, _stream(stream)))
+
+
+def fq_fp8_linear(x, M: int, K: int, ldx: int, gamma, eps: float, w_codes, wscale, N: int, bias, residual, ldr: int,
+                  head_dim: int, y, ldy: int, workspace, workspace_bytes: int, stream=None):
+    _check(lib().fq_fp8_linear(_dptr(x), M, K, ldx, _dptr(gamma), eps, _dptr(w_codes), _dptr(wscale), N, _dptr(bias),
+                               _dptr(residual), ldr, head_dim, _dptr(y), ldy, _dptr(workspace), workspace_bytes,
+                               _stream(stream)))
+
+
+def fq_block_norm(M: int, K: int, x, ldx: int, post_gamma, post_eps: float, gate, ld_gate: int, res_scale: float,
+                  stream_in, ld_in: int, stream_out, ld_out: int, stream_f32: int, pre_gamma, pre_eps: float, mod_scale,
+                  mod_shift, ld_mod: int, rows_per_cond: int, h, ld_h: int, act_codes=None, act_scale=None,
+                  stream=None):
+    _check(lib().fq_block_norm(M, K, _dptr(x), ldx, _dptr(post_gamma), post_eps, _dptr(gate), ld_gate, res_scale,
+                               _dptr(stream_in), ld_in, _dptr(stream_out), ld_out, stream_f32, _dptr(pre_gamma),
+                               pre_eps, _dptr(mod_scale), _dptr(mod_shift), ld_mod, rows_per_cond, _dptr(h), ld_h,
+                               _dptr(act_codes), _dptr(act_scale), _stream(stream)))
+
+
+def fq_rope(x, x_token: int, x_head: int, M: int, heads: int, rot_heads: int, head_dim: int, rot_dim: int,
+            interleaved: int, freq, attn_scale: float, positions, pos0: int, inverse: int, y, y_token: int, y_head: int,
+            stream=None):
+    _check(lib().fq_rope(_dptr(x), x_token, x_head, M, heads, rot_heads, head_dim, rot_dim, interleaved, _dptr(freq),
+                         attn_scale, _dptr(positions), pos0, inverse, _dptr(y), y_token, y_head, _stream(stream)))

@@ -2,7 +2,7 @@
 run under it (AddressSanitizer + UndefinedBehaviorSanitizer).
 
 The host code -- argument validation, error messages, the weight packer and
-dequantiser (fq_api.cpp, fq_pack.cpp) -- and the oracle (fqo.c) are compiled
+dequantiser, the FP8 and rotary host parts (HOST_SOURCES) -- and the oracle (fqo.c) are compiled
 with g++/gcc and -fsanitize=address,undefined; the HIP kernel objects are
 taken unchanged from the ordinary build (run build.py first), since device
 code is not sanitized.  The result, libfq_san.so and oracle/liboracle_san.so,
@@ -25,13 +25,14 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libfq_san.so")
 ORACLE_LIB = os.path.join(ROOT, "oracle", "liboracle_san.so")
 SAN = ["-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer", "-g"]
-HOST_SOURCES = ["fq_api.cpp", "fq_pack.cpp"]
+HOST_SOURCES = ["fq_api.cpp", "fq_pack.cpp", "fq_api_block.cpp", "fq_fp8_pack.cpp", "fq_rope_plan.cpp"]
 # the library's kernels, as the ordinary build compiled them (its list of sources)
 sys.path.insert(0, ROOT)
 from w4a4_integer_gemm_amd.build import SOURCES as _LIB_SOURCES  # noqa: E402
 
 DEVICE_OBJECTS = [os.path.splitext(s)[0] + ".o" for s in _LIB_SOURCES if s.endswith(".hip")]
-TESTS = ["tests/test_abi_cpu.py", "tests/test_oracle_pins.py", "tests/test_fold_consistency.py"]
+TESTS = ["tests/test_abi_cpu.py", "tests/test_oracle_pins.py", "tests/test_fold_consistency.py",
+         "tests/test_block_cpu.py"]
 
 
 def run(cmd):

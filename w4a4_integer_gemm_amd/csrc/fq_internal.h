@@ -102,6 +102,79 @@ hipError_t launch_gemv(const GemmArgs& a, const DeviceInfo& dev, hipStream_t str
 // it, and the launch (prologue arguments and GEMM arguments of the same call).
 bool decode1_eligible(const PrologueArgs& p, const GemmArgs& g);
 hipError_t launch_decode1(const PrologueArgs& p, const GemmArgs& g, hipStream_t stream);
+// Rows of the block norms and of the FP8 prologue (fq_block_norm.hip):
+//   r' = r + res_scale * gate * norm(x; post_gamma)   (only with x)
+//   h  = norm(r'; pre_gamma) * (1 + mod_scale) + mod_shift
+// h leaves as bf16 rows, as e4m3 codes with their scales, or both.
+struct NormArgs {
+    int32_t M, K;
+    const uint16_t* x;  // nullptr: the stream is taken as it is
+    int64_t ldx;
+    const float* post_gamma;  // nullptr: x is added without a norm
+    float post_eps;
+    const uint16_t* gate;  // nullptr: 1
+    int64_t ld_gate;
+    float res_scale;
+    const void* r_in;  // bf16, or float32 with stream_f32
+    int64_t ld_rin;
+    void* r_out;  // nullptr: not written
+    int64_t ld_rout;
+    int32_t stream_f32;
+    int32_t pre_norm;        // 0: h = r' (the FP8 prologue of a quant-only site)
+    const float* pre_gamma;  // nullptr: unit gain
+    float pre_eps;
+    const uint16_t* mod_scale;  // nullptr: 0
+    const uint16_t* mod_shift;  // nullptr: 0
+    int64_t ld_mod;
+    int32_t rows_per_cond;
+    uint16_t* h;  // nullptr: not written
+    int64_t ld_h;
+    uint8_t* codes;    // nullptr: not written
+    float* act_scale;  // [K / 128][fp8_scale_ld(M)]
+};
+// Pieces of 8 values per lane (1, 2, 4 or 8) and threads of a row's workgroup.
+inline int block_norm_pieces(int32_t K) { return K <= 8192 ? 1 : K <= 16384 ? 2 : K <= 32768 ? 4 : 8; }
+inline int block_norm_threads(int32_t K) {
+    const int P = block_norm_pieces(K);
+    return ((K / 8 + P - 1) / P + 63) / 64 * 64;
+}
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream);
+
+// FP8 sites: row stride of an activation scale matrix [K / 128][ld] in floats
+// (16-byte aligned rows), and the GEMM's arguments.
+__host__ __device__ inline int32_t fp8_scale_ld(int32_t M) { return (M + 3) / 4 * 4; }
+struct Fp8Args {
+    const uint8_t* act;      // e4m3 [M][K]
+    const float* act_scale;  // [K / 128][fp8_scale_ld(M)]
+    int32_t M;
+    const uint8_t* w;     // e4m3 [N][K]
+    const float* wscale;  // [ceil(N / 128)][K / 128]
+    int32_t N, K;
+    const float* bias;         // nullptr: none
+    const uint16_t* residual;  // nullptr: none
+    int64_t ldr;
+    uint16_t* y;
+    int64_t ldy;
+    int32_t head_dim;  // 0: y is [M][ldy]; else y is [N/head_dim][M][head_dim]
+};
+hipError_t launch_fp8_gemm(const Fp8Args& g, hipStream_t stream);
+hipError_t launch_fp8_gemv(const Fp8Args& g, hipStream_t stream);
+
+// Rotary positions (fq_rope.hip).
+struct RopeArgs {
+    const uint16_t* x;
+    int64_t x_token, x_head;
+    int32_t M, heads, rot_heads, head_dim, rot_dim, interleaved;
+    const uint64_t* freq;  // [rot_dim / 2] turns per position, fraction of a turn in 2^-64
+    float attn_scale;
+    const int32_t* positions;  // nullptr: pos0 + m
+    int32_t pos0;
+    int32_t inverse;
+    uint16_t* y;
+    int64_t y_token, y_head;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
+
 hipError_t launch_geglu(const uint16_t* gu, int32_t M, int32_t F, int64_t ld_in, uint16_t* h, int64_t ld_out,
                         hipStream_t stream);
 

@@ -136,3 +136,88 @@ class DeviceSite:
     @staticmethod
     def upload(a, device="cuda"):
         return _to_dev(a, device)
+
+
+class Fp8Site:
+    """One FP8 site with block scales: x [M][K] bf16 -> y [M][N] bf16.
+
+    W float32 [N][K], or codes [N][K] and wscale [ceil(N / 128)][K / 128] as a
+    checkpoint stores them (numpy arrays, or torch tensors already on the
+    device); gamma: RMSNorm gain (None for a quant-only site)."""
+
+    def __init__(self, W: Optional[np.ndarray] = None, gamma=None, bias=None, eps: float = 1e-6, device="cuda",
+                 codes=None, wscale=None):
+        import torch
+        self.device = torch.device(device)
+        self.eps = float(eps)
+        if codes is None:
+            codes, wscale = B.fq_fp8_pack_weights(W)
+        self.N, self.K = codes.shape
+        self.codes = codes if isinstance(codes, torch.Tensor) else _to_dev(codes, self.device)
+        self.wscale = wscale if isinstance(wscale, torch.Tensor) else _to_dev(np.asarray(wscale, np.float32), self.device)
+        if not (self.codes.is_contiguous() and self.wscale.is_contiguous()):
+            raise ValueError("codes and wscale must be contiguous")
+        if self.codes.element_size() != 1 or self.wscale.dtype != torch.float32:
+            raise ValueError("codes are bytes and wscale is float32")
+        if self.wscale.numel() != B.fq_fp8_wscale_count(self.N, self.K):
+            raise ValueError(f"wscale has {self.wscale.numel()} values, not {B.fq_fp8_wscale_count(self.N, self.K)} "
+                             f"for N={self.N} K={self.K}")
+        self.gamma = _to_dev(None if gamma is None else np.ascontiguousarray(gamma, np.float32), self.device)
+        self.bias = _to_dev(None if bias is None else np.ascontiguousarray(bias, np.float32), self.device)
+        self._ws = None
+        self._ws_bytes = {}  # M -> fq_fp8_linear_workspace_bytes
+
+    # -- buffers
+    def workspace(self, M: int):
+        import torch
+        nbytes = self._ws_bytes.get(M)
+        if nbytes is None:
+            nbytes = self._ws_bytes[M] = B.fq_fp8_linear_workspace_bytes(M, self.K)
+        if self._ws is None or self._ws.numel() < nbytes:
+            self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return self._ws
+
+    def workspace_codes(self, M: int):
+        """(codes [M][K], scales [K / 128][M]) views of the workspace after linear()."""
+        import torch
+        ws = self.workspace(M)
+        nb = M * self.K
+        off = (nb + 255) // 256 * 256
+        sc = ws[off:off + 4 * B.fq_fp8_ascale_count(M, self.K)].view(torch.float32)
+        return ws[:nb].view(M, self.K), sc.view(self.K // 128, -1)[:, :M]
+
+    def empty_codes(self, M: int):
+        import torch
+        return (torch.empty((M, self.K), dtype=torch.uint8, device=self.device),
+                torch.empty((self.K // 128, -(-M // 4) * 4), dtype=torch.float32, device=self.device))
+
+    def _out(self, M: int, head_dim: int):
+        import torch
+        shape = (self.N // head_dim, M, head_dim) if head_dim else (M, self.N)
+        return torch.empty(shape, dtype=torch.int16, device=self.device)
+
+    # -- calls
+    def prologue(self, x, codes=None, scales=None, stream=None):
+        M = x.shape[0]
+        if codes is None:
+            codes, scales = self.empty_codes(M)
+        B.fq_fp8_prologue(x, M, self.K, x.stride(0), self.gamma, self.eps, codes, scales, stream)
+        return codes, scales
+
+    def gemm(self, codes, scales, M: int, residual=None, head_dim: int = 0, y=None, stream=None):
+        """y [M][N], or [N / head_dim][M][head_dim], from codes that a prologue or fq_block_norm wrote."""
+        if y is None:
+            y = self._out(M, head_dim)
+        B.fq_fp8_gemm(codes, scales, M, self.codes, self.wscale, self.N, self.K, self.bias, residual,
+                      0 if residual is None else residual.stride(0), head_dim, y, 0 if head_dim else y.stride(0), stream)
+        return y
+
+    def linear(self, x, residual=None, head_dim: int = 0, y=None, stream=None):
+        M = x.shape[0]
+        if y is None:
+            y = self._out(M, head_dim)
+        ws = self.workspace(M)
+        B.fq_fp8_linear(x, M, self.K, x.stride(0), self.gamma, self.eps, self.codes, self.wscale, self.N, self.bias,
+                        residual, 0 if residual is None else residual.stride(0), head_dim, y,
+                        0 if head_dim else y.stride(0), ws, ws.numel(), stream)
+        return y
