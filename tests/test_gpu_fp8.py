@@ -206,6 +206,47 @@ def test_linear_is_repeatable_and_leaves_its_inputs():
         assert np.array_equal(host(x, np.uint16), xb)
 
 
+TILES = ["256x256", "256x128", "128x192", "128x160", "128x128", "128x96", "128x64", "64x128", "64x64"]
+
+
+@pytest.mark.parametrize("tile", TILES)
+def test_every_tile_shape(tile, hook):
+    hook("fp8_tile=" + tile)
+    rng = np.random.default_rng(len(tile))
+    for M, N, K in ((33, 8, 128), (130, 264, 384), (257, 392, 256), (64, 520, 1152)):
+        qa, sa, qw, sw = rand_site(rng, M, N, K)
+        bias, residual = rng.standard_normal(N).astype(np.float32), ref.bf16(rng, M, N)
+        y, tol = ref.fp8_gemm(qa, sa, qw, sw, bias, residual)
+        ref.assert_gemm(run_gemm(qa, sa, qw, sw, bias, residual), y, tol, f"{tile} {M}x{N}x{K}")
+        ref.assert_gemm(run_gemm(qa, sa, qw, sw, bias, residual, head_dim=8), y, tol, f"{tile} {M}x{N}x{K} heads")
+
+
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("K", [128, 256, 640])
+def test_more_tiles_than_workgroups(tile, K, hook):
+    """Each workgroup runs several tiles, its copies ahead into the next one; sampled outputs."""
+    hook("fp8_tile=" + tile)
+    M, N = (4101, 5000) if tile == "256x256" else (2053, 5000)
+    rng = np.random.default_rng(K)
+    qa, sa, qw, sw = rand_site(rng, M, N, K)
+    got = run_gemm(qa, sa, qw, sw)
+    rows = np.unique(np.concatenate([np.arange(0, M, 293), [M - 1]]))
+    b = np.array([0, 1, 7, 20, 38])
+    cols = (128 * b[:, None] + np.arange(128)).ravel()
+    y, tol = ref.fp8_gemm(qa[rows], sa[:, rows], qw[cols], sw[b])
+    ref.assert_gemm(got[np.ix_(rows, cols)], y, tol, f"{tile} K={K}")
+    # every output of a workgroup's tiles: against a float32 product of the same codes, coarsely
+    import torch
+    tab = torch.from_numpy(ref.TABLE.astype(np.float32)).cuda()
+    a = tab[torch.from_numpy(qa.astype(np.int64)).cuda()] * dev(sa).t().repeat_interleave(128, 1)
+    w = tab[torch.from_numpy(qw.astype(np.int64)).cuda()] * dev(sw).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)
+    full = (a @ w.t()).cpu().numpy()
+    g = bf16_to_f64(got)
+    scale = np.sqrt(np.mean(full.astype(np.float64) ** 2))
+    # the bf16 rounding (2^-8) and sums of products cut at 2^-13 of the largest of eight
+    assert np.all(np.abs(g - full) <= 2.0 ** -7 * np.abs(full) + 2.0 ** -7 * scale)
+
+
 def test_full_size_layers_sampled():
     """The gate+up decode layer, prefills of the qkv and down layers, on sampled outputs."""
     rng = np.random.default_rng(13)

@@ -27,10 +27,10 @@ void clear_error() { g_error.clear(); }
 namespace {
 
 // Applies a test-hook spec "key=value,key=value" (keys gemm_tile, gemm_mfma,
-// gemv, decode1; "" or "default" resets every hook).  Returns false, with the reason in
+// fp8_tile, gemv, decode1; "" or "default" resets every hook).  Returns false, with the reason in
 // *why, on an unknown key or value; nothing changes then.
 bool apply_hooks(Hooks& h, const char* spec, std::string* why) {
-    int tile = -1, mfma = 16, split = 0, d1off = 0;
+    int tile = -1, fp8 = -1, mfma = 16, split = 0, d1off = 0;
     std::string s = spec ? spec : "";
     if (s == "default") s.clear();
     size_t pos = 0;
@@ -46,6 +46,12 @@ bool apply_hooks(Hooks& h, const char* spec, std::string* why) {
             tile = val == "auto" ? -1 : gemm_tile_id(val.c_str());
             if (tile < 0 && val != "auto") {
                 *why = "unknown gemm_tile '" + val + "'";
+                return false;
+            }
+        } else if (key == "fp8_tile") {
+            fp8 = val == "auto" ? -1 : fp8_tile_id(val.c_str());
+            if (fp8 < 0 && val != "auto") {
+                *why = "unknown fp8_tile '" + val + "'";
                 return false;
             }
         } else if (key == "gemm_mfma") {
@@ -67,11 +73,12 @@ bool apply_hooks(Hooks& h, const char* spec, std::string* why) {
             }
             d1off = val == "off";
         } else {
-            *why = "unknown hook '" + key + "' (gemm_tile, gemm_mfma, gemv, decode1)";
+            *why = "unknown hook '" + key + "' (gemm_tile, gemm_mfma, fp8_tile, gemv, decode1)";
             return false;
         }
     }
     h.gemm_tile.store(tile, std::memory_order_relaxed);
+    h.fp8_tile.store(fp8, std::memory_order_relaxed);
     h.gemm_mfma.store(mfma, std::memory_order_relaxed);
     h.gemv_split.store(split, std::memory_order_relaxed);
     h.decode1_off.store(d1off, std::memory_order_relaxed);

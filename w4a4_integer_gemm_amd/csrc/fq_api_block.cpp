@@ -116,8 +116,8 @@ fq::NormArgs prologue_args(const void* x, int32_t M, int32_t K, int64_t ldx, con
     return a;
 }
 
-fq_status run_fp8_gemm(const char* fn, const fq::Fp8Args& g, hipStream_t stream) {
-    return device_status(fn, g.M <= fq::kGemvMaxM ? fq::launch_fp8_gemv(g, stream) : fq::launch_fp8_gemm(g, stream));
+fq_status run_fp8_gemm(const char* fn, const fq::Fp8Args& g, const fq::DeviceInfo& dev, hipStream_t stream) {
+    return device_status(fn, g.M <= fq::kGemvMaxM ? fq::launch_fp8_gemv(g, stream) : fq::launch_fp8_gemm(g, dev, stream));
 }
 
 }  // namespace
@@ -157,7 +157,7 @@ fq_status fq_fp8_gemm(const void* act_codes, const float* act_scale, int32_t M, 
     fq::Fp8Args g{static_cast<const uint8_t*>(act_codes), act_scale, M, static_cast<const uint8_t*>(w_codes), wscale,
                   N, K, bias, static_cast<const uint16_t*>(residual_bf16), ldr, static_cast<uint16_t*>(y_bf16), ldy,
                   head_dim};
-    return run_fp8_gemm(fn, g, static_cast<hipStream_t>(stream));
+    return run_fp8_gemm(fn, g, *dev, static_cast<hipStream_t>(stream));
 }
 
 fq_status fq_fp8_linear(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, const float* gamma, float eps,
@@ -184,7 +184,7 @@ fq_status fq_fp8_linear(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, c
     fq::Fp8Args g{codes, scales, M, static_cast<const uint8_t*>(w_codes), wscale, N, K, bias,
                   static_cast<const uint16_t*>(residual_bf16), ldr, static_cast<uint16_t*>(y_bf16), ldy, head_dim};
     FQ_TRY(device_status(fn, fq::launch_block_norm(prologue_args(x_bf16, M, K, ldx, gamma, eps, codes, scales), s)));
-    return run_fp8_gemm(fn, g, s);
+    return run_fp8_gemm(fn, g, *dev, s);
 }
 
 fq_status fq_block_norm(int32_t M, int32_t K, const void* x_bf16, int64_t ldx, const float* post_gamma, float post_eps,

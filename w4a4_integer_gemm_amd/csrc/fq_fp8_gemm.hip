@@ -6,26 +6,39 @@
 // One instruction covers one scale group exactly: it multiplies 16 weight
 // rows by 16 tokens over 128 k from a zero accumulator, and the four results a
 // lane holds (four rows of one 128-row block, one token) are added to the
-// float32 sums with one fma each, scaled by sa * sw (one product per lane,
-// token fragment and stage).
+// float32 sums with one fma each, scaled by sa * sw.
 //
-// Tile BM tokens x BN weight rows, one k stage = 128 codes of every row.  Four
-// load waves copy a stage into an LDS ring slot with global_load_lds_dwordx4;
-// four MFMA waves split the tile 2 x 2.  A row's 16-byte chunk c sits at slot
-// 8 row + (c ^ ((row / 2) % 8)), so the 16 lanes of an LDS read phase (16
-// consecutive rows, one chunk) take 16 distinct groups of four banks.
+// A k stage is the 128 codes of the tile's BM tokens and BN weight rows, the
+// tokens' BM scales and the scales of the weight rows' blocks; NS stages live in
+// LDS, copied there without passing through registers.  A stage's 16-byte chunk
+// c of row rho sits at slot 8 rho + (c ^ ((rho / 2) % 8)), so the 16 lanes of an
+// LDS read phase (16 consecutive rows, one chunk) take 16 distinct groups of
+// four banks.
 //
-// Ring protocol (barrier B(s) ends MFMA iteration s; B(-1) precedes it):
-//   - an MFMA wave reads stage 0 after B(-1) and stage s + 1 during iteration
-//     s, and waits for those reads before B(s): after B(s) the slots of
-//     stages <= s + 1 are free;
-//   - the load waves first fill the slots of stages 0 .. NS-2; at iteration s
-//     a load wave refills slot (s - 1) mod NS (free since B(s - 1); at s = 0
-//     the slot still empty) with stage s + NS - 1, waits until stage s + 2 has
-//     landed, and reaches B(s), which publishes it for iteration s + 1's reads.
+// A multiplying wave holds its TW weight fragments of a stage in registers and
+// runs through its TF token fragments, reading each one step ahead; the sums of
+// a step are scaled and added between the next step's products.  Before the
+// products of a stage's last step its LDS reads have returned: the barrier there
+// frees the stage's slot and publishes the next stage, whose first fragments
+// are read behind the last step's products.  Copies run NS - 1 stages ahead,
+// from four waves that do nothing else, or, on the largest tile, from the first
+// four of the eight multiplying waves (one per SIMD: while one waits to issue a
+// copy the other wave of its SIMD multiplies).
+//
+// Workgroups are persistent: as many as fit the chip, each running through its
+// tiles with the copies going on into the next tile, so that only a tile's
+// epilogue interrupts the products.
+//
+// Measured (4096 x 3584 x 37888, 256 x 256 tiles): 530 us, 2100 TFLOP/s, against
+// 890 us for the first version, whose stages waited for their scales from
+// global memory.  What bounds it is power and the copies: without copies the same
+// loop takes 430 us, and the clock falls to 1.6 GHz from 2.4 with both.  A
+// prefetch of later stages into L2 (one dword of each line) made it slower
+// (594 us; shared among the workgroups of an XCD 563).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 #include <type_traits>
 
 #include "fq_device.h"
@@ -36,170 +49,387 @@
 namespace fq {
 namespace {
 
-constexpr int kThreads = 512;  // 4 load waves + 4 MFMA waves
-constexpr int kLdsMax = 160 * 1024;
-
-template <int BM_, int BN_>
+template <int BM_, int BN_, int WM_, int WN_, int LW_, int OCC_, int NS_>
 struct Fp8Cfg {
-    static constexpr int BM = BM_, BN = BN_;
-    static constexpr int STAGE = (BM + BN) * 128;
-    static constexpr int COPIES = STAGE / 1024;  // 1 KB copies of 8 rows
-    static constexpr int NHI = COPIES / 4;       // per load wave
-    static constexpr int NS = kLdsMax / STAGE > 8 ? 8 : kLdsMax / STAGE;
+    static constexpr int BM = BM_, BN = BN_;  // tokens and weight rows of a tile
+    static constexpr int WM = WM_, WN = WN_;  // waves along each
+    static constexpr int OCC = OCC_;          // waves of a SIMD that share the registers
+    static constexpr int NS = NS_;            // stages in LDS
+    static constexpr int LW = LW_;            // waves that only copy (0: the multiplying waves copy)
+    static constexpr int MW = WM * WN, WAVES = MW + LW, THREADS = 64 * WAVES;
+    static constexpr int WGS = OCC * 4 / WAVES;                 // workgroups per CU
+    static constexpr int TF = BM / WM / 16, TW = BN / WN / 16;  // fragments of a wave
+    static constexpr int COPIES = (BM + BN) / 8;                // 1 KB copies of 8 rows
+    static constexpr int CW = LW ? LW : MW == 8 ? 4 : MW;       // waves that copy: one per SIMD
+    static constexpr int NC = (COPIES + CW - 1) / CW;           // per copying wave
+    static constexpr bool EVEN = (BM / 8) % CW == 0 && COPIES % CW == 0;  // every copying wave's first BM / 8 / CW are tokens
+    static constexpr int SA_OFF = (BM + BN) * 128;              // the tokens' scales (one 1 KB copy)
+    static constexpr int SW_OFF = SA_OFF + 1024;                // the row blocks' scales (one 256-byte copy)
+    static constexpr int STAGE = SW_OFF + 256;
     static constexpr int LDS = NS * STAGE;
-    static constexpr int TF = BM / 32;  // token fragments per MFMA wave
-    static constexpr int TW = BN / 32;  // weight fragments per MFMA wave
-    static_assert(BM % 32 == 0 && BN % 32 == 0, "whole fragments per wave");
-    static_assert(COPIES % 4 == 0, "the load waves' shares are equal");
-    static_assert(BN / 2 <= 128 && 128 % (BN / 2) == 0, "a wave's rows stay in one scale block");
-    static_assert(NS >= 4, "the ring needs four stages");
-    static_assert((NS - 2) * NHI < 64, "vmcnt range");
+    static constexpr bool ALIGNED = BN % 128 == 0 && 128 % (16 * TW) == 0;  // a wave's rows share one scale block
+    static constexpr int UNITS = (TF - 1) * TW;                 // products before a stage's last step
+    static constexpr int SPREAD = UNITS / 4 > 0 ? UNITS / 4 : 1;  // those with copies behind them
+    static constexpr int NP = ALIGNED ? 1 : TW;                            // scale products per token fragment
+    static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "whole fragments per wave");
+    static_assert(BM <= 256, "one copy holds the tokens' scales");
+    static_assert(TF % 2 == 0, "the two token registers alternate from stage to stage");
+    static_assert(CW >= 2 && CW % 2 == 0 && WGS >= 1, "two waves copy the scales; a wave's rows share their swizzle");
+    static_assert(LDS * WGS <= 160 * 1024, "LDS of a CU");
+    // With copying waves and four stages a barrier publishes the stage after the
+    // next, so that the next one's first fragments are read without waiting for it.
+    static constexpr bool EARLY = LW > 0 && NS >= 4;
+    static constexpr int FLIGHT = EARLY ? NS - 3 : NS - 2;  // newest stages that may be in flight at a barrier
+    static_assert(FLIGHT >= 0 && FLIGHT * (NC + 1) < 64, "slots of the ring; vmcnt range");
 };
 
+// Copies global -> LDS, lane l's bytes landing at lds_dst + 16 l or + 4 l, in
+// inline asm for the reason given at copy16_to_lds (no VGPR result).  The five
+// wait states cover scalar operands that a vector instruction has just written
+// (v_readfirstlane, or v_readlane of a spilled register), which the compiler
+// does not see being read by a memory instruction here, and the M0 write.
+//
+// 16 bytes from a buffer descriptor at voff + soff; what lies past its end
+// reads as zero.
+__device__ __forceinline__ void copy16_buffer(const v4i& rsrc, uint32_t voff, uint32_t soff, uint32_t lds_dst) {
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_dst)
+                 : "memory");
+}
+// 16 or 4 bytes from base + voff.
+__device__ __forceinline__ void copy16_base(const uint8_t* base, uint32_t voff, uint32_t lds_dst) {
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds_dst) : "memory");
+}
+__device__ __forceinline__ void copy4_base(const uint8_t* base, uint32_t voff, uint32_t lds_dst) {
+    asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds_dst) : "memory");
+}
+
+// Descriptor of `bytes` bytes at p (wave uniform): base, no stride, size, raw 32-bit data.
+__device__ __forceinline__ v4i buffer_of(const uint8_t* p, uint32_t bytes) {
+    const uint64_t u = reinterpret_cast<uintptr_t>(p);
+    return v4i{__builtin_amdgcn_readfirstlane(int(u)), __builtin_amdgcn_readfirstlane(int(u >> 32)),
+               __builtin_amdgcn_readfirstlane(int(bytes)), 0x00020000};
+}
+
+typedef __attribute__((address_space(3))) const float lds_cfloat;
+__device__ __forceinline__ float lds_float(uint32_t addr) { return *reinterpret_cast<lds_cfloat*>(uintptr_t(addr)); }
+
 template <class CF>
-__global__ __launch_bounds__(kThreads) void fp8_gemm_kernel(Fp8Args g, int tiles_m, int tiles_n) {
+__global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF::OCC, CF::OCC))) void fp8_gemm_kernel(
+    Fp8Args g, int tiles_m, int tiles_n, int group_m) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[CF::LDS];
+    constexpr int TF = CF::TF, TW = CF::TW, NC = CF::NC, NS = CF::NS, NP = CF::NP;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
-    // XCD-aware tile order: dispatch b runs on XCD b % 8, which takes the tile
-    // range [x per, (x + 1) per), m fastest
-    const int ntiles = tiles_m * tiles_n;
-    int t = blockIdx.x;
-    if (ntiles % 8 == 0) t = (blockIdx.x % 8) * (ntiles / 8) + blockIdx.x / 8;
-    const int m0 = (t % tiles_m) * CF::BM, n0 = (t / tiles_m) * CF::BN;
-    const int64_t ld = g.K;
+    const int cw = CF::LW ? wave - CF::MW : wave;  // copying wave (0 .. CW - 1), or none
+    const int q = lane >> 4;
     const int nk = g.K / 128;
+    const int lda = fp8_scale_ld(g.M);
+    const uint32_t lds0 = lds_address(lds);
 
-    if (wave >= 4) {
-        // copy q = p + 4 i of a stage is rows 8 q .. 8 q + 7 (tokens first):
-        // lane l fills the slot of row 8 q + l / 8 and chunk (l % 8) ^ swizzle
-        const int p = wave - 4;
-        uint32_t voff[CF::NHI];
-#pragma unroll
-        for (int i = 0; i < CF::NHI; ++i) {
-            const int q = p + 4 * i;
-            const int rho = 8 * q + (lane >> 3);
-            const int c = (lane & 7) ^ fp8_swizzle(rho);
-            const bool act = 8 * q < CF::BM;
-            int row = act ? m0 + rho : n0 + rho - CF::BM;
-            const int last = act ? g.M - 1 : g.N - 1;
-            row = row < last ? row : last;
-            voff[i] = uint32_t(int64_t(row - (act ? m0 : n0)) * ld + 16 * c);
+    // This workgroup's tiles: dispatch b runs on XCD b % 8, each XCD takes a
+    // contiguous range of tiles, and its workgroups go through that range side
+    // by side.
+    const int ntiles = tiles_m * tiles_n;
+    const int x = blockIdx.x % 8, rem = ntiles % 8;
+    const int on_xcd = (int(gridDim.x) - x + 7) / 8;  // workgroups of this XCD
+    const int first = x * (ntiles / 8) + (x < rem ? x : rem), count = ntiles / 8 + (x < rem ? 1 : 0);
+    const int j0 = blockIdx.x / 8;
+    const int mine = j0 < count ? (count - j0 + on_xcd - 1) / on_xcd : 0;
+    // Tiles are ordered in groups of group_m tiles of tokens, m fastest, so that
+    // those in flight on an XCD share operand rows in its L2.
+    auto origin = [&](int i, int& m0, int& n0) {
+        const int t = first + j0 + i * on_xcd;
+        const int gsize = group_m * tiles_n;
+        const int gi = t / gsize, r = t - gi * gsize;
+        const int left = tiles_m - gi * group_m;
+        const int gm = left < group_m ? left : group_m;
+        m0 = (gi * group_m + r % gm) * CF::BM;
+        n0 = (r / gm) * CF::BN;
+    };
+
+    // The copy side, up to NS stages ahead of the products: copy i of a wave is
+    // rows 8 c .. 8 c + 7 of the stage (tokens first), c = cw + CW i; lane l
+    // fills the slot of row 8 c + l / 8, chunk (l % 8) ^ swizzle (the same for
+    // every c: the swizzle has period 16 rows, a wave's copies are 8 CW apart).
+    // Rows past M or N read as zeros (their results are not stored).
+    const uint32_t voff = uint32_t((lane >> 3) * g.K + 16 * ((lane & 7) ^ fp8_swizzle(8 * (cw & 1) + (lane >> 3))));
+    uint32_t sc_off = 0;
+    v4i ra{}, rw{};
+    const uint8_t* psc = nullptr;
+    const int64_t sc_step = cw == 0 ? 4 * int64_t(lda) : 4;  // bytes from one stage's scales to the next's
+    int copy_tile = 0, copy_s = 0;
+    uint32_t copy_dst = lds0;
+    auto chunk = [&](int i) {
+        const int c = cw + CF::CW * i;
+        return CF::EVEN || c < CF::COPIES ? c : c - CF::CW;  // (past the end: the wave's copy before, again)
+    };
+    auto aim = [&](int tile) {
+        int m0, n0;
+        origin(tile, m0, n0);
+        const int rows_a = g.M - m0 < CF::BM ? g.M - m0 : CF::BM, rows_w = g.N - n0 < CF::BN ? g.N - n0 : CF::BN;
+        ra = buffer_of(g.act + int64_t(m0) * g.K, uint32_t(rows_a) * uint32_t(g.K));
+        rw = buffer_of(g.w + int64_t(n0) * g.K, uint32_t(rows_w) * uint32_t(g.K));
+        if (cw == 0) {  // four tokens' scales per lane; the last whole four past the end
+            int m = m0 + 4 * (lane < CF::BM / 4 ? lane : 0);
+            m = m < lda - 4 ? m : lda - 4;
+            sc_off = uint32_t(4 * (m - m0));
+            psc = reinterpret_cast<const uint8_t*>(g.act_scale + m0);
+        } else if (cw == 1) {  // one row block's scale per lane
+            const int blk0 = n0 / 128, blk_last = (g.N - 1) / 128;
+            const int blk = blk0 + lane < blk_last ? blk0 + lane : blk_last;
+            sc_off = uint32_t(4 * (blk - blk0) * nk);
+            psc = reinterpret_cast<const uint8_t*>(g.wscale + int64_t(blk0) * nk);
         }
-        const uint8_t* const abase = g.act + int64_t(m0) * ld;
-        const uint8_t* const wbase = g.w + int64_t(n0) * ld;
-        const uint32_t lds0 = lds_address(lds);
-        auto load_stage = [&](int j) {
-            const int src = j < nk ? j : nk - 1;  // stages past K repeat the last one (never read)
-            const uint32_t dst = lds0 + uint32_t((j % CF::NS) * CF::STAGE);
-#pragma unroll
-            for (int i = 0; i < CF::NHI; ++i) {
-                const int q = p + 4 * i;
-                copy16_to_lds((8 * q < CF::BM ? abase : wbase) + int64_t(src) * 128, voff[i], dst + q * 1024);
-            }
-        };
-        for (int j = 0; j < CF::NS - 1; ++j) load_stage(j);
-        int issued = CF::NS - 1;
-        wait_vmcnt<(CF::NS - 3) * CF::NHI>();  // stages 0 and 1 landed
-        barrier_nofence();                      // B(-1)
-        for (int s = 0; s < nk; ++s) {
-            if (s + CF::NS - 1 < nk) {
-                load_stage(s + CF::NS - 1);
-                ++issued;
-            }
-            const int younger = issued - (s + 3);  // copies issued after stage s + 2
-            wait_stages_in_flight<CF::NHI>(younger > 0 ? younger : 0);
-            barrier_nofence();  // B(s)
+    };
+    auto copy_part = [&](int i) {
+        const int c = chunk(i);
+        const bool act = CF::EVEN ? i < CF::BM / 8 / CF::CW : 8 * c < CF::BM;
+        const uint32_t soff = uint32_t((8 * c - (act ? 0 : CF::BM)) * g.K + 128 * copy_s);
+        copy16_buffer(act ? ra : rw, voff, soff, copy_dst + c * 1024);
+    };
+    auto copy_scales = [&]() {
+        if (cw == 0)
+            copy16_base(psc, sc_off, copy_dst + CF::SA_OFF);
+        else if (cw == 1)
+            copy4_base(psc, sc_off, copy_dst + CF::SW_OFF);
+    };
+    // To the next stage.  Past the last one the copies go on with descriptors of
+    // no bytes and the last scales, into slots that nobody reads any more: every
+    // stage has the same copies, without a branch between its products (a branch
+    // around each copy cost 20 % of a stage's time even where no copy was made).
+    auto copy_advance = [&]() {
+        copy_dst = copy_dst + CF::STAGE == lds0 + CF::LDS ? lds0 : copy_dst + CF::STAGE;
+        if (copy_tile == mine) return;
+        if (++copy_s < nk) {
+            psc += sc_step;
+            return;
         }
+        copy_s = 0;
+        if (++copy_tile < mine) {
+            aim(copy_tile);
+        } else {
+            ra[2] = 0;
+            rw[2] = 0;
+        }
+    };
+    // Waits until all but the newest k stages of this wave's copies have landed
+    // (they return in order).
+    auto wait_but = [&](auto k_tag) {
+        constexpr int k = decltype(k_tag)::value;
+        if (cw < 0) return;
+        if (k == 0 || cw < 2)
+            wait_vmcnt<k * (NC + 1)>();
+        else if (cw < CF::CW)
+            wait_vmcnt<k * NC>();
+    };
+    if (mine == 0) return;
+    if (cw >= 0 && cw < CF::CW) aim(0);
+    auto copy_stage = [&]() {
+        if (cw < 0 || cw >= CF::CW) return;
+        copy_scales();
+#pragma unroll
+        for (int i = 0; i < NC; ++i) copy_part(i);
+        copy_advance();
+    };
+    for (int s = 0; s < NS - 1; ++s) copy_stage();
+    wait_but(std::integral_constant<int, CF::FLIGHT>{});
+    barrier_nofence();
+    if (CF::LW && cw >= 0) {
+        for (int i = mine * nk; i > 0; --i) {
+            copy_stage();
+            wait_but(std::integral_constant<int, CF::FLIGHT>{});
+            barrier_nofence();
+        }
+        wait_vmcnt<0>();  // no copy outlives its workgroup's LDS
         return;
     }
 
-    constexpr int TF = CF::TF, TW = CF::TW;
-    const int wm = wave & 1, wn = wave >> 1;
-    const int q = lane >> 4;
-    uint32_t oa[TF], ow[TW];
-#pragma unroll
-    for (int f = 0; f < TF; ++f) oa[f] = fp8_slot(wm * (CF::BM / 2) + 16 * f + (lane & 15), q);
-#pragma unroll
-    for (int n = 0; n < TW; ++n) ow[n] = fp8_slot(CF::BM + wn * (CF::BN / 2) + 16 * n + (lane & 15), q);
-    v4f acc[TW][TF];
-#pragma unroll
-    for (int n = 0; n < TW; ++n)
-#pragma unroll
-        for (int f = 0; f < TF; ++f) acc[n][f] = v4f{0.f, 0.f, 0.f, 0.f};
-    v8i fa[2][TF], fw[2][TW];
-    float sa[2][TF], sw[2];
-    const uint32_t lds0 = lds_address(lds);
-    // scales of stage s: this lane's tokens, and the wave's block of 128 rows
-    const int lda = fp8_scale_ld(g.M);
-    int mrow[TF];
-#pragma unroll
-    for (int f = 0; f < TF; ++f) {
-        const int m = m0 + wm * (CF::BM / 2) + 16 * f + (lane & 15);
-        mrow[f] = m < g.M ? m : g.M - 1;
-    }
-    const int nrow = n0 + wn * (CF::BN / 2);
-    const float* const swp = g.wscale + int64_t((nrow < g.N ? nrow : g.N - 1) / 128) * nk;
-    auto read_stage = [&](int s, int b) {
-        const uint32_t base = lds0 + uint32_t((s % CF::NS) * CF::STAGE);
-        const int sc = s < nk ? s : nk - 1;
-#pragma unroll
-        for (int f = 0; f < TF; ++f) sa[b][f] = g.act_scale[int64_t(sc) * lda + mrow[f]];
-        sw[b] = swp[sc];
-#pragma unroll
-        for (int f = 0; f < TF; ++f) fa[b][f] = fp8_read_frag(base + oa[f]);
-#pragma unroll
-        for (int n = 0; n < TW; ++n) fw[b][n] = fp8_read_frag(base + ow[n]);
-    };
-    auto iteration = [&](int s, auto b_tag) {
-        constexpr int B = decltype(b_tag)::value;
-        read_stage(s + 1, B ^ 1);  // (past K: a slot's stale bytes, never used)
-        float p[TF];
-#pragma unroll
-        for (int f = 0; f < TF; ++f) p[f] = sa[B][f] * sw[B];
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int n = 0; n < TW; ++n)
-#pragma unroll
-            for (int f = 0; f < TF; ++f) {
-                const v4f d = mfma_e4m3(fw[B][n], fa[B][f], v4f{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][f][i] = __builtin_fmaf(d[i], p[f], acc[n][f][i]);
-            }
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): stage s + 1 is in registers
-        barrier_nofence();                   // B(s)
-    };
-    barrier_nofence();  // B(-1): stages 0 and 1 published
-    read_stage(0, 0);
-    __builtin_amdgcn_s_waitcnt(0xC07F);
-    __builtin_amdgcn_sched_barrier(0);
-    int s = 0;
-    for (; s + 1 < nk; s += 2) {  // stages in pairs, so that the register set of each is fixed
-        iteration(s, std::integral_constant<int, 0>{});
-        iteration(s + 1, std::integral_constant<int, 1>{});
-    }
-    if (s < nk) iteration(s, std::integral_constant<int, 0>{});
+    const int wm = wave % CF::WM, wn = wave / CF::WM;
+    const int arow = wm * 16 * TF, wrow = wn * 16 * TW;
+    // fragment j of an operand is 2048 j bytes further (the swizzle has period 16)
+    const uint32_t oa = fp8_slot(arow + (lane & 15), q), ow = fp8_slot(CF::BM + wrow + (lane & 15), q);
+    uint32_t ra0 = lds0 + oa, ra1 = lds0 + (oa ^ 64u), rw0 = lds0 + ow, rw1 = lds0 + (ow ^ 64u);
+    const uint32_t osa = CF::SA_OFF + 4 * (arow + (lane & 15));
 
-    int mm[TF], nn[TW];
+    v4f acc[TW][TF];
+    v8i fa[2], fw[TW];
+    v4f d[2][TW];
+    float sa[TF], sw[NP], p[2][NP];
+    uint32_t osw[NP];  // each weight fragment's scale block, from the tile's first
+    auto add = [&](int f, int n) {
 #pragma unroll
-    for (int f = 0; f < TF; ++f) mm[f] = m0 + wm * (CF::BM / 2) + 16 * f + (lane & 15);
+        for (int i = 0; i < 4; ++i) acc[n][f][i] = __builtin_fmaf(d[f & 1][n][i], p[f & 1][NP == 1 ? 0 : n], acc[n][f][i]);
+        // (pinned here: left alone the compiler sinks the adds behind the stage's
+        // branches, with every product of the stage live until then)
+        asm volatile("" : "+v"(acc[n][f]));
+    };
+    auto products = [&](int f) {
 #pragma unroll
-    for (int n = 0; n < TW; ++n) nn[n] = n0 + wn * (CF::BN / 2) + 16 * n + 4 * q;
-    fp8_store_tiles<TW, TF>(acc, mm, nn, g);
+        for (int n = 0; n < NP; ++n) p[f & 1][n] = sa[f] * sw[n];
+    };
+    auto read_scales = [&](uint32_t base) {
+#pragma unroll
+        for (int f = 0; f < TF; ++f) sa[f] = lds_float(base + osa + 64 * f);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) sw[n] = lds_float(base + osw[n]);
+    };
+
+    uint32_t cur = lds0, nxt = lds0 + CF::STAGE;
+    // One stage; COPY: with the copies of the stage NS - 1 further, one by one
+    // behind the first products.
+    auto stage = [&](auto copy_tag) {
+        constexpr bool COPY = decltype(copy_tag)::value;
+        if constexpr (COPY) copy_scales();
+        // One product and the four adds of an earlier one in turn: the adds
+        // then fit between the products' issue slots (clustered by the
+        // scheduler, products and adds took 82 % of this order's rate).  The
+        // copies of stage s + NS - 1, whose slot the last barrier freed, go
+        // out one by one between the first products.
+#pragma unroll
+        for (int f = 0; f < TF - 1; ++f) {
+            fa[(f + 1) & 1] = fp8_read_frag(ra0 + 2048 * (f + 1), ra1 + 2048 * (f + 1));
+            products(f);
+#pragma unroll
+            for (int n = 0; n < TW; ++n) {
+                d[f & 1][n] = mfma_e4m3(fw[n], fa[f & 1], v4f{0.f, 0.f, 0.f, 0.f});
+                __builtin_amdgcn_sched_barrier(0);
+                add((f + TF - 1) % TF, n);
+                const int unit = f * TW + n;
+                if constexpr (COPY) {
+#pragma unroll
+                    for (int i = 0; i < NC; ++i)
+                        if (i * CF::SPREAD / NC == unit) copy_part(i);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                if (COPY && unit == CF::SPREAD - 1) copy_advance();
+            }
+        }
+        constexpr int L = TF - 1;
+        products(L);
+        if constexpr (!CF::EARLY) {
+            // this wave's reads of stage s (and copies of stage s + 1) are done
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            if constexpr (CF::LW == 0) wait_but(std::integral_constant<int, CF::FLIGHT>{});
+            barrier_nofence();
+        }
+        ra0 += nxt - cur;
+        ra1 += nxt - cur;
+        rw0 += nxt - cur;
+        rw1 += nxt - cur;
+        read_scales(nxt);
+        fa[0] = fp8_read_frag(ra0, ra1);  // (past the last stage: a slot's stale bytes, never used)
+#pragma unroll
+        for (int n = 0; n < TW; ++n) {
+            d[L & 1][n] = mfma_e4m3(fw[n], fa[L & 1], v4f{0.f, 0.f, 0.f, 0.f});
+            fw[n] = fp8_read_frag(rw0 + 2048 * n, rw1 + 2048 * n);
+            __builtin_amdgcn_sched_barrier(0);
+            add(L - 1, n);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (CF::EARLY) barrier_nofence();  // (the products above have waited for every read of stage s)
+        cur = nxt;
+        nxt = nxt + CF::STAGE == lds0 + CF::LDS ? lds0 : nxt + CF::STAGE;
+    };
+
+    auto run = [&](auto copy_tag) {
+    for (int tile = 0; tile < mine; ++tile) {
+        int m0, n0;
+        origin(tile, m0, n0);
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            osw[n] = CF::SW_OFF + 4 * (CF::ALIGNED ? wrow / 128 : (n0 + wrow + 16 * n) / 128 - n0 / 128);
+        if (CF::ALIGNED ? tile == 0 : true) read_scales(cur);
+        if (tile == 0) {
+            fa[0] = fp8_read_frag(ra0, ra1);
+#pragma unroll
+            for (int n = 0; n < TW; ++n) fw[n] = fp8_read_frag(rw0 + 2048 * n, rw1 + 2048 * n);
+        }
+#pragma unroll
+        for (int n = 0; n < TW; ++n) {
+#pragma unroll
+            for (int f = 0; f < TF; ++f) acc[n][f] = v4f{0.f, 0.f, 0.f, 0.f};
+            d[1][n] = v4f{0.f, 0.f, 0.f, 0.f};  // no pending sums
+        }
+#pragma unroll
+        for (int n = 0; n < NP; ++n) p[1][n] = 0.0f;
+
+        for (int s = 0; s < nk; ++s) stage(copy_tag);
+#pragma unroll
+        for (int n = 0; n < TW; ++n) add(TF - 1, n);
+        fp8_store_tile<TW, TF>(acc, m0 + arow, n0 + wrow, lane, g);
+    }
+    };
+    if (CF::LW == 0 && (CF::CW == CF::MW || wave < CF::CW))
+        run(std::true_type{});
+    else
+        run(std::false_type{});
+    wait_vmcnt<0>();  // no copy outlives its workgroup's LDS
 }
 
 template <class CF>
-hipError_t launch_cfg(const Fp8Args& g, hipStream_t st) {
+hipError_t launch_cfg(const Fp8Args& g, const DeviceInfo& dev, hipStream_t st) {
     const int tiles_m = (g.M + CF::BM - 1) / CF::BM;
     const int tiles_n = (g.N + CF::BN - 1) / CF::BN;
-    hipLaunchKernelGGL((fp8_gemm_kernel<CF>), dim3(tiles_m * tiles_n), dim3(kThreads), 0, st, g, tiles_m, tiles_n);
+    const int slots = dev.cus * CF::WGS, tiles = tiles_m * tiles_n;
+    hipLaunchKernelGGL((fp8_gemm_kernel<CF>), dim3(tiles < slots ? tiles : slots), dim3(CF::THREADS), 0, st, g, tiles_m,
+                       tiles_n, 8);
     return hipGetLastError();
+}
+
+struct Tile {
+    const char* name;
+    int bm, bn;
+    float stage_us;  // one stage of one tile alone on a CU
+    hipError_t (*launch)(const Fp8Args&, const DeviceInfo&, hipStream_t);
+};
+template <int BM, int BN, int WM, int WN, int LW, int NS>
+constexpr Tile tile(const char* name, float stage_us) {
+    return {name, BM, BN, stage_us, launch_cfg<Fp8Cfg<BM, BN, WM, WN, LW, 2, NS>>};
+}
+// The largest tile copies the fewest bytes per product and multiplies on eight
+// waves, half of which copy between their products: with two waves of 256
+// registers on a SIMD there is no room for waves that only copy.  The others
+// multiply on four waves and copy on four more (128 x 128 this way: 0.38 us a
+// stage, 0.61 with its multiplying waves copying).
+const Tile kTiles[] = {
+    tile<256, 256, 2, 4, 0, 2>("256x256", 1.15f), tile<256, 128, 2, 2, 4, 3>("256x128", 0.59f),
+    tile<128, 192, 2, 2, 4, 3>("128x192", 0.52f), tile<128, 160, 2, 2, 4, 4>("128x160", 0.46f),
+    tile<128, 128, 2, 2, 4, 4>("128x128", 0.37f), tile<128, 96, 2, 2, 4, 5>("128x96", 0.35f),
+    tile<128, 64, 2, 2, 4, 6>("128x64", 0.29f),   tile<64, 128, 2, 2, 4, 6>("64x128", 0.32f),
+    tile<64, 64, 2, 2, 4, 8>("64x64", 0.25f),
+};
+constexpr int kTileCount = int(sizeof kTiles / sizeof kTiles[0]);
+constexpr float kTileUs = 2.0f;  // a tile's epilogue and first loads
+
+// The tile with the least time by rounds of tiles over the CUs.  Measured (us,
+// the chosen one first): 1024 x 3584 x 4608: 128x160 22.7, 128x192 23.9, 256x128
+// 27.2, 128x128 30.3; 811 x 16384 x 2048: 128x64 45.7, 64x128 46.1, 128x96 50.7,
+// 256x256 165; 4096 x 3584 x 37888: 256x256 530, 256x128 538, 128x128 740.
+int pick_tile(const Fp8Args& g, int cus) {
+    int best = 0;
+    float least = 0.0f;
+    for (int i = 0; i < kTileCount; ++i) {
+        const Tile& t = kTiles[i];
+        const int64_t tiles = int64_t((g.M + t.bm - 1) / t.bm) * ((g.N + t.bn - 1) / t.bn);
+        const float us = float((tiles + cus - 1) / cus) * (float(g.K / 128) * t.stage_us + kTileUs);
+        if (i == 0 || us < least) best = i, least = us;
+    }
+    return best;
 }
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8Args& g, hipStream_t stream) { return launch_cfg<Fp8Cfg<128, 128>>(g, stream); }
+int fp8_tile_id(const char* name) {
+    for (int i = 0; i < kTileCount; ++i)
+        if (!std::strcmp(kTiles[i].name, name)) return i;
+    return -1;
+}
+
+hipError_t launch_fp8_gemm(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream) {
+    const int forced = hooks().fp8_tile.load(std::memory_order_relaxed);
+    return kTiles[forced >= 0 ? forced : pick_tile(g, dev.cus)].launch(g, dev, stream);
+}
 
 }  // namespace fq

@@ -35,9 +35,9 @@ __device__ __forceinline__ uint32_t fp8_slot(int rho, int q) {
 }
 typedef __attribute__((address_space(3))) const v4i lds_cv4i;
 // A lane's 32 codes of a fragment: chunks q and q + 4 of its row.
-__device__ __forceinline__ v8i fp8_read_frag(uint32_t addr) {
-    const v4i a = *reinterpret_cast<lds_cv4i*>(uintptr_t(addr));
-    const v4i b = *reinterpret_cast<lds_cv4i*>(uintptr_t(addr ^ 64u));
+__device__ __forceinline__ v8i fp8_read_frag(uint32_t lo, uint32_t hi) {
+    const v4i a = *reinterpret_cast<lds_cv4i*>(uintptr_t(lo));
+    const v4i b = *reinterpret_cast<lds_cv4i*>(uintptr_t(hi));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -90,6 +90,96 @@ __device__ __forceinline__ void fp8_store_tiles(const v4f (&acc)[TN][TM], const 
             *reinterpret_cast<uint2*>(fp8_out_ptr(g, m[j], n[i])) =
                 make_uint2(pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3]));
         }
+}
+
+// Epilogue of a wave's TW x TF fragments (weight rows n0 .. n0 + 16 TW - 1,
+// tokens m0 .. m0 + 16 TF - 1) from the registers.  A lane holds 4 consecutive
+// features of each fragment; exchanging the odd 16-lane rows of fragment n with
+// the even rows of fragment n + 1 leaves every lane 8 consecutive features of
+// one of the two (fragment n + q % 2, features 8 (q / 2) .. + 7, q = lane / 16),
+// so it stores 16 bytes and four lanes store 64 consecutive bytes of a row.
+// The addresses of a fragment pair are the row's plus a constant; the options
+// (bias, residual) are decided once, outside the loops.
+template <bool EXTRAS, int TW, int TF>
+__device__ __forceinline__ void fp8_store_pairs(const v4f (&acc)[TW][TF], int m0, int n0, int lane, const Fp8Args& g) {
+    const int q = lane >> 4;
+    const int c0 = n0 + 16 * (q & 1) + 8 * (q >> 1);  // column of pair 0
+    // y of (m, c0 + 32 pair): rows ld apart; a pair's column offset is 32 pair,
+    // or with heads that of its head
+    const int64_t row_step = g.head_dim > 0 ? g.head_dim : g.ldy;
+    uint16_t* yp[(TW + 1) / 2];
+#pragma unroll
+    for (int n = 0; n + 1 < TW; n += 2) {
+        const int col = c0 + 16 * n;
+        yp[n / 2] = fp8_out_ptr(g, m0 + (lane & 15), col);
+    }
+    float bs[EXTRAS ? (TW + 1) / 2 : 1][8];
+    if constexpr (EXTRAS) {
+#pragma unroll
+        for (int n = 0; n + 1 < TW; n += 2) {
+            const int col = c0 + 16 * n;
+            const bool on = g.bias && col < g.N;
+            const float4 a = on ? *reinterpret_cast<const float4*>(g.bias + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 b = on ? *reinterpret_cast<const float4*>(g.bias + col + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            bs[n / 2][0] = a.x, bs[n / 2][1] = a.y, bs[n / 2][2] = a.z, bs[n / 2][3] = a.w;
+            bs[n / 2][4] = b.x, bs[n / 2][5] = b.y, bs[n / 2][6] = b.z, bs[n / 2][7] = b.w;
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < TF; ++f) {
+        const int m = m0 + 16 * f + (lane & 15);
+        uint4 rs[EXTRAS ? (TW + 1) / 2 : 1];
+        if constexpr (EXTRAS) {
+#pragma unroll
+            for (int n = 0; n + 1 < TW; n += 2) {
+                const int col = c0 + 16 * n;
+                rs[n / 2] = (g.residual && m < g.M && col < g.N)
+                                ? *reinterpret_cast<const uint4*>(g.residual + int64_t(m) * g.ldr + col)
+                                : make_uint4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n + 1 < TW; n += 2) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[n][f][i]),
+                                                                __float_as_uint(acc[n + 1][f][i]), false, false);
+                v[i] = __uint_as_float(r[0]);
+                v[4 + i] = __uint_as_float(r[1]);
+            }
+            if constexpr (EXTRAS) {
+                if (g.bias) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += bs[n / 2][i];
+                }
+                if (g.residual) {
+                    const uint4 r = rs[n / 2];
+                    v[0] += bf16_lo(r.x), v[1] += bf16_hi(r.x), v[2] += bf16_lo(r.y), v[3] += bf16_hi(r.y);
+                    v[4] += bf16_lo(r.z), v[5] += bf16_hi(r.z), v[6] += bf16_lo(r.w), v[7] += bf16_hi(r.w);
+                }
+            }
+            if (m < g.M && c0 + 16 * n < g.N)
+                *reinterpret_cast<uint4*>(yp[n / 2] + 16 * f * row_step) =
+                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7]));
+        }
+    }
+    if constexpr (TW % 2 == 1) {  // the last fragment alone: 4 features per lane
+#pragma unroll
+        for (int f = 0; f < TF; ++f) {
+            const v4f one[1][1] = {{acc[TW - 1][f]}};
+            const int mm[1] = {m0 + 16 * f + (lane & 15)}, nn[1] = {n0 + 16 * (TW - 1) + 4 * q};
+            fp8_store_tiles<1, 1>(one, mm, nn, g);
+        }
+    }
+}
+template <int TW, int TF>
+__device__ __forceinline__ void fp8_store_tile(const v4f (&acc)[TW][TF], int m0, int n0, int lane, const Fp8Args& g) {
+    if (g.bias || g.residual)
+        fp8_store_pairs<true>(acc, m0, n0, lane, g);
+    else
+        fp8_store_pairs<false>(acc, m0, n0, lane, g);
 }
 
 }  // namespace fq

@@ -60,11 +60,14 @@ struct Hooks {
     std::atomic<int> gemm_tile{-1};  // -1: the cost model picks; else a tile id of fq_gemm.hip
     std::atomic<int> gemm_mfma{16};  // 16: v_mfma_i32_16x16x64_i8 where it applies; 32: 32x32x32 only
     std::atomic<int> gemv_split{0};  // 1: decode-sized M always takes the split-K GEMV
+    std::atomic<int> fp8_tile{-1};   // -1: the rule of fq_fp8_gemm.hip picks; else one of its tile ids
     std::atomic<int> decode1_off{0}; // 1: one-token fq_linear as two launches, never the fused kernel
 };
 Hooks& hooks();
 // Tile id of a tile name ("128x144", ...), or -1 (fq_gemm.hip).
 int gemm_tile_id(const char* name);
+// The same for the FP8 GEMM (fq_fp8_gemm.hip).
+int fp8_tile_id(const char* name);
 
 // What a device's launches need to know, gathered once per device and process
 // by prepare_device (fq_api.cpp): the compute-unit count, the LDS of a CU and,
@@ -157,7 +160,7 @@ struct Fp8Args {
     int64_t ldy;
     int32_t head_dim;  // 0: y is [M][ldy]; else y is [N/head_dim][M][head_dim]
 };
-hipError_t launch_fp8_gemm(const Fp8Args& g, hipStream_t stream);
+hipError_t launch_fp8_gemm(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
 hipError_t launch_fp8_gemv(const Fp8Args& g, hipStream_t stream);
 
 // Rotary positions (fq_rope.hip).
