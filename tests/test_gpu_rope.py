@@ -10,6 +10,24 @@ from fqtest import bf16_to_f64, dev, host
 pytestmark = pytest.mark.gpu
 
 
+def test_a_host_call_before_torch_leaves_the_device_usable():
+    """A fresh process whose first call is the host plan (torch not imported yet), then a rotation."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import numpy as np, w4a4_integer_gemm_amd as fq\n"
+            "f, s = fq.fq_rope_freqs(64)\n"
+            "import torch\n"
+            "x = torch.ones(2, 64, dtype=torch.bfloat16, device='cuda')\n"
+            "y = torch.zeros_like(x)\n"
+            "fq.fq_rope(x, 64, 64, 2, 1, 1, 64, 64, 0, torch.from_numpy(f.view('int64')).cuda(), s, None, 0, 0, y, 64, 64)\n"
+            "assert torch.equal(y[0], x[0]) and not torch.equal(y[1], x[1])\n"
+            "print('rotated')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "rotated" in r.stdout, r.stderr[-2000:]
+
+
 def run(M, heads, rot_heads, D, rot, inter=0, inverse=0, layout="heads", kind=fq.ROPE_PLAIN, pos="random", pos0=0, seed=0,
         in_place=False, pad=0, **kw):
     rng = np.random.default_rng(seed)

@@ -87,6 +87,13 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"libfq.so not found at {LIB_PATH}; build it with "
                                "`python w4a4_integer_gemm_amd/build.py` (hipcc, gfx950)")
+        # torch first: it brings its own HIP runtime, and a host call of this
+        # library before `import torch` (a packer, a rotary plan) would load the
+        # system's, which then sees no device
+        try:
+            import torch  # noqa: F401
+        except ImportError:
+            pass  # the host entry points need no torch
         L = ctypes.CDLL(LIB_PATH)
         for name, (args, res) in SIGNATURES.items():
             fn = getattr(L, name)

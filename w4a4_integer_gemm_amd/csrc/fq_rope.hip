@@ -13,9 +13,12 @@
 // series on an eighth of a turn around the nearest quarter (remainders below
 // 2^-28), in float32.
 //
-// Bound by reading and writing the heads once.  A thread owns one 16-byte piece
-// of `a` and one of `b` (interleaved: two pieces) of one token, computes its 8
-// angles once and applies them to its share of the heads.
+// Bound by reading and writing the heads once.  A thread owns one item of one
+// token: with halves the 16-byte piece of 8 `a` elements and the piece of their
+// 8 `b` elements, interleaved one piece of 4 pairs, past rot_dim one copied piece.
+// It computes the item's angles once and applies them to its share of the heads,
+// UN heads' loads ahead of their stores.  (rot_dim not a multiple of 16, or of 8
+// interleaved, has pieces that are neither: those sizes take a thread per pair.)
 #include <hip/hip_runtime.h>
 
 #include "fq_device.h"
@@ -53,6 +56,86 @@ __device__ __forceinline__ uint32_t angle(uint64_t f, int32_t pos) {
 __device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
 __device__ __forceinline__ uint16_t to_bf16(float v) { return uint16_t(pack_bf16x2(v, 0.0f)); }
 
+__device__ __forceinline__ void angles(const RopeArgs& a, int32_t pos, int i0, int n, float* c, float* s) {
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+        cos_sin_turns(angle(a.freq[i0 + j], pos), &c[j], &s[j]);
+        c[j] *= a.attn_scale;
+        s[j] *= a.inverse ? -a.attn_scale : a.attn_scale;
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+}
+
+// Rotates the pieces u, v (halves) or u alone (interleaved).
+template <bool INTER>
+__device__ __forceinline__ void rotate(uint4& u, uint4& v, const float (&c)[8], const float (&s)[8]) {
+    float p[8], q[8];
+    unpack8(u, p);
+    if constexpr (INTER) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            q[2 * j] = __builtin_fmaf(p[2 * j], c[j], -(p[2 * j + 1] * s[j]));
+            q[2 * j + 1] = __builtin_fmaf(p[2 * j + 1], c[j], p[2 * j] * s[j]);
+        }
+        u = pack8(q);
+    } else {
+        float r[8];
+        unpack8(v, q);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r[j] = __builtin_fmaf(p[j], c[j], -(q[j] * s[j]));
+            q[j] = __builtin_fmaf(q[j], c[j], p[j] * s[j]);
+        }
+        u = pack8(r);
+        v = pack8(q);
+    }
+}
+
+// blockIdx.y: heads [y * share, (y + 1) * share); UN of them at a time.
+template <bool INTER, int UN>
+__global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, uint32_t items, int share) {
+    const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t m = idx / items, item = idx - m * items;
+    if (m >= uint32_t(a.M)) return;
+    const uint32_t rot_items = uint32_t(a.rot_dim) / (INTER ? 8u : 16u);
+    const bool rot = item < rot_items;
+    // element of u, and the distance from u to v
+    const int e = 8 * int(rot || INTER ? item : item + rot_items);
+    const int dv = !INTER && rot ? a.rot_dim / 2 : 0;
+    float c[8], s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = 1.0f, s[j] = 0.0f;
+    if (rot) {
+        const int32_t pos = a.positions ? a.positions[m] : a.pos0 + int32_t(m);
+        angles(a, pos, INTER ? 4 * int(item) : 8 * int(item), INTER ? 4 : 8, c, s);
+    }
+    const int h0 = blockIdx.y * share, h1 = h0 + share < a.heads ? h0 + share : a.heads;
+    const uint16_t* const xp = a.x + m * a.x_token + e;
+    uint16_t* const yp = a.y + m * a.y_token + e;
+    const bool in_place = a.x == a.y;
+    for (int h = h0; h < h1; h += UN) {
+        uint4 u[UN], v[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            const int hk = h + k < h1 ? h + k : h1 - 1;  // (past the share: loaded again, not stored)
+            u[k] = *reinterpret_cast<const uint4*>(xp + hk * a.x_head);
+            if (!INTER) v[k] = *reinterpret_cast<const uint4*>(xp + hk * a.x_head + dv);
+        }
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            const bool turn = rot && h + k < a.rot_heads;
+            if (h + k >= h1 || (in_place && !turn)) continue;
+            if (turn) rotate<INTER>(u[k], v[k], c, s);
+            *reinterpret_cast<uint4*>(yp + (h + k) * a.y_head) = u[k];
+            if (!INTER && rot) *reinterpret_cast<uint4*>(yp + (h + k) * a.y_head + dv) = v[k];
+        }
+    }
+}
+
 // One element pair (or copied pair of elements) per thread: any even rot_dim.
 __global__ __launch_bounds__(256) void rope_pairs_kernel(RopeArgs a) {
     const int half = a.head_dim / 2, rh = a.rot_dim / 2;
@@ -86,7 +169,30 @@ __global__ __launch_bounds__(256) void rope_pairs_kernel(RopeArgs a) {
 
 }  // namespace
 
+// Heads per thread: all of them where the tokens alone fill the chip (the angles
+// are then computed once), fewer below kFill threads, one for a few tokens.
+constexpr int64_t kFill = 256 * 1024;
+
+template <bool INTER>
+hipError_t launch_items(const RopeArgs& a, hipStream_t st) {
+    const uint32_t items = INTER ? a.head_dim / 8 : a.rot_dim / 16 + (a.head_dim - a.rot_dim) / 8;
+    const int64_t threads = int64_t(a.M) * items;
+    int64_t parts = kFill / threads;
+    parts = parts < 1 ? 1 : parts > a.heads ? a.heads : parts;
+    const int share = int((a.heads + parts - 1) / parts);
+    const dim3 grid(uint32_t((threads + 255) / 256), uint32_t((a.heads + share - 1) / share));
+    if (share == 1)
+        hipLaunchKernelGGL((rope_kernel<INTER, 1>), grid, dim3(256), 0, st, a, items, share);
+    else if (share <= 3)
+        hipLaunchKernelGGL((rope_kernel<INTER, 2>), grid, dim3(256), 0, st, a, items, share);
+    else
+        hipLaunchKernelGGL((rope_kernel<INTER, 4>), grid, dim3(256), 0, st, a, items, share);
+    return hipGetLastError();
+}
+
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
+    if (a.interleaved && a.rot_dim % 8 == 0) return launch_items<true>(a, stream);
+    if (!a.interleaved && a.rot_dim % 16 == 0) return launch_items<false>(a, stream);
     const int64_t threads = int64_t(a.M) * (a.head_dim / 2);
     hipLaunchKernelGGL(rope_pairs_kernel, dim3(uint32_t((threads + 255) / 256), a.heads), dim3(256), 0, stream, a);
     return hipGetLastError();
