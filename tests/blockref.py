@@ -168,7 +168,8 @@ def rope_theta(rot, base=10000.0, kind=0, factor=1.0, trained=1, low=1.0, high=3
 def rope(x, pos, turns, scale, rot_heads, rot, interleaved, inverse):
     """x float64 [heads][M][D]; turns: fraction of a turn per position of each pair
     (exact integers / 2^64).  Returns (y, |a| + |b| of each rotated element)."""
-    frac = np.array([[(int(t) * int(p)) % 2 ** 64 / 2.0 ** 64 for t in turns] for p in pos])
+    # the fraction of a turn in integers modulo 2^64 (wrapping products), then one rounding
+    frac = (np.asarray(turns, np.uint64)[None] * np.asarray(pos).astype(np.int64).astype(np.uint64)[:, None]) / 2.0 ** 64
     c, s = np.cos(2 * np.pi * frac) * scale, np.sin(2 * np.pi * frac) * scale * (-1 if inverse else 1)
     y, mag = x.copy(), np.zeros_like(x)
     i = np.arange(rot // 2)

@@ -74,13 +74,14 @@ def test_every_option(post, gate, mod, f32, out):
 
 
 @pytest.mark.parametrize("M,K", [(1, 8), (1, 24), (2, 504), (1, 512), (3, 520), (1, 2048), (7, 3584), (2, 8192), (3, 8200),
-                                 (2, 16384), (2, 16392), (1, 32768), (1, 32776), (1, 65536), (300, 136)])
+                                 (2, 16384), (2, 16392), (1, 32768), (1, 32776), (1, 65536), (300, 136), (257, 2056), (256, 520),
+                                 (258, 8200)])
 @pytest.mark.parametrize("f32", [False, True])
 def test_sizes(M, K, f32):
     run(M, K, M + K, f32=f32)
 
 
-@pytest.mark.parametrize("M,K", [(1, 128), (5, 1152), (2, 8320), (1, 18944), (1, 33024), (131, 256)])
+@pytest.mark.parametrize("M,K", [(1, 128), (5, 1152), (2, 8320), (1, 18944), (1, 33024), (131, 256), (300, 1152), (257, 8320)])
 @pytest.mark.parametrize("f32", [False, True])
 def test_code_sizes(M, K, f32):
     run(M, K, M + K, f32=f32, out="both")

@@ -82,6 +82,18 @@ def test_tokens_and_layouts(M, heads, rot_heads, inter, layout):
 
 
 @pytest.mark.parametrize("inter", [0, 1])
+@pytest.mark.parametrize("inverse", [0, 1])
+@pytest.mark.parametrize("M,heads,rot_heads,D,rot", [(700, 9, 7, 64, 64), (260, 33, 30, 128, 32), (900, 5, 5, 80, 48),
+                                                     (150, 13, 11, 256, 16), (2000, 2, 1, 72, 72), (3001, 3, 3, 40, 16)])
+@pytest.mark.parametrize("layout", ["heads", "rows", "in place"])
+def test_many_tokens(M, heads, rot_heads, D, rot, inter, inverse, layout):
+    """Above the size where a thread takes whole pieces of several heads."""
+    assert M * heads * D // 2 > 128 * 1024
+    run(M, heads, rot_heads, D, rot, inter, inverse, layout="rows" if layout == "in place" else layout, pad=16,
+        in_place=layout == "in place", seed=M)
+
+
+@pytest.mark.parametrize("inter", [0, 1])
 @pytest.mark.parametrize("D,rot", [(64, 64), (80, 20)])
 def test_in_place(D, rot, inter):
     run(9, 4, 3, D, rot, inter, in_place=True, layout="rows", pad=8)

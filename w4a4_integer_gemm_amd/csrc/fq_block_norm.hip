@@ -53,10 +53,9 @@ __device__ __forceinline__ float inv_rms(double ss, int K, double rk, float eps)
     return 1.0f / sqrtf(ms + eps);
 }
 
-__device__ __forceinline__ void load_gain(const float* __restrict__ g, int k, float (&o)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(g + k), b = *reinterpret_cast<const float4*>(g + k + 4);
-    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
-    o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+__device__ __forceinline__ void unpack4(const float4 (&v)[2], float (&o)[8]) {
+    o[0] = v[0].x, o[1] = v[0].y, o[2] = v[0].z, o[3] = v[0].w;
+    o[4] = v[1].x, o[5] = v[1].y, o[6] = v[1].z, o[7] = v[1].w;
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
@@ -64,8 +63,19 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                       pack_bf16x2(v[6], v[7]));
 }
 
-// P pieces of 8 values per lane; F32: the stream is float32; CODES: e4m3 codes go out.
-template <int P, bool F32, bool CODES>
+// A row's vectors that a lane needs, by piece: gains float32, conditions bf16.
+template <int P>
+struct Vectors {
+    float4 post[P][2], pre[P][2];
+    uint4 gate[P], scale[P], shift[P];
+};
+
+// P pieces of 8 values per lane; F32: the stream is float32; CODES: e4m3 codes
+// go out.  kAhead: every vector is requested with the row, before the first
+// reduction, so that one memory latency covers them all; otherwise each is
+// requested where it is used, which takes 38 registers less and lets a CU hold
+// more rows.
+template <int P, bool F32, bool CODES, bool kAhead>
 __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormArgs a, double rk) {
     __shared__ double red[2][kMaxWaves];
     const int m = blockIdx.x;
@@ -73,130 +83,172 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormArgs a, dou
     const int pieces = a.K / 8;
     const int64_t cond = m / a.rows_per_cond;
 
-    float r[P][8];
+    int kk[P];  // first value of each piece (lanes past the row: the row's first piece, left out below)
     bool on[P];
 #pragma unroll
-    for (int j = 0; j < P; ++j) on[j] = t + T * j < pieces;
+    for (int j = 0; j < P; ++j) {
+        on[j] = t + T * j < pieces;
+        kk[j] = on[j] ? 8 * (t + T * j) : 0;
+    }
 
-    // the stream
+    uint4 xr[P];
+    float4 rr[P][2];
+    Vectors<P> w;
+    auto load4 = [](const float* p, int k, float4 (&o)[2]) {
+        o[0] = *reinterpret_cast<const float4*>(p + k);
+        o[1] = *reinterpret_cast<const float4*>(p + k + 4);
+    };
+    auto load8 = [](const uint16_t* p, int k) { return *reinterpret_cast<const uint4*>(p + k); };
+    if (a.x) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) xr[j] = load8(a.x + int64_t(m) * a.ldx, kk[j]);
+    }
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-        const int k = 8 * (t + T * j);
+        if constexpr (F32) {
+            load4(static_cast<const float*>(a.r_in) + int64_t(m) * a.ld_rin, kk[j], rr[j]);
+        } else {
+            const uint4 u = load8(static_cast<const uint16_t*>(a.r_in) + int64_t(m) * a.ld_rin, kk[j]);
+            rr[j][0] = *reinterpret_cast<const float4*>(&u);  // (bits; unpacked below)
+        }
+    }
+    auto load_post = [&](int j) { load4(a.post_gamma, kk[j], w.post[j]); };
+    auto load_gate = [&](int j) { w.gate[j] = load8(a.gate + cond * a.ld_gate, kk[j]); };
+    auto load_pre = [&](int j) { load4(a.pre_gamma, kk[j], w.pre[j]); };
+    auto load_scale = [&](int j) { w.scale[j] = load8(a.mod_scale + cond * a.ld_mod, kk[j]); };
+    auto load_shift = [&](int j) { w.shift[j] = load8(a.mod_shift + cond * a.ld_mod, kk[j]); };
+    if constexpr (kAhead) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[j][i] = 0.0f;
-        if (on[j]) {
-            if constexpr (F32)
-                load_gain(static_cast<const float*>(a.r_in) + int64_t(m) * a.ld_rin, k, r[j]);
-            else
-                unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.r_in) + int64_t(m) * a.ld_rin + k),
-                        r[j]);
+        for (int j = 0; j < P; ++j) {
+            if (a.post_gamma) load_post(j);
+            if (a.gate) load_gate(j);
+            if (a.pre_gamma) load_pre(j);
+            if (a.mod_scale) load_scale(j);
+            if (a.mod_shift) load_shift(j);
+        }
+    }
+
+    float r[P][8];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        if constexpr (F32) {
+            unpack4(rr[j], r[j]);
+        } else {
+            unpack8(*reinterpret_cast<const uint4*>(&rr[j][0]), r[j]);
         }
     }
 
     if (a.x) {
-        float p[P][8];
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[j][i] = 0.0f;
-            if (on[j]) unpack8(*reinterpret_cast<const uint4*>(a.x + int64_t(m) * a.ldx + 8 * (t + T * j)), p[j]);
-        }
+        float rinv = 0.0f;
         if (a.post_gamma) {
             double ss = 0.0;
 #pragma unroll
-            for (int j = 0; j < P; ++j) ss += lane_sumsq<8>(p[j]);
-            const float rinv = inv_rms(block_sum(ss, nwaves, red[0]), a.K, rk, a.post_eps);
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-                if (on[j]) {
-                    float g[8];
-                    load_gain(a.post_gamma, 8 * (t + T * j), g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) p[j][i] = (p[j][i] * rinv) * g[i];
-                }
-        }
-        if (a.gate) {
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-                if (on[j]) {
-                    float g[8];
-                    unpack8(*reinterpret_cast<const uint4*>(a.gate + cond * a.ld_gate + 8 * (t + T * j)), g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) p[j][i] = p[j][i] * g[i];
-                }
+            for (int j = 0; j < P; ++j) {
+                float p[8];
+                unpack8(xr[j], p);
+                ss += on[j] ? lane_sumsq<8>(p) : 0.0;
+            }
+            rinv = inv_rms(block_sum(ss, nwaves, red[0]), a.K, rk, a.post_eps);
         }
 #pragma unroll
         for (int j = 0; j < P; ++j) {
+            float p[8], g[8];
+            unpack8(xr[j], p);
+            if (a.post_gamma) {
+                if constexpr (!kAhead) load_post(j);
+                unpack4(w.post[j], g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[j][i] = r[j][i] + a.res_scale * p[j][i];
-            const int k = 8 * (t + T * j);
+                for (int i = 0; i < 8; ++i) p[i] = (p[i] * rinv) * g[i];
+            }
+            if (a.gate) {
+                if constexpr (!kAhead) load_gate(j);
+                unpack8(w.gate[j], g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = p[i] * g[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[j][i] = r[j][i] + a.res_scale * p[i];
             if constexpr (F32) {
-                if (on[j] && a.r_out) {
-                    float* o = static_cast<float*>(a.r_out) + int64_t(m) * a.ld_rout + k;
+                if (on[j]) {
+                    float* o = static_cast<float*>(a.r_out) + int64_t(m) * a.ld_rout + kk[j];
                     *reinterpret_cast<float4*>(o) = make_float4(r[j][0], r[j][1], r[j][2], r[j][3]);
                     *reinterpret_cast<float4*>(o + 4) = make_float4(r[j][4], r[j][5], r[j][6], r[j][7]);
                 }
             } else {
-                const uint4 w = pack8(r[j]);
-                if (on[j] && a.r_out)
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.r_out) + int64_t(m) * a.ld_rout + k) = w;
-                unpack8(w, r[j]);  // the norm reads the stream as it is stored
+                const uint4 u = pack8(r[j]);
+                if (on[j]) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.r_out) + int64_t(m) * a.ld_rout + kk[j]) = u;
+                unpack8(u, r[j]);  // the norm reads the stream as it is stored
             }
         }
     }
 
     if (!a.h && !CODES) return;
+    float rinv = 0.0f;
     if (a.pre_norm) {
         double ss = 0.0;
 #pragma unroll
-        for (int j = 0; j < P; ++j) ss += lane_sumsq<8>(r[j]);
-        const float rinv = inv_rms(block_sum(ss, nwaves, red[1]), a.K, rk, a.pre_eps);
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[j][i] = r[j][i] * rinv;
-            if (on[j] && a.pre_gamma) {
-                float g[8];
-                load_gain(a.pre_gamma, 8 * (t + T * j), g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) r[j][i] = r[j][i] * g[i];
-            }
-        }
+        for (int j = 0; j < P; ++j) ss += on[j] ? lane_sumsq<8>(r[j]) : 0.0;
+        rinv = inv_rms(block_sum(ss, nwaves, red[1]), a.K, rk, a.pre_eps);
     }
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-        const int k = 8 * (t + T * j);
-        if (on[j] && a.mod_scale) {
-            float s[8];
-            unpack8(*reinterpret_cast<const uint4*>(a.mod_scale + cond * a.ld_mod + k), s);
+        float (&h)[8] = r[j];
+        float g[8];
+        if (a.pre_norm) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[j][i] = r[j][i] * (1.0f + s[i]);
-        }
-        if (on[j] && a.mod_shift) {
-            float s[8];
-            unpack8(*reinterpret_cast<const uint4*>(a.mod_shift + cond * a.ld_mod + k), s);
+            for (int i = 0; i < 8; ++i) h[i] = h[i] * rinv;
+            if (a.pre_gamma) {
+                if constexpr (!kAhead) load_pre(j);
+                unpack4(w.pre[j], g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[j][i] = r[j][i] + s[i];
+                for (int i = 0; i < 8; ++i) h[i] = h[i] * g[i];
+            }
         }
-        if (on[j] && a.h) *reinterpret_cast<uint4*>(a.h + int64_t(m) * a.ld_h + k) = pack8(r[j]);
+        if (a.mod_scale) {
+            if constexpr (!kAhead) load_scale(j);
+            unpack8(w.scale[j], g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = h[i] * (1.0f + g[i]);
+        }
+        if (a.mod_shift) {
+            if constexpr (!kAhead) load_shift(j);
+            unpack8(w.shift[j], g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = h[i] + g[i];
+        }
+        if (a.h && on[j]) *reinterpret_cast<uint4*>(a.h + int64_t(m) * a.ld_h + kk[j]) = pack8(h);
         if constexpr (CODES) {
             // (K is a multiple of 128: the 16 lanes of a group are all on or all off)
-            const float s = fp8_scale(max16_nonneg(lane_absmax<8>(r[j])));
-            const uint2 q = fp8_codes8(r[j], s);
+            const float s = fp8_scale(max16_nonneg(lane_absmax<8>(h)));
+            const uint2 q = fp8_codes8(h, s);
             if (on[j]) {
-                *reinterpret_cast<uint2*>(a.codes + int64_t(m) * a.K + k) = q;
-                if ((t & 15) == 0) a.act_scale[int64_t(k / 128) * fp8_scale_ld(a.M) + m] = s;
+                *reinterpret_cast<uint2*>(a.codes + int64_t(m) * a.K + kk[j]) = q;
+                if ((t & 15) == 0) a.act_scale[int64_t(kk[j] / 128) * fp8_scale_ld(a.M) + m] = s;
             }
         }
     }
 }
 
+// Rows that are at most one per CU request their vectors ahead (one row of 2048,
+// gated and modulated: 3.23 us against 3.56, graph-replayed); more rows do not
+// (1024 x 3584 to codes: 9.4 us against 10.1).
+constexpr int kAheadRows = 256;
+
 template <int P, bool F32>
 hipError_t launch_p(const NormArgs& a, int T, hipStream_t st) {
-    if (a.codes)
-        hipLaunchKernelGGL((block_norm_kernel<P, F32, true>), dim3(a.M), dim3(T), 0, st, a, 1.0 / double(a.K));
-    else
-        hipLaunchKernelGGL((block_norm_kernel<P, F32, false>), dim3(a.M), dim3(T), 0, st, a, 1.0 / double(a.K));
+    constexpr bool kMayAhead = P <= 2;  // (wider rows have no registers for it)
+    const double rk = 1.0 / double(a.K);
+    if (kMayAhead && a.M <= kAheadRows) {
+        if (a.codes)
+            hipLaunchKernelGGL((block_norm_kernel<P, F32, true, kMayAhead>), dim3(a.M), dim3(T), 0, st, a, rk);
+        else
+            hipLaunchKernelGGL((block_norm_kernel<P, F32, false, kMayAhead>), dim3(a.M), dim3(T), 0, st, a, rk);
+    } else {
+        if (a.codes)
+            hipLaunchKernelGGL((block_norm_kernel<P, F32, true, false>), dim3(a.M), dim3(T), 0, st, a, rk);
+        else
+            hipLaunchKernelGGL((block_norm_kernel<P, F32, false, false>), dim3(a.M), dim3(T), 0, st, a, rk);
+    }
     return hipGetLastError();
 }
 

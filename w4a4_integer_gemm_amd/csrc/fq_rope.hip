@@ -18,7 +18,8 @@
 // 8 `b` elements, interleaved one piece of 4 pairs, past rot_dim one copied piece.
 // It computes the item's angles once and applies them to its share of the heads,
 // UN heads' loads ahead of their stores.  (rot_dim not a multiple of 16, or of 8
-// interleaved, has pieces that are neither: those sizes take a thread per pair.)
+// interleaved, has pieces that are neither: those sizes, and small calls, take
+// a thread per pair of every head.)
 #include <hip/hip_runtime.h>
 
 #include "fq_device.h"
@@ -169,6 +170,10 @@ __global__ __launch_bounds__(256) void rope_pairs_kernel(RopeArgs a) {
 
 }  // namespace
 
+// Few pairs take a thread each, whose chain is one angle instead of eight
+// (graph-replayed, us, pairs against items: 1 x 12 x 256 1.93 / 2.55, 56 x 36 x
+// 128 2.2 / 2.65, 512 x 36 x 128 4.98 / 3.78).
+constexpr int64_t kFewPairs = 128 * 1024;
 // Heads per thread: all of them where the tokens alone fill the chip (the angles
 // are then computed once), fewer below kFill threads, one for a few tokens.
 constexpr int64_t kFill = 256 * 1024;
@@ -191,8 +196,9 @@ hipError_t launch_items(const RopeArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
-    if (a.interleaved && a.rot_dim % 8 == 0) return launch_items<true>(a, stream);
-    if (!a.interleaved && a.rot_dim % 16 == 0) return launch_items<false>(a, stream);
+    const bool few = int64_t(a.M) * a.heads * (a.head_dim / 2) <= kFewPairs;
+    if (!few && a.interleaved && a.rot_dim % 8 == 0) return launch_items<true>(a, stream);
+    if (!few && !a.interleaved && a.rot_dim % 16 == 0) return launch_items<false>(a, stream);
     const int64_t threads = int64_t(a.M) * (a.head_dim / 2);
     hipLaunchKernelGGL(rope_pairs_kernel, dim3(uint32_t((threads + 255) / 256), a.heads), dim3(256), 0, stream, a);
     return hipGetLastError();
