@@ -20,7 +20,7 @@ def rand_site(rng, M, N, K, spread=True):
 
 
 def dev_scales(sa):
-    """[K / 128][M] scales in the kernel's stride, the pad filled with NaN (never read)."""
+    """[K / 128][M] scales in the kernel's stride, the pad filled with NaN (never used)."""
     g, M = sa.shape
     full = np.full((g, -(-M // 4) * 4), np.nan, np.float32)
     full[:, :M] = sa
@@ -258,3 +258,40 @@ def test_full_size_layers_sampled():
         cols = (128 * b[:, None] + np.arange(128)).ravel()
         y, tol = ref.fp8_gemm(qa[rows], sa[:, rows], qw[cols], sw[b])
         ref.assert_gemm(got[np.ix_(rows, cols)], y, tol, f"{M}x{K}x{N}")
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 16400, 256), (16, 12296, 1152), (32, 20008, 384), (1, 33000, 128)])
+def test_few_tokens_and_wide_layers(M, N, K):
+    """Up to 32 tokens where row groups outnumber CUs: both sides of the choice between the two products."""
+    rng = np.random.default_rng(M + N + K)
+    qa, sa, qw, sw = rand_site(rng, M, N, K)
+    y, tol = ref.fp8_gemm(qa, sa, qw, sw)
+    ref.assert_gemm(run_gemm(qa, sa, qw, sw), y, tol, f"gemm {M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("K,N", [(128, 16), (640, 4104), (1024, 4104), (1280, 4104), (3584, 4112), (4096, 40), (5120, 72),
+                                 (8192, 4104), (8320, 40), (16512, 24), (32768, 16), (33024, 8)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_one_token_linear(K, N, norm):
+    """One token: the codes and scales are the prologue's bit for bit, the outputs those codes' products."""
+    rng = np.random.default_rng(K + N + norm)
+    gamma = rng.uniform(0.5, 1.5, K).astype(np.float32) if norm else None
+    site = fq.Fp8Site((rng.standard_normal((N, K)) * 0.02).astype(np.float32), gamma=gamma,
+                      bias=rng.standard_normal(N).astype(np.float32))
+    x, residual = dev(ref.bf16(rng, 1, K)), ref.bf16(rng, 1, N)
+    y = host(site.linear(x, residual=dev(residual)), np.uint16)
+    codes, scales = (host(t) for t in site.workspace_codes(1))
+    want_codes, want_scales = (host(t) for t in site.prologue(x))
+    assert np.array_equal(codes, want_codes) and np.array_equal(scales, want_scales[:, :1])
+    want, tol = ref.fp8_gemm(codes, scales, host(site.codes), host(site.wscale), host(site.bias), residual)
+    ref.assert_gemm(y, want, tol, f"K={K} N={N} norm={norm}")
+
+
+@pytest.mark.parametrize("tile", ["256x256", "64x64"])
+def test_tiles_take_single_tokens_too(tile, hook):
+    hook("fp8_tile=" + tile)
+    rng = np.random.default_rng(17)
+    for M, N, K in ((1, 264, 384), (5, 8, 128), (32, 72, 640)):
+        qa, sa, qw, sw = rand_site(rng, M, N, K)
+        y, tol = ref.fp8_gemm(qa, sa, qw, sw)
+        ref.assert_gemm(run_gemm(qa, sa, qw, sw), y, tol, f"{tile} {M}x{N}x{K}")

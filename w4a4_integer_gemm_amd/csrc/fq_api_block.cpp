@@ -117,7 +117,8 @@ fq::NormArgs prologue_args(const void* x, int32_t M, int32_t K, int64_t ldx, con
 }
 
 fq_status run_fp8_gemm(const char* fn, const fq::Fp8Args& g, const fq::DeviceInfo& dev, hipStream_t stream) {
-    return device_status(fn, g.M <= fq::kGemvMaxM ? fq::launch_fp8_gemv(g, stream) : fq::launch_fp8_gemm(g, dev, stream));
+    return device_status(fn, fq::fp8_gemv_takes(g, dev) ? fq::launch_fp8_gemv(g, dev, stream)
+                                                        : fq::launch_fp8_gemm(g, dev, stream));
 }
 
 }  // namespace
@@ -183,7 +184,9 @@ fq_status fq_fp8_linear(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, c
     const hipStream_t s = static_cast<hipStream_t>(stream);
     fq::Fp8Args g{codes, scales, M, static_cast<const uint8_t*>(w_codes), wscale, N, K, bias,
                   static_cast<const uint16_t*>(residual_bf16), ldr, static_cast<uint16_t*>(y_bf16), ldy, head_dim};
-    FQ_TRY(device_status(fn, fq::launch_block_norm(prologue_args(x_bf16, M, K, ldx, gamma, eps, codes, scales), s)));
+    const fq::NormArgs a = prologue_args(x_bf16, M, K, ldx, gamma, eps, codes, scales);
+    if (fq::fp8_decode1_takes(a, g)) return device_status(fn, fq::launch_fp8_decode1(a, g, *dev, s));
+    FQ_TRY(device_status(fn, fq::launch_block_norm(a, s)));
     return run_fp8_gemm(fn, g, *dev, s);
 }
 

@@ -334,32 +334,32 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
     };
 
     auto run = [&](auto copy_tag) {
-    for (int tile = 0; tile < mine; ++tile) {
-        int m0, n0;
-        origin(tile, m0, n0);
+        for (int tile = 0; tile < mine; ++tile) {
+            int m0, n0;
+            origin(tile, m0, n0);
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-            osw[n] = CF::SW_OFF + 4 * (CF::ALIGNED ? wrow / 128 : (n0 + wrow + 16 * n) / 128 - n0 / 128);
-        if (CF::ALIGNED ? tile == 0 : true) read_scales(cur);
-        if (tile == 0) {
-            fa[0] = fp8_read_frag(ra0, ra1);
+            for (int n = 0; n < NP; ++n)
+                osw[n] = CF::SW_OFF + 4 * (CF::ALIGNED ? wrow / 128 : (n0 + wrow + 16 * n) / 128 - n0 / 128);
+            if (CF::ALIGNED ? tile == 0 : true) read_scales(cur);
+            if (tile == 0) {
+                fa[0] = fp8_read_frag(ra0, ra1);
 #pragma unroll
-            for (int n = 0; n < TW; ++n) fw[n] = fp8_read_frag(rw0 + 2048 * n, rw1 + 2048 * n);
-        }
+                for (int n = 0; n < TW; ++n) fw[n] = fp8_read_frag(rw0 + 2048 * n, rw1 + 2048 * n);
+            }
 #pragma unroll
-        for (int n = 0; n < TW; ++n) {
+            for (int n = 0; n < TW; ++n) {
 #pragma unroll
-            for (int f = 0; f < TF; ++f) acc[n][f] = v4f{0.f, 0.f, 0.f, 0.f};
-            d[1][n] = v4f{0.f, 0.f, 0.f, 0.f};  // no pending sums
-        }
+                for (int f = 0; f < TF; ++f) acc[n][f] = v4f{0.f, 0.f, 0.f, 0.f};
+                d[1][n] = v4f{0.f, 0.f, 0.f, 0.f};  // no pending sums
+            }
 #pragma unroll
-        for (int n = 0; n < NP; ++n) p[1][n] = 0.0f;
+            for (int n = 0; n < NP; ++n) p[1][n] = 0.0f;
 
-        for (int s = 0; s < nk; ++s) stage(copy_tag);
+            for (int s = 0; s < nk; ++s) stage(copy_tag);
 #pragma unroll
-        for (int n = 0; n < TW; ++n) add(TF - 1, n);
-        fp8_store_tile<TW, TF>(acc, m0 + arow, n0 + wrow, lane, g);
-    }
+            for (int n = 0; n < TW; ++n) add(TF - 1, n);
+            fp8_store_tile<TW, TF>(acc, m0 + arow, n0 + wrow, lane, g);
+        }
     };
     if (CF::LW == 0 && (CF::CW == CF::MW || wave < CF::CW))
         run(std::true_type{});
@@ -403,18 +403,22 @@ const Tile kTiles[] = {
 constexpr int kTileCount = int(sizeof kTiles / sizeof kTiles[0]);
 constexpr float kTileUs = 2.0f;  // a tile's epilogue and first loads
 
-// The tile with the least time by rounds of tiles over the CUs.  Measured (us,
-// the chosen one first): 1024 x 3584 x 4608: 128x160 22.7, 128x192 23.9, 256x128
-// 27.2, 128x128 30.3; 811 x 16384 x 2048: 128x64 45.7, 64x128 46.1, 128x96 50.7,
-// 256x256 165; 4096 x 3584 x 37888: 256x256 530, 256x128 538, 128x128 740.
-int pick_tile(const Fp8Args& g, int cus) {
-    int best = 0;
-    float least = 0.0f;
+// The tile with the least time by rounds of tiles over the CUs, and that time.
+// Measured (us, the chosen one first): 1024 x 3584 x 4608: 128x160 22.7, 128x192
+// 23.9, 256x128 27.2, 128x128 30.3; 811 x 16384 x 2048: 128x64 45.7, 64x128 46.1,
+// 128x96 50.7, 256x256 165; 4096 x 3584 x 37888: 256x256 530, 256x128 538, 128x128
+// 740.  Tiles of 32 tokens were no faster than those of 64 at 32 tokens.
+struct Pick {
+    int tile;
+    float us;
+};
+Pick pick_tile(const Fp8Args& g, int cus) {
+    Pick best{0, 0.0f};
     for (int i = 0; i < kTileCount; ++i) {
         const Tile& t = kTiles[i];
         const int64_t tiles = int64_t((g.M + t.bm - 1) / t.bm) * ((g.N + t.bn - 1) / t.bn);
         const float us = float((tiles + cus - 1) / cus) * (float(g.K / 128) * t.stage_us + kTileUs);
-        if (i == 0 || us < least) best = i, least = us;
+        if (i == 0 || us < best.us) best = Pick{i, us};
     }
     return best;
 }
@@ -427,9 +431,27 @@ int fp8_tile_id(const char* name) {
     return -1;
 }
 
+// Which of the two for up to 32 tokens, by what each has to move: both stream the
+// weights (at 5.1 TB/s); the GEMV reads the codes again from L2 for every 16
+// weight rows (8 TB/s in all, less where row groups are fewer than CUs), the GEMM
+// takes its rounds of tiles.  Measured (us, GEMV / GEMM):
+//   K = 3584, N = 37888: 26.9 / 28.0 with 4 tokens, 36.9 / 28.0 with 16, 50.5 / 28.1 with 32
+//   K = 3584, N = 4608: 8.8 / 11.0 with 16, 12.0 / 11.1 with 32
+//   K = 8192, N = 8192: 18.7 / 22.0 with 16, 25.7 / 23.9 with 32
+//   K = 16384, N = 2048: 16.9 / 35.2 with 16, 23.9 / 35.4 with 32
+//   K = 1024, N = 16384: 5.6 / 6.5 with 8, 8.4 / 6.8 with 32
+bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev) {
+    if (g.M > kGemvMaxM || hooks().fp8_tile.load(std::memory_order_relaxed) >= 0) return false;
+    const int groups = (g.N + 15) / 16;
+    const float weights = float(g.N) * float(g.K) * 1e-6f, codes = float(groups) * float(g.M) * float(g.K) * 1e-6f;
+    const float fill = groups < dev.cus ? float(groups) / float(dev.cus) : 1.0f;
+    const float stream = weights / 5.1f, reads = (weights + codes) / (8.0f * fill), tiles = pick_tile(g, dev.cus).us;
+    return 2.5f + (reads > stream ? reads : stream) <= 2.8f + (tiles > stream ? tiles : stream);
+}
+
 hipError_t launch_fp8_gemm(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream) {
     const int forced = hooks().fp8_tile.load(std::memory_order_relaxed);
-    return kTiles[forced >= 0 ? forced : pick_tile(g, dev.cus)].launch(g, dev, stream);
+    return kTiles[forced >= 0 ? forced : pick_tile(g, dev.cus).tile].launch(g, dev, stream);
 }
 
 }  // namespace fq

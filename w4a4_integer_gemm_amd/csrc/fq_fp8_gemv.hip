@@ -1,11 +1,18 @@
-// FP8 sites for decode-sized M (at most 32 tokens): a weight-streaming GEMV.
+// FP8 sites for decode-sized M (at most 32 tokens): the weight-streaming GEMV
+// that reads the tokens' codes from L2.
 //
-// Bound by reading the weight codes once.  A workgroup owns one group of 16
-// weight rows; its waves split K in units of 128 (one scale group): per unit a
-// lane loads 2 x 16 bytes of weight codes and of each token tile's codes, one
-// v_mfma_f32_16x16x128_f8f6f4 multiplies 16 rows by 16 tokens, and the product
-// is added to the float32 sums times sa * sw.  The waves' partial tiles meet
-// in LDS; one wave per token tile runs the epilogue.
+// Bound by reading the weight codes once.  S waves of a workgroup share the K
+// range of a group of 16 weight rows, in units of 128 (one scale group): per
+// unit a lane loads 2 x 16 bytes of weight codes and of each token tile's codes,
+// one v_mfma_f32_16x16x128_f8f6f4 multiplies 16 rows by 16 tokens, and the product
+// is added to the float32 sums times sa * sw.  A wave requests C units before it
+// uses the first; the S partial tiles meet in LDS in a fixed order.
+//
+// What costs beside the weights is the codes, read again for every row group:
+// K = 3584, N = 37888 (26.6 us at copy rate): 25.7 us with one token, 26.9 with
+// 4, 30 with 8, beyond which the tiled GEMM takes over (fp8_gemv_takes).
+// Narrow layers keep it up to 32 tokens: K = 16384, N = 2048 12.0 us with one
+// token, 23.9 with 32 (half of the CUs have a row group; the GEMM 35).
 #include <hip/hip_runtime.h>
 
 #include "fq_device.h"
@@ -17,27 +24,23 @@ namespace {
 
 constexpr int kWaves = 8;
 
-__device__ __forceinline__ v8i join(uint4 a, uint4 b) {
-    return v8i{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
-}
-
 // MT token tiles of 16, C units loaded before any is used
-template <int MT, int C>
+template <int MT, int S, int C>
 __global__ __launch_bounds__(64 * kWaves) void fp8_gemv_kernel(Fp8Args g, int per) {
+    constexpr int G = kWaves / S;  // row groups of a workgroup
     __shared__ v4f red[kWaves][MT][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int q = lane >> 4;
-    const int n0 = blockIdx.x * 16;
+    const int q = lane >> 4, ks = wave % S;
+    const int n0 = (blockIdx.x * G + wave / S) * 16;
     const int nu = g.K / 128;
-    const int u_begin = wave * per;
-    const int u_end = u_begin + per < nu ? u_begin + per : nu;
+    const int u_begin = ks * per, u_end = u_begin + per < nu ? u_begin + per : nu;
     const int lda = fp8_scale_ld(g.M);
 
     int row = n0 + (lane & 15);
     row = row < g.N ? row : g.N - 1;  // rows past N load a valid row; their outputs are not stored
     const uint8_t* const wp = g.w + int64_t(row) * g.K + 16 * q;
-    const float* const swp = g.wscale + int64_t(n0 / 128) * nu;
+    const float* const swp = g.wscale + int64_t((n0 < g.N ? n0 : g.N - 1) / 128) * nu;
     const uint8_t* ap[MT];
     int tok[MT];
 #pragma unroll
@@ -83,27 +86,49 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_gemv_kernel(Fp8Args g, int pe
 #pragma unroll
     for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
     __syncthreads();
-    if (wave >= MT) return;
-    v4f sum[1][1] = {{red[0][wave][lane]}};
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum[0][0] += red[w][wave][lane];
-    const int mm[1] = {16 * wave + (lane & 15)};
-    const int nn[1] = {n0 + 4 * q};
-    fp8_store_tiles<1, 1>(sum, mm, nn, g);
+    for (int t = 0; t < MT; ++t) {
+        if (ks != t % S) continue;
+        v4f sum[1][1] = {{red[wave - ks][t][lane]}};
+#pragma unroll
+        for (int i = 1; i < S; ++i) sum[0][0] += red[wave - ks + i][t][lane];
+        const int mm[1] = {16 * t + (lane & 15)}, nn[1] = {n0 + 4 * q};
+        fp8_store_tiles<1, 1>(sum, mm, nn, g);
+    }
+}
+
+template <int S, int C>
+hipError_t launch_c(const Fp8Args& g, int per, hipStream_t st) {
+    constexpr int rows = 16 * (kWaves / S);
+    const dim3 grid((g.N + rows - 1) / rows), block(64 * kWaves);
+    if (g.M <= 16)
+        hipLaunchKernelGGL((fp8_gemv_kernel<1, S, C>), grid, block, 0, st, g, per);
+    else
+        hipLaunchKernelGGL((fp8_gemv_kernel<2, S, C>), grid, block, 0, st, g, per);
+    return hipGetLastError();
+}
+
+// Four units at a time, three where that requests fewer units past a wave's share.
+template <int S>
+hipError_t launch_s(const Fp8Args& g, hipStream_t st) {
+    const int per = (g.K / 128 + S - 1) / S;
+    return (per + 2) / 3 * 3 < (per + 3) / 4 * 4 ? launch_c<S, 3>(g, per, st) : launch_c<S, 4>(g, per, st);
 }
 
 }  // namespace
 
-hipError_t launch_fp8_gemv(const Fp8Args& g, hipStream_t stream) {
+// Waves that share a row group: 8 where a wave then still has more than two
+// units, or where there is at most one group for each CU; otherwise 4, 2 or 1, so
+// that a wave's loads in flight are not cut short by its share (M = 1, K = 2048,
+// N = 32768: 22.6 us with 8, 14.0 with 4, 15.5 with 2; K = 1024, N = 16384: 9.2, 7.2,
+// 5.2; K = 3584, N = 37888: 26.0, 29.0, 33.9; K = 896, N = 1024: 3.5, 4.1, 4.3).
+hipError_t launch_fp8_gemv(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream) {
     if (g.M > kGemvMaxM) return hipErrorInvalidValue;
-    const int nu = g.K / 128;
-    const int per = (nu + kWaves - 1) / kWaves;
-    const dim3 grid((g.N + 15) / 16), block(64 * kWaves);
-    if (g.M <= 16)
-        hipLaunchKernelGGL((fp8_gemv_kernel<1, 4>), grid, block, 0, stream, g, per);
-    else
-        hipLaunchKernelGGL((fp8_gemv_kernel<2, 4>), grid, block, 0, stream, g, per);
-    return hipGetLastError();
+    const int nu = g.K / 128, groups = (g.N + 15) / 16;
+    if (nu > 16 || groups <= dev.cus) return launch_s<8>(g, stream);
+    if (nu > 8) return launch_s<4>(g, stream);
+    if (nu > 4) return launch_s<2>(g, stream);
+    return launch_s<1>(g, stream);
 }
 
 }  // namespace fq

@@ -41,6 +41,11 @@ __device__ __forceinline__ v8i fp8_read_frag(uint32_t lo, uint32_t hi) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// The 32 codes of a fragment from the two 16-byte pieces.
+__device__ __forceinline__ v8i join(uint4 a, uint4 b) {
+    return v8i{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
+}
+
 __device__ __forceinline__ uint16_t* fp8_out_ptr(const Fp8Args& g, int m, int n) {
     if (g.head_dim > 0) {
         const int h = n / g.head_dim;

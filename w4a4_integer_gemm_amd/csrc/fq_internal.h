@@ -161,7 +161,11 @@ struct Fp8Args {
     int32_t head_dim;  // 0: y is [M][ldy]; else y is [N/head_dim][M][head_dim]
 };
 hipError_t launch_fp8_gemm(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
-hipError_t launch_fp8_gemv(const Fp8Args& g, hipStream_t stream);
+bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev);
+hipError_t launch_fp8_gemv(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
+// The one-token form with its prologue (fq_fp8_decode1.hip) and whether it takes a call.
+bool fp8_decode1_takes(const NormArgs& p, const Fp8Args& g);
+hipError_t launch_fp8_decode1(const NormArgs& p, const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
 
 // Rotary positions (fq_rope.hip).
 struct RopeArgs {

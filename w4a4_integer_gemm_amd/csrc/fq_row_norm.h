@@ -1,0 +1,37 @@
+// The sums and the normalisation of a row held by one workgroup (gfx950,
+// wave64): shared by the kernels whose codes have to agree bit for bit.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "fq_token.h"
+
+namespace fq {
+
+// Sum over the workgroup; every thread gets the same value.  `red` is used by
+// one call only (no barrier separates two uses).
+__device__ __forceinline__ double block_sum(double v, int nwaves, double* red) {
+    v = wave_sum(v);
+    if (nwaves > 1) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0;
+        for (int w = 0; w < nwaves; ++w) v += red[w];
+    }
+    return v;
+}
+
+// 1 / sqrt(mean + eps) from a row's float64 sum of squares.  ss / K correctly
+// rounded without a divide: Markstein's correction of ss * RN(1/K), rk.
+__device__ __forceinline__ float inv_rms(double ss, int K, double rk, float eps) {
+    const double q0 = ss * rk;
+    const float ms = float(__builtin_fma(__builtin_fma(-q0, double(K), ss), rk, q0));
+    return 1.0f / sqrtf(ms + eps);
+}
+
+__device__ __forceinline__ void unpack4(const float4 (&v)[2], float (&o)[8]) {
+    o[0] = v[0].x, o[1] = v[0].y, o[2] = v[0].z, o[3] = v[0].w;
+    o[4] = v[1].x, o[5] = v[1].y, o[6] = v[1].z, o[7] = v[1].w;
+}
+
+}  // namespace fq
