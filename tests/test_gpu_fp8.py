@@ -295,3 +295,22 @@ def test_tiles_take_single_tokens_too(tile, hook):
         qa, sa, qw, sw = rand_site(rng, M, N, K)
         y, tol = ref.fp8_gemm(qa, sa, qw, sw)
         ref.assert_gemm(run_gemm(qa, sa, qw, sw), y, tol, f"{tile} {M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("M,K,N", [(2, 128, 8), (3, 640, 4112), (5, 1408, 72), (8, 512, 4104), (7, 1024, 40), (4, 4096, 264),
+                                   (2, 8192, 72), (16, 256, 512), (9, 896, 4104), (3, 5248, 24), (17, 384, 4120),
+                                   (32, 512, 136), (32, 1024, 72), (5, 4096, 24), (2, 4096, 4104)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_few_tokens_linear(M, K, N, norm):
+    """A few tokens, strided, in one launch or two: codes and scales are the prologue's bit for bit."""
+    rng = np.random.default_rng(M + K + N + norm)
+    gamma = rng.uniform(0.5, 1.5, K).astype(np.float32) if norm else None
+    site = fq.Fp8Site((rng.standard_normal((N, K)) * 0.02).astype(np.float32), gamma=gamma)
+    x, residual = dev(ref.bf16(rng, M, K + 24)), ref.bf16(rng, M, N)
+    x = x[:, :K]
+    y = host(site.linear(x, residual=dev(residual)), np.uint16)
+    codes, scales = (host(t) for t in site.workspace_codes(M))
+    want_codes, want_scales = (host(t) for t in site.prologue(x))
+    assert np.array_equal(codes, want_codes) and np.array_equal(scales, want_scales[:, :M])
+    want, tol = ref.fp8_gemm(codes, scales, host(site.codes), host(site.wscale), None, residual)
+    ref.assert_gemm(y, want, tol, f"M={M} K={K} N={N} norm={norm}")

@@ -185,7 +185,7 @@ fq_status fq_fp8_linear(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, c
     fq::Fp8Args g{codes, scales, M, static_cast<const uint8_t*>(w_codes), wscale, N, K, bias,
                   static_cast<const uint16_t*>(residual_bf16), ldr, static_cast<uint16_t*>(y_bf16), ldy, head_dim};
     const fq::NormArgs a = prologue_args(x_bf16, M, K, ldx, gamma, eps, codes, scales);
-    if (fq::fp8_decode1_takes(a, g)) return device_status(fn, fq::launch_fp8_decode1(a, g, *dev, s));
+    if (fq::fp8_decode_takes(a, g)) return device_status(fn, fq::launch_fp8_decode(a, g, *dev, s));
     FQ_TRY(device_status(fn, fq::launch_block_norm(a, s)));
     return run_fp8_gemm(fn, g, *dev, s);
 }

@@ -163,9 +163,9 @@ struct Fp8Args {
 hipError_t launch_fp8_gemm(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
 bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev);
 hipError_t launch_fp8_gemv(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
-// The one-token form with its prologue (fq_fp8_decode1.hip) and whether it takes a call.
-bool fp8_decode1_takes(const NormArgs& p, const Fp8Args& g);
-hipError_t launch_fp8_decode1(const NormArgs& p, const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
+// A few tokens with their prologue in one launch (fq_fp8_decode.hip), and whether it takes a call.
+bool fp8_decode_takes(const NormArgs& p, const Fp8Args& g);
+hipError_t launch_fp8_decode(const NormArgs& p, const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
 
 // Rotary positions (fq_rope.hip).
 struct RopeArgs {
