@@ -142,3 +142,10 @@ def test_rows_of_zeros_and_non_finite_rows():
     for a, b in zip(got[:3], clean[:3]):
         assert np.array_equal(a[keep], b[keep])
     assert np.array_equal(got[3][:, keep], clean[3][:, keep])
+
+
+@pytest.mark.parametrize("M,K,out,f32", [(4099, 1032, "bf16", True), (4101, 1024, "both", False), (1025, 4352, "fp8", False),
+                                         (521, 8192, "both", True), (2055, 2056, "none", False)])
+def test_many_rows(M, K, out, f32):
+    """Calls large enough for two pieces per lane."""
+    run(M, K, 8, out=out, f32=f32, per=64)

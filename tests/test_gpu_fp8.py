@@ -314,3 +314,14 @@ def test_few_tokens_linear(M, K, N, norm):
     assert np.array_equal(codes, want_codes) and np.array_equal(scales, want_scales[:, :M])
     want, tol = ref.fp8_gemm(codes, scales, host(site.codes), host(site.wscale), None, residual)
     ref.assert_gemm(y, want, tol, f"M={M} K={K} N={N} norm={norm}")
+
+
+@pytest.mark.parametrize("M", [17, 24, 32])
+@pytest.mark.parametrize("N,K", [(2048, 384), (2056, 1152), (24, 2176), (4096, 128)])
+def test_two_token_tiles_of_narrow_layers(M, N, K):
+    """Either side of the choice to give the second tile of 16 tokens workgroups of its own."""
+    rng = np.random.default_rng(M + N + K)
+    qa, sa, qw, sw = rand_site(rng, M, N, K)
+    residual = ref.bf16(rng, M, N)
+    y, tol = ref.fp8_gemm(qa, sa, qw, sw, None, residual)
+    ref.assert_gemm(run_gemm(qa, sa, qw, sw, None, residual), y, tol, f"gemm {M}x{N}x{K}")

@@ -40,9 +40,9 @@ fq_status check_vector(const char* fn, const char* name, const void* p) {
 
 // One workgroup per row.
 fq_status check_norm_launch(const char* fn, int32_t M, int32_t K) {
-    if (int64_t(M) * fq::block_norm_threads(K) >= kMaxThreads)
+    if (int64_t(M) * fq::block_norm_threads(K, M) >= kMaxThreads)
         return fail(FQ_ERR_SHAPE, fmt("%s: M=%d rows of K=%d are too many for one launch (M x %d threads >= 2^32)", fn, M,
-                                      K, fq::block_norm_threads(K)));
+                                      K, fq::block_norm_threads(K, M)));
     return FQ_OK;
 }
 

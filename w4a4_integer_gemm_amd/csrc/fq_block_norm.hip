@@ -229,9 +229,9 @@ hipError_t launch_p(const NormArgs& a, int T, hipStream_t st) {
 
 template <bool F32>
 hipError_t launch_f(const NormArgs& a, hipStream_t st) {
-    const int T = block_norm_threads(a.K);
+    const int T = block_norm_threads(a.K, a.M);
     if (T > kMaxThreads) return hipErrorInvalidValue;
-    switch (block_norm_pieces(a.K)) {
+    switch (block_norm_pieces(a.K, a.M)) {
         case 1: return launch_p<1, F32>(a, T, st);
         case 2: return launch_p<2, F32>(a, T, st);
         case 4: return launch_p<4, F32>(a, T, st);

@@ -438,7 +438,7 @@ int fp8_tile_id(const char* name) {
 //   K = 3584, N = 37888: 26.9 / 28.0 with 4 tokens, 36.9 / 28.0 with 16, 50.5 / 28.1 with 32
 //   K = 3584, N = 4608: 8.8 / 11.0 with 16, 12.0 / 11.1 with 32
 //   K = 8192, N = 8192: 18.7 / 22.0 with 16, 25.7 / 23.9 with 32
-//   K = 16384, N = 2048: 16.9 / 35.2 with 16, 23.9 / 35.4 with 32
+//   K = 16384, N = 2048: 16.8 / 35.2 with 16, 16.7 / 35.4 with 32
 //   K = 1024, N = 16384: 5.6 / 6.5 with 8, 8.4 / 6.8 with 32
 bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev) {
     if (g.M > kGemvMaxM || hooks().fp8_tile.load(std::memory_order_relaxed) >= 0) return false;

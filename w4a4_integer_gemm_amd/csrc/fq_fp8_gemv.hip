@@ -12,7 +12,8 @@
 // K = 3584, N = 37888 (26.6 us at copy rate): 25.7 us with one token, 26.9 with
 // 4, 30 with 8, beyond which the tiled GEMM takes over (fp8_gemv_takes).
 // Narrow layers keep it up to 32 tokens: K = 16384, N = 2048 12.0 us with one
-// token, 23.9 with 32 (half of the CUs have a row group; the GEMM 35).
+// token, 16.7 with 32 (the GEMM 35), bound by what a CU keeps in flight: 16 waves
+// on a row group took the same time, and so did groups of 8 rows on twice the CUs.
 #include <hip/hip_runtime.h>
 
 #include "fq_device.h"
@@ -32,7 +33,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_gemv_kernel(Fp8Args g, int pe
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, ks = wave % S;
-    const int n0 = (blockIdx.x * G + wave / S) * 16;
+    const int n0 = (blockIdx.x * G + wave / S) * 16, m0 = blockIdx.y * 16 * MT;
     const int nu = g.K / 128;
     const int u_begin = ks * per, u_end = u_begin + per < nu ? u_begin + per : nu;
     const int lda = fp8_scale_ld(g.M);
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_gemv_kernel(Fp8Args g, int pe
     int tok[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        tok[t] = 16 * t + (lane & 15);
+        tok[t] = m0 + 16 * t + (lane & 15);
         tok[t] = tok[t] < g.M ? tok[t] : g.M - 1;  // (columns past M are not stored)
         ap[t] = g.act + int64_t(tok[t]) * g.K + 16 * q;
     }
@@ -92,27 +93,31 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_gemv_kernel(Fp8Args g, int pe
         v4f sum[1][1] = {{red[wave - ks][t][lane]}};
 #pragma unroll
         for (int i = 1; i < S; ++i) sum[0][0] += red[wave - ks + i][t][lane];
-        const int mm[1] = {16 * t + (lane & 15)}, nn[1] = {n0 + 4 * q};
+        const int mm[1] = {m0 + 16 * t + (lane & 15)}, nn[1] = {n0 + 4 * q};
         fp8_store_tiles<1, 1>(sum, mm, nn, g);
     }
 }
 
+// More than 16 tokens: both tiles in one workgroup share its weights, two
+// workgroups where that only fills idle CUs (K = 16384, N = 2048, 23 tokens: 16.7 us
+// against 21.0; K = N = 4096: 9.1 against 7.4).
 template <int S, int C>
-hipError_t launch_c(const Fp8Args& g, int per, hipStream_t st) {
+hipError_t launch_c(const Fp8Args& g, const DeviceInfo& dev, int per, hipStream_t st) {
     constexpr int rows = 16 * (kWaves / S);
-    const dim3 grid((g.N + rows - 1) / rows), block(64 * kWaves);
-    if (g.M <= 16)
-        hipLaunchKernelGGL((fp8_gemv_kernel<1, S, C>), grid, block, 0, st, g, per);
+    const int blocks = (g.N + rows - 1) / rows, tiles = (g.M + 15) / 16;
+    const dim3 block(64 * kWaves);
+    if (tiles == 1 || 2 * ((g.N + 15) / 16) <= dev.cus)
+        hipLaunchKernelGGL((fp8_gemv_kernel<1, S, C>), dim3(blocks, tiles), block, 0, st, g, per);
     else
-        hipLaunchKernelGGL((fp8_gemv_kernel<2, S, C>), grid, block, 0, st, g, per);
+        hipLaunchKernelGGL((fp8_gemv_kernel<2, S, C>), dim3(blocks), block, 0, st, g, per);
     return hipGetLastError();
 }
 
 // Four units at a time, three where that requests fewer units past a wave's share.
 template <int S>
-hipError_t launch_s(const Fp8Args& g, hipStream_t st) {
+hipError_t launch_s(const Fp8Args& g, const DeviceInfo& dev, hipStream_t st) {
     const int per = (g.K / 128 + S - 1) / S;
-    return (per + 2) / 3 * 3 < (per + 3) / 4 * 4 ? launch_c<S, 3>(g, per, st) : launch_c<S, 4>(g, per, st);
+    return (per + 2) / 3 * 3 < (per + 3) / 4 * 4 ? launch_c<S, 3>(g, dev, per, st) : launch_c<S, 4>(g, dev, per, st);
 }
 
 }  // namespace
@@ -125,10 +130,10 @@ hipError_t launch_s(const Fp8Args& g, hipStream_t st) {
 hipError_t launch_fp8_gemv(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream) {
     if (g.M > kGemvMaxM) return hipErrorInvalidValue;
     const int nu = g.K / 128, groups = (g.N + 15) / 16;
-    if (nu > 16 || groups <= dev.cus) return launch_s<8>(g, stream);
-    if (nu > 8) return launch_s<4>(g, stream);
-    if (nu > 4) return launch_s<2>(g, stream);
-    return launch_s<1>(g, stream);
+    if (nu > 16 || groups <= dev.cus) return launch_s<8>(g, dev, stream);
+    if (nu > 8) return launch_s<4>(g, dev, stream);
+    if (nu > 4) return launch_s<2>(g, dev, stream);
+    return launch_s<1>(g, dev, stream);
 }
 
 }  // namespace fq

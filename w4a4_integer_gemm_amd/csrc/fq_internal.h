@@ -135,10 +135,17 @@ struct NormArgs {
     uint8_t* codes;    // nullptr: not written
     float* act_scale;  // [K / 128][fp8_scale_ld(M)]
 };
-// Pieces of 8 values per lane (1, 2, 4 or 8) and threads of a row's workgroup.
-inline int block_norm_pieces(int32_t K) { return K <= 8192 ? 1 : K <= 16384 ? 2 : K <= 32768 ? 4 : 8; }
-inline int block_norm_threads(int32_t K) {
-    const int P = block_norm_pieces(K);
+// Pieces of 8 values per lane (1, 2, 4 or 8) and threads of a row's workgroup.  Many
+// rows are bound by the instructions of their waves, half of which are the row's
+// sums and scales, once per wave: two pieces per lane halve those (us, two / one:
+// 4096 x 3584 to codes 13.0 / 15.3, with post norm and stream 24.5 / 26.6, 4096 x
+// 8192 29.2 / 35.0; 1024 x 3584 and 1024 x 2048 within 0.2 of each other).
+inline int block_norm_pieces(int32_t K, int32_t M) {
+    if (K > 8192) return K <= 16384 ? 2 : K <= 32768 ? 4 : 8;
+    return K >= 1024 && int64_t(M) * K >= 1 << 22 ? 2 : 1;
+}
+inline int block_norm_threads(int32_t K, int32_t M) {
+    const int P = block_norm_pieces(K, M);
     return ((K / 8 + P - 1) / P + 63) / 64 * 64;
 }
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream);
