@@ -81,6 +81,26 @@ def test_fp8_sizes():
     assert fq.fq_fp8_linear_workspace_bytes(3, 200) == 0
 
 
+def test_fp8_workspace_has_room_for_parts():
+    """Long sums of up to 1024 tokens: 256 tiles of 64 x 64 floats behind the codes and scales."""
+    for M, K in ((2, 4096), (1024, 65536), (37, 5120)):
+        codes = -(-M * K // 256) * 256
+        scales = -(-4 * fq.fq_fp8_ascale_count(M, K) // 256) * 256
+        assert fq.fq_fp8_linear_workspace_bytes(M, K) == codes + scales + (4 << 20)
+    assert fq.fq_fp8_linear_workspace_bytes(1, 4096) == 4096 + 512
+    assert fq.fq_fp8_linear_workspace_bytes(1025, 4096) < 4 << 21
+    assert fq.fq_fp8_linear_workspace_bytes(64, 3968) < 1 << 20
+
+
+def test_fp8_tile_hook_parses_and_rejects():
+    names = ("256x256", "256x128", "128x192", "128x160", "128x128", "128x96", "128x64", "64x128", "64x64", "auto")
+    for name in names:
+        fq.fq_test_hook("fp8_tile=" + name)
+    with pytest.raises(fq.FqError, match="unknown fp8_tile '32x32'"):
+        fq.fq_test_hook("fp8_tile=32x32")
+    fq.fq_test_hook("")
+
+
 @pytest.mark.parametrize("W,match", [
     (np.full((2, 128), np.nan, np.float32), r"W\[\d\]\[\d+\] is not finite"),
     (np.full((2, 128), np.inf, np.float32), "is not finite"),

@@ -1,6 +1,7 @@
 """FP8 sites with block scales on the GPU against plain 64-bit references."""
 import numpy as np
 import pytest
+import torch
 
 import blockref as ref
 import synth
@@ -325,3 +326,41 @@ def test_two_token_tiles_of_narrow_layers(M, N, K):
     residual = ref.bf16(rng, M, N)
     y, tol = ref.fp8_gemm(qa, sa, qw, sw, None, residual)
     ref.assert_gemm(run_gemm(qa, sa, qw, sw, None, residual), y, tol, f"gemm {M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("M,K,N", [(2, 4096, 64), (17, 16384, 136), (23, 18944, 72), (40, 4096, 1032), (64, 8192, 520), (65, 5120, 264),
+                                   (130, 9728, 896), (200, 16384, 512), (33, 5248, 264), (1024, 8192, 64)])
+@pytest.mark.parametrize("head_dim", [0, 8])
+def test_long_narrow_layers(M, K, N, head_dim):
+    """Few tiles of long sums: K in parts that meet in the workspace."""
+    rng = np.random.default_rng(M + K + N)
+    site = fq.Fp8Site((rng.standard_normal((N, K)) * 0.02).astype(np.float32), gamma=rng.uniform(0.5, 1.5, K).astype(np.float32),
+                      bias=rng.standard_normal(N).astype(np.float32))
+    x, residual = dev(ref.bf16(rng, M, K)), ref.bf16(rng, M, N + 8)
+    site.workspace(M).fill_(0xFF)  # (NaN patterns wherever a part is not written)
+    y = torch.full((N // 8, M, 8) if head_dim else (M + 1, N + 16), 77, dtype=torch.int16, device="cuda")
+    site.linear(x, residual=dev(residual), head_dim=head_dim, y=y[:M, :N] if not head_dim else y)
+    codes, scales = (host(t) for t in site.workspace_codes(M))
+    want, tol = ref.fp8_gemm(codes, scales, host(site.codes), host(site.wscale), host(site.bias), residual[:, :N])
+    got = host(y, np.uint16)
+    if head_dim:
+        got = got.transpose(1, 0, 2).reshape(M, N)
+    else:
+        assert np.all(got[M:] == 77) and np.all(got[:, N:] == 77), "wrote outside its rows"
+    ref.assert_gemm(got[:M, :N], want, tol, f"M={M} K={K} N={N}")
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 512, 264), (3, 640, 72), (20, 1152, 2056), (40, 512, 264), (140, 640, 520), (300, 256, 1032),
+                                   (48, 8192, 136)])
+def test_output_over_its_residual(M, K, N):
+    """y = residual: each output replaces the value that it added."""
+    rng = np.random.default_rng(M + K + N)
+    site = fq.Fp8Site((rng.standard_normal((N, K)) * 0.02).astype(np.float32))
+    x, residual = dev(ref.bf16(rng, M, K)), dev(ref.bf16(rng, M, N))
+    want = host(site.linear(x, residual=residual))
+    y = residual.clone()
+    assert np.array_equal(host(site.linear(x, residual=y, y=y)), want)
+    codes, scales = site.prologue(x)
+    want = host(site.gemm(codes, scales, M, residual=residual))
+    y = residual.clone()
+    assert np.array_equal(host(site.gemm(codes, scales, M, residual=y, y=y)), want)

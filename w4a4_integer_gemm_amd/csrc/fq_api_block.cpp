@@ -39,10 +39,10 @@ fq_status check_vector(const char* fn, const char* name, const void* p) {
 }
 
 // One workgroup per row.
-fq_status check_norm_launch(const char* fn, int32_t M, int32_t K) {
-    if (int64_t(M) * fq::block_norm_threads(K, M) >= kMaxThreads)
+fq_status check_norm_launch(const char* fn, int32_t M, int32_t K, bool f32) {
+    if (int64_t(M) * fq::block_norm_threads(K, M, f32) >= kMaxThreads)
         return fail(FQ_ERR_SHAPE, fmt("%s: M=%d rows of K=%d are too many for one launch (M x %d threads >= 2^32)", fn, M,
-                                      K, fq::block_norm_threads(K, M)));
+                                      K, fq::block_norm_threads(K, M, f32)));
     return FQ_OK;
 }
 
@@ -60,7 +60,7 @@ fq_status validate_fp8_prologue(const char* fn, const void* x, int32_t M, int32_
     if (!scale) return fail(FQ_ERR_ARG, fmt("%s: act_scale is NULL", fn));
     FQ_TRY(check_m(fn, M));
     FQ_TRY(check_k(fn, K, kGemmK));
-    FQ_TRY(check_norm_launch(fn, M, K));
+    FQ_TRY(check_norm_launch(fn, M, K, false));
     FQ_TRY(check_rows(fn, "x_bf16", "ldx", x, ldx, K, 8));
     if (gamma) FQ_TRY(check_eps(fn, "eps", eps));
     FQ_TRY(check_vector(fn, "gamma", gamma));
@@ -132,7 +132,8 @@ size_t fq_fp8_ascale_count(int32_t M, int32_t K) {
 
 size_t fq_fp8_linear_workspace_bytes(int32_t M, int32_t K) {
     if (!fq_fp8_ascale_count(M, K)) return 0;
-    return round_up(size_t(M) * size_t(K), 256) + round_up(scale_bytes(M, K), 256);
+    const size_t parts = fq::fp8_may_split(M, K) ? size_t(fq::kSplitTiles) * 64 * 64 * sizeof(float) : 0;
+    return round_up(size_t(M) * size_t(K), 256) + round_up(scale_bytes(M, K), 256) + parts;
 }
 
 fq_status fq_fp8_prologue(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, const float* gamma, float eps,
@@ -187,6 +188,11 @@ fq_status fq_fp8_linear(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, c
     const fq::NormArgs a = prologue_args(x_bf16, M, K, ldx, gamma, eps, codes, scales);
     if (fq::fp8_decode_takes(a, g)) return device_status(fn, fq::launch_fp8_decode(a, g, *dev, s));
     FQ_TRY(device_status(fn, fq::launch_block_norm(a, s)));
+    const int splits = fq::fp8_split(g, *dev);
+    if (splits > 1) {
+        float* const part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(scales) + round_up(scale_bytes(M, K), 256));
+        return device_status(fn, fq::launch_fp8_split(g, splits, part, *dev, s));
+    }
     return run_fp8_gemm(fn, g, *dev, s);
 }
 
@@ -200,7 +206,7 @@ fq_status fq_block_norm(int32_t M, int32_t K, const void* x_bf16, int64_t ldx, c
     const char* fn = "fq_block_norm";
     FQ_TRY(check_m(fn, M));
     FQ_TRY(check_k(fn, K, act_codes ? kGemmK : 8));
-    FQ_TRY(check_norm_launch(fn, M, K));
+    FQ_TRY(check_norm_launch(fn, M, K, stream_f32 != 0));
     if (stream_f32 != 0 && stream_f32 != 1)
         return fail(FQ_ERR_ARG, fmt("%s: stream_f32=%d must be 0 or 1", fn, stream_f32));
     if (!stream_in) return fail(FQ_ERR_ARG, fmt("%s: stream_in is NULL", fn));

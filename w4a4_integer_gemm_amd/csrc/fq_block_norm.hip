@@ -33,11 +33,6 @@ namespace {
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxWaves = kMaxThreads / 64;
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                      pack_bf16x2(v[6], v[7]));
-}
-
 // A row's vectors that a lane needs, by piece: gains float32, conditions bf16.
 template <int P>
 struct Vectors {
@@ -229,9 +224,9 @@ hipError_t launch_p(const NormArgs& a, int T, hipStream_t st) {
 
 template <bool F32>
 hipError_t launch_f(const NormArgs& a, hipStream_t st) {
-    const int T = block_norm_threads(a.K, a.M);
+    const int T = block_norm_threads(a.K, a.M, F32);
     if (T > kMaxThreads) return hipErrorInvalidValue;
-    switch (block_norm_pieces(a.K, a.M)) {
+    switch (block_norm_pieces(a.K, a.M, F32)) {
         case 1: return launch_p<1, F32>(a, T, st);
         case 2: return launch_p<2, F32>(a, T, st);
         case 4: return launch_p<4, F32>(a, T, st);

@@ -44,6 +44,7 @@
 #include "fq_device.h"
 #include "fq_fp8_tile.h"
 #include "fq_internal.h"
+#include "fq_row_norm.h"
 #include "fq_ring.h"
 
 namespace fq {
@@ -115,23 +116,25 @@ __device__ __forceinline__ v4i buffer_of(const uint8_t* p, uint32_t bytes) {
 typedef __attribute__((address_space(3))) const float lds_cfloat;
 __device__ __forceinline__ float lds_float(uint32_t addr) { return *reinterpret_cast<lds_cfloat*>(uintptr_t(addr)); }
 
-template <class CF>
+// SPLIT: each of `splits` parts of K (a divisor of its units) makes tiles of its
+// own, whose float32 sums go to part[split][M][N] instead of the epilogue.
+template <class CF, bool SPLIT>
 __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF::OCC, CF::OCC))) void fp8_gemm_kernel(
-    Fp8Args g, int tiles_m, int tiles_n, int group_m) {
+    Fp8Args g, int tiles_m, int tiles_n, int group_m, int splits, float* part) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[CF::LDS];
     constexpr int TF = CF::TF, TW = CF::TW, NC = CF::NC, NS = CF::NS, NP = CF::NP;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cw = CF::LW ? wave - CF::MW : wave;  // copying wave (0 .. CW - 1), or none
     const int q = lane >> 4;
-    const int nk = g.K / 128;
+    const int nu = g.K / 128, nk = SPLIT ? nu / splits : nu;
     const int lda = fp8_scale_ld(g.M);
     const uint32_t lds0 = lds_address(lds);
 
     // This workgroup's tiles: dispatch b runs on XCD b % 8, each XCD takes a
     // contiguous range of tiles, and its workgroups go through that range side
     // by side.
-    const int ntiles = tiles_m * tiles_n;
+    const int tiles = tiles_m * tiles_n, ntiles = SPLIT ? tiles * splits : tiles;
     const int x = blockIdx.x % 8, rem = ntiles % 8;
     const int on_xcd = (int(gridDim.x) - x + 7) / 8;  // workgroups of this XCD
     const int first = x * (ntiles / 8) + (x < rem ? x : rem), count = ntiles / 8 + (x < rem ? 1 : 0);
@@ -139,14 +142,16 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
     const int mine = j0 < count ? (count - j0 + on_xcd - 1) / on_xcd : 0;
     // Tiles are ordered in groups of group_m tiles of tokens, m fastest, so that
     // those in flight on an XCD share operand rows in its L2.
-    auto origin = [&](int i, int& m0, int& n0) {
-        const int t = first + j0 + i * on_xcd;
+    auto origin = [&](int i, int& m0, int& n0) {  // returns the part of K
+        const int item = first + j0 + i * on_xcd;
+        const int split = SPLIT ? item / tiles : 0, t = SPLIT ? item - split * tiles : item;
         const int gsize = group_m * tiles_n;
         const int gi = t / gsize, r = t - gi * gsize;
         const int left = tiles_m - gi * group_m;
         const int gm = left < group_m ? left : group_m;
         m0 = (gi * group_m + r % gm) * CF::BM;
         n0 = (r / gm) * CF::BN;
+        return split;
     };
 
     // The copy side, up to NS stages ahead of the products: copy i of a wave is
@@ -159,7 +164,7 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
     v4i ra{}, rw{};
     const uint8_t* psc = nullptr;
     const int64_t sc_step = cw == 0 ? 4 * int64_t(lda) : 4;  // bytes from one stage's scales to the next's
-    int copy_tile = 0, copy_s = 0;
+    int copy_tile = 0, copy_s = 0, copy_u0 = 0;  // (u0: the part's first unit)
     uint32_t copy_dst = lds0;
     auto chunk = [&](int i) {
         const int c = cw + CF::CW * i;
@@ -167,7 +172,7 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
     };
     auto aim = [&](int tile) {
         int m0, n0;
-        origin(tile, m0, n0);
+        copy_u0 = origin(tile, m0, n0) * nk;
         const int rows_a = g.M - m0 < CF::BM ? g.M - m0 : CF::BM, rows_w = g.N - n0 < CF::BN ? g.N - n0 : CF::BN;
         ra = buffer_of(g.act + int64_t(m0) * g.K, uint32_t(rows_a) * uint32_t(g.K));
         rw = buffer_of(g.w + int64_t(n0) * g.K, uint32_t(rows_w) * uint32_t(g.K));
@@ -175,18 +180,18 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
             int m = m0 + 4 * (lane < CF::BM / 4 ? lane : 0);
             m = m < lda - 4 ? m : lda - 4;
             sc_off = uint32_t(4 * (m - m0));
-            psc = reinterpret_cast<const uint8_t*>(g.act_scale + m0);
+            psc = reinterpret_cast<const uint8_t*>(g.act_scale + int64_t(copy_u0) * lda + m0);
         } else if (cw == 1) {  // one row block's scale per lane
             const int blk0 = n0 / 128, blk_last = (g.N - 1) / 128;
             const int blk = blk0 + lane < blk_last ? blk0 + lane : blk_last;
-            sc_off = uint32_t(4 * (blk - blk0) * nk);
-            psc = reinterpret_cast<const uint8_t*>(g.wscale + int64_t(blk0) * nk);
+            sc_off = uint32_t(4 * (blk - blk0) * nu);
+            psc = reinterpret_cast<const uint8_t*>(g.wscale + int64_t(blk0) * nu + copy_u0);
         }
     };
     auto copy_part = [&](int i) {
         const int c = chunk(i);
         const bool act = CF::EVEN ? i < CF::BM / 8 / CF::CW : 8 * c < CF::BM;
-        const uint32_t soff = uint32_t((8 * c - (act ? 0 : CF::BM)) * g.K + 128 * copy_s);
+        const uint32_t soff = uint32_t((8 * c - (act ? 0 : CF::BM)) * g.K + 128 * ((SPLIT ? copy_u0 : 0) + copy_s));
         copy16_buffer(act ? ra : rw, voff, soff, copy_dst + c * 1024);
     };
     auto copy_scales = [&]() {
@@ -336,7 +341,7 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
     auto run = [&](auto copy_tag) {
         for (int tile = 0; tile < mine; ++tile) {
             int m0, n0;
-            origin(tile, m0, n0);
+            const int split = origin(tile, m0, n0);
 #pragma unroll
             for (int n = 0; n < NP; ++n)
                 osw[n] = CF::SW_OFF + 4 * (CF::ALIGNED ? wrow / 128 : (n0 + wrow + 16 * n) / 128 - n0 / 128);
@@ -358,7 +363,10 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
             for (int s = 0; s < nk; ++s) stage(copy_tag);
 #pragma unroll
             for (int n = 0; n < TW; ++n) add(TF - 1, n);
-            fp8_store_tile<TW, TF>(acc, m0 + arow, n0 + wrow, lane, g);
+            if constexpr (SPLIT)
+                fp8_store_part<TW, TF>(acc, m0 + arow, n0 + wrow, lane, g, part + int64_t(split) * g.M * g.N);
+            else
+                fp8_store_tile<TW, TF>(acc, m0 + arow, n0 + wrow, lane, g);
         }
     };
     if (CF::LW == 0 && (CF::CW == CF::MW || wave < CF::CW))
@@ -373,9 +381,38 @@ hipError_t launch_cfg(const Fp8Args& g, const DeviceInfo& dev, hipStream_t st) {
     const int tiles_m = (g.M + CF::BM - 1) / CF::BM;
     const int tiles_n = (g.N + CF::BN - 1) / CF::BN;
     const int slots = dev.cus * CF::WGS, tiles = tiles_m * tiles_n;
-    hipLaunchKernelGGL((fp8_gemm_kernel<CF>), dim3(tiles < slots ? tiles : slots), dim3(CF::THREADS), 0, st, g, tiles_m,
-                       tiles_n, 8);
+    hipLaunchKernelGGL((fp8_gemm_kernel<CF, false>), dim3(tiles < slots ? tiles : slots), dim3(CF::THREADS), 0, st, g,
+                       tiles_m, tiles_n, 8, 1, nullptr);
     return hipGetLastError();
+}
+
+// Joins the parts of K in their order and runs the epilogue: a thread for 8
+// features of one token.
+__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Args g, int splits, const float* part) {
+    const int per_row = g.N / 8, i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= g.M * per_row) return;
+    const int m = i / per_row, n = 8 * (i - m * per_row);
+    const float* p = part + int64_t(m) * g.N + n;
+    const int64_t step = int64_t(g.M) * g.N;
+    float s[8], v[8];
+    unpack4({*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)}, s);
+    for (int k = 1; k < splits; ++k) {
+        const float* const q = p + k * step;
+        unpack4({*reinterpret_cast<const float4*>(q), *reinterpret_cast<const float4*>(q + 4)}, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += v[e];
+    }
+    if (g.bias) {
+        unpack4({*reinterpret_cast<const float4*>(g.bias + n), *reinterpret_cast<const float4*>(g.bias + n + 4)}, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += v[e];
+    }
+    if (g.residual) {
+        unpack8(*reinterpret_cast<const uint4*>(g.residual + int64_t(m) * g.ldr + n), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += v[e];
+    }
+    *reinterpret_cast<uint4*>(fp8_out_ptr(g, m, n)) = pack8(s);
 }
 
 struct Tile {
@@ -431,10 +468,33 @@ int fp8_tile_id(const char* name) {
     return -1;
 }
 
-// Which of the two for up to 32 tokens, by what each has to move: both stream the
-// weights (at 5.1 TB/s); the GEMV reads the codes again from L2 for every 16
-// weight rows (8 TB/s in all, less where row groups are fewer than CUs), the GEMM
-// takes its rounds of tiles.  Measured (us, GEMV / GEMM):
+// Estimates (us) that choose between the GEMV, the GEMM and the GEMM with K in
+// parts.  All stream the weights, at 5.1 TB/s; the GEMV reads the codes again from
+// L2 for every 16 weight rows (8 TB/s in all, less where row groups are fewer than
+// CUs; a second tile of 16 tokens then runs beside the first); the GEMM takes its
+// rounds of tiles; parts of K are written, read and joined by a launch more.
+namespace {
+constexpr float kCopyRate = 5.1f, kReadRate = 8.0f;  // MB per us
+
+float weights_us(const Fp8Args& g) { return float(g.N) * float(g.K) * 1e-6f / kCopyRate; }
+float larger(float a, float b) { return a > b ? a : b; }
+
+float gemv_us(const Fp8Args& g, const DeviceInfo& dev) {
+    const int groups = (g.N + 15) / 16, rows = 2 * groups <= dev.cus && g.M > 16 ? 16 : g.M;
+    const float fill = groups < dev.cus ? float(groups) / float(dev.cus) : 1.0f;
+    const float bytes = (float(g.N) + float(groups) * float(rows)) * float(g.K) * 1e-6f;
+    return 2.5f + larger(bytes / (kReadRate * fill), weights_us(g));
+}
+float gemm_us(const Fp8Args& g, const DeviceInfo& dev) {
+    return 2.8f + larger(pick_tile(g, dev.cus).us, weights_us(g));
+}
+float split_us(const Fp8Args& g, int splits) {
+    const float parts = 8e-6f * float(splits) * float(g.M) * float(g.N);  // (written and read)
+    return 7.5f + larger(float(g.K / 128 / splits) * kTiles[kTileCount - 1].stage_us, weights_us(g)) + parts / kCopyRate;
+}
+}  // namespace
+
+// Measured (us, GEMV / GEMM):
 //   K = 3584, N = 37888: 26.9 / 28.0 with 4 tokens, 36.9 / 28.0 with 16, 50.5 / 28.1 with 32
 //   K = 3584, N = 4608: 8.8 / 11.0 with 16, 12.0 / 11.1 with 32
 //   K = 8192, N = 8192: 18.7 / 22.0 with 16, 25.7 / 23.9 with 32
@@ -442,11 +502,36 @@ int fp8_tile_id(const char* name) {
 //   K = 1024, N = 16384: 5.6 / 6.5 with 8, 8.4 / 6.8 with 32
 bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev) {
     if (g.M > kGemvMaxM || hooks().fp8_tile.load(std::memory_order_relaxed) >= 0) return false;
-    const int groups = (g.N + 15) / 16;
-    const float weights = float(g.N) * float(g.K) * 1e-6f, codes = float(groups) * float(g.M) * float(g.K) * 1e-6f;
-    const float fill = groups < dev.cus ? float(groups) / float(dev.cus) : 1.0f;
-    const float stream = weights / 5.1f, reads = (weights + codes) / (8.0f * fill), tiles = pick_tile(g, dev.cus).us;
-    return 2.5f + (reads > stream ? reads : stream) <= 2.8f + (tiles > stream ? tiles : stream);
+    return gemv_us(g, dev) <= gemm_us(g, dev);
+}
+
+// Parts of K for a call of few tiles: as many as the CUs take at once, each of at
+// least 8 units, all alike (K is cut at unit borders), so that every workgroup has
+// as many stages; 1 where that is no gain.  Measured (us of fq_fp8_linear, in parts
+// / whole): K = 16384, N = 2048: 16.5 / 20.6 with 23 tokens, 17.6 / 41.4 with 64, 29.6 /
+// 42.6 with 256; K = 18944, N = 3584: 23.5 / 27.3 with 16, 28.7 / 56.5 with 64; K =
+// 4096, N = 1024: 11.1 / 8.6 with 16, 11.8 / 14.5 with 64, 14.6 / 16.3 with 256.
+int fp8_split(const Fp8Args& g, const DeviceInfo& dev) {
+    if (hooks().fp8_tile.load(std::memory_order_relaxed) >= 0 || !fp8_may_split(g.M, g.K)) return 1;
+    const int cus = dev.cus < kSplitTiles ? dev.cus : kSplitTiles, nu = g.K / 128;
+    const int64_t tiles = int64_t((g.M + 63) / 64) * ((g.N + 63) / 64);
+    if (2 * tiles > cus) return 1;
+    int splits = int(cus / tiles) < nu / 8 ? int(cus / tiles) : nu / 8;
+    while (splits > 1 && nu % splits) --splits;
+    if (splits == 1) return 1;
+    const float whole = g.M <= kGemvMaxM && gemv_us(g, dev) < gemm_us(g, dev) ? gemv_us(g, dev) : gemm_us(g, dev);
+    return split_us(g, splits) < whole ? splits : 1;
+}
+
+hipError_t launch_fp8_split(const Fp8Args& g, int splits, float* part, const DeviceInfo& dev, hipStream_t stream) {
+    using CF = Fp8Cfg<64, 64, 2, 2, 4, 2, 8>;
+    const int tiles_m = (g.M + 63) / 64, tiles_n = (g.N + 63) / 64;
+    hipLaunchKernelGGL((fp8_gemm_kernel<CF, true>), dim3(tiles_m * tiles_n * splits), dim3(CF::THREADS), 0, stream, g,
+                       tiles_m, tiles_n, 8, splits, part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(fp8_join_kernel, dim3((g.M * (g.N / 8) + 255) / 256), dim3(256), 0, stream, g, splits, part);
+    return hipGetLastError();
 }
 
 hipError_t launch_fp8_gemm(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream) {

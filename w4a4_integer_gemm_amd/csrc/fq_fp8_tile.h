@@ -179,6 +179,18 @@ __device__ __forceinline__ void fp8_store_pairs(const v4f (&acc)[TW][TF], int m0
         }
     }
 }
+// A wave's float32 sums as they are, to part[m][n].
+template <int TW, int TF>
+__device__ __forceinline__ void fp8_store_part(const v4f (&acc)[TW][TF], int m0, int n0, int lane, const Fp8Args& g,
+                                               float* part) {
+#pragma unroll
+    for (int f = 0; f < TF; ++f)
+#pragma unroll
+        for (int n = 0; n < TW; ++n) {
+            const int m = m0 + 16 * f + (lane & 15), at = n0 + 16 * n + 4 * (lane >> 4);
+            if (m < g.M && at < g.N) *reinterpret_cast<v4f*>(part + int64_t(m) * g.N + at) = acc[n][f];
+        }
+}
 template <int TW, int TF>
 __device__ __forceinline__ void fp8_store_tile(const v4f (&acc)[TW][TF], int m0, int n0, int lane, const Fp8Args& g) {
     if (g.bias || g.residual)

@@ -139,13 +139,14 @@ struct NormArgs {
 // rows are bound by the instructions of their waves, half of which are the row's
 // sums and scales, once per wave: two pieces per lane halve those (us, two / one:
 // 4096 x 3584 to codes 13.0 / 15.3, with post norm and stream 24.5 / 26.6, 4096 x
-// 8192 29.2 / 35.0; 1024 x 3584 and 1024 x 2048 within 0.2 of each other).
-inline int block_norm_pieces(int32_t K, int32_t M) {
+// 8192 29.2 / 35.0; 1024 x 3584 and 1024 x 2048 within 0.2 of each other).  Rows
+// of a float32 stream wait for memory instead (12800 x 2048 gated: 64.4 / 60.6).
+inline int block_norm_pieces(int32_t K, int32_t M, bool f32) {
     if (K > 8192) return K <= 16384 ? 2 : K <= 32768 ? 4 : 8;
-    return K >= 1024 && int64_t(M) * K >= 1 << 22 ? 2 : 1;
+    return !f32 && K >= 1024 && int64_t(M) * K >= 1 << 22 ? 2 : 1;
 }
-inline int block_norm_threads(int32_t K, int32_t M) {
-    const int P = block_norm_pieces(K, M);
+inline int block_norm_threads(int32_t K, int32_t M, bool f32) {
+    const int P = block_norm_pieces(K, M, f32);
     return ((K / 8 + P - 1) / P + 63) / 64 * 64;
 }
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream);
@@ -168,6 +169,12 @@ struct Fp8Args {
     int32_t head_dim;  // 0: y is [M][ldy]; else y is [N/head_dim][M][head_dim]
 };
 hipError_t launch_fp8_gemm(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
+// K in parts (fq_fp8_linear's workspace has room for kSplitTiles partial tiles of
+// 64 x 64 floats where fp8_may_split): how many, and the two launches.
+constexpr int kSplitTiles = 256;
+inline bool fp8_may_split(int32_t M, int32_t K) { return M > 1 && M <= 1024 && K >= 4096; }
+int fp8_split(const Fp8Args& g, const DeviceInfo& dev);
+hipError_t launch_fp8_split(const Fp8Args& g, int splits, float* part, const DeviceInfo& dev, hipStream_t stream);
 bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev);
 hipError_t launch_fp8_gemv(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
 // A few tokens with their prologue in one launch (fq_fp8_decode.hip), and whether it takes a call.
