@@ -318,7 +318,7 @@ fq_status fq_fp8_gemm(const void* act_codes, const float* act_scale, int32_t M, 
 /* Device: prologue and GEMM on one stream, in one launch for a few tokens.
  * workspace: at least fq_fp8_linear_workspace_bytes(M, K) bytes, 256-byte aligned;
  * it holds the codes and, at the next 256-byte boundary, the scales after the
- * call (for 2 to 1024 tokens and K >= 4096 4 MiB more, for partial sums of
+ * call (for 2 to 1024 tokens and K >= 4096 16 MiB more, for partial sums of
  * layers of few tiles), and belongs to one call at a time.  y may be the residual
  * (with equal strides); it overlaps neither x nor the workspace. */
 size_t fq_fp8_linear_workspace_bytes(int32_t M, int32_t K);

@@ -132,7 +132,8 @@ size_t fq_fp8_ascale_count(int32_t M, int32_t K) {
 
 size_t fq_fp8_linear_workspace_bytes(int32_t M, int32_t K) {
     if (!fq_fp8_ascale_count(M, K)) return 0;
-    const size_t parts = fq::fp8_may_split(M, K) ? size_t(fq::kSplitTiles) * 64 * 64 * sizeof(float) : 0;
+    const size_t tile = size_t(fq::kSplitEdge) * fq::kSplitEdge * sizeof(float);
+    const size_t parts = fq::fp8_may_split(M, K) ? fq::kSplitTiles * tile : 0;
     return round_up(size_t(M) * size_t(K), 256) + round_up(scale_bytes(M, K), 256) + parts;
 }
 
@@ -188,10 +189,10 @@ fq_status fq_fp8_linear(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, c
     const fq::NormArgs a = prologue_args(x_bf16, M, K, ldx, gamma, eps, codes, scales);
     if (fq::fp8_decode_takes(a, g)) return device_status(fn, fq::launch_fp8_decode(a, g, *dev, s));
     FQ_TRY(device_status(fn, fq::launch_block_norm(a, s)));
-    const int splits = fq::fp8_split(g, *dev);
-    if (splits > 1) {
+    const fq::Fp8Split how = fq::fp8_split(g, *dev);
+    if (how.splits > 1) {
         float* const part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(scales) + round_up(scale_bytes(M, K), 256));
-        return device_status(fn, fq::launch_fp8_split(g, splits, part, *dev, s));
+        return device_status(fn, fq::launch_fp8_split(g, how, part, s));
     }
     return run_fp8_gemm(fn, g, *dev, s);
 }

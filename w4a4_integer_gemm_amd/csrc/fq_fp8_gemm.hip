@@ -425,6 +425,7 @@ template <int BM, int BN, int WM, int WN, int LW, int NS>
 constexpr Tile tile(const char* name, float stage_us) {
     return {name, BM, BN, stage_us, launch_cfg<Fp8Cfg<BM, BN, WM, WN, LW, 2, NS>>};
 }
+constexpr float kStage64 = 0.25f, kStage128 = 0.37f;
 // The largest tile copies the fewest bytes per product and multiplies on eight
 // waves, half of which copy between their products: with two waves of 256
 // registers on a SIMD there is no room for waves that only copy.  The others
@@ -433,9 +434,9 @@ constexpr Tile tile(const char* name, float stage_us) {
 const Tile kTiles[] = {
     tile<256, 256, 2, 4, 0, 2>("256x256", 1.15f), tile<256, 128, 2, 2, 4, 3>("256x128", 0.59f),
     tile<128, 192, 2, 2, 4, 3>("128x192", 0.52f), tile<128, 160, 2, 2, 4, 4>("128x160", 0.46f),
-    tile<128, 128, 2, 2, 4, 4>("128x128", 0.37f), tile<128, 96, 2, 2, 4, 5>("128x96", 0.35f),
+    tile<128, 128, 2, 2, 4, 4>("128x128", kStage128), tile<128, 96, 2, 2, 4, 5>("128x96", 0.35f),
     tile<128, 64, 2, 2, 4, 6>("128x64", 0.29f),   tile<64, 128, 2, 2, 4, 6>("64x128", 0.32f),
-    tile<64, 64, 2, 2, 4, 8>("64x64", 0.25f),
+    tile<64, 64, 2, 2, 4, 8>("64x64", kStage64),
 };
 constexpr int kTileCount = int(sizeof kTiles / sizeof kTiles[0]);
 constexpr float kTileUs = 2.0f;  // a tile's epilogue and first loads
@@ -488,9 +489,20 @@ float gemv_us(const Fp8Args& g, const DeviceInfo& dev) {
 float gemm_us(const Fp8Args& g, const DeviceInfo& dev) {
     return 2.8f + larger(pick_tile(g, dev.cus).us, weights_us(g));
 }
-float split_us(const Fp8Args& g, int splits) {
+// K in parts on tiles of `edge` squared: as many parts as the CUs take at once,
+// each of at least 8 units, all alike, so that every workgroup has as many stages.
+int parts_of(const Fp8Args& g, const DeviceInfo& dev, int edge) {
+    const int cus = dev.cus < kSplitTiles ? dev.cus : kSplitTiles, nu = g.K / 128;
+    const int64_t tiles = int64_t((g.M + edge - 1) / edge) * ((g.N + edge - 1) / edge);
+    if (2 * tiles > cus) return 1;
+    int splits = int(cus / tiles) < nu / 8 ? int(cus / tiles) : nu / 8;
+    while (splits > 1 && nu % splits) --splits;
+    return splits;
+}
+float split_us(const Fp8Args& g, int splits, int edge) {
+    const float stage_us = edge == 64 ? kStage64 : kStage128, fixed = edge == 64 ? 7.5f : 9.5f;
     const float parts = 8e-6f * float(splits) * float(g.M) * float(g.N);  // (written and read)
-    return 7.5f + larger(float(g.K / 128 / splits) * kTiles[kTileCount - 1].stage_us, weights_us(g)) + parts / kCopyRate;
+    return fixed + larger(float(g.K / 128 / splits) * stage_us, weights_us(g)) + parts / kCopyRate;
 }
 }  // namespace
 
@@ -505,32 +517,39 @@ bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev) {
     return gemv_us(g, dev) <= gemm_us(g, dev);
 }
 
-// Parts of K for a call of few tiles: as many as the CUs take at once, each of at
-// least 8 units, all alike (K is cut at unit borders), so that every workgroup has
-// as many stages; 1 where that is no gain.  Measured (us of fq_fp8_linear, in parts
-// / whole): K = 16384, N = 2048: 16.5 / 20.6 with 23 tokens, 17.6 / 41.4 with 64, 29.6 /
-// 42.6 with 256; K = 18944, N = 3584: 23.5 / 27.3 with 16, 28.7 / 56.5 with 64; K =
-// 4096, N = 1024: 11.1 / 8.6 with 16, 11.8 / 14.5 with 64, 14.6 / 16.3 with 256.
-int fp8_split(const Fp8Args& g, const DeviceInfo& dev) {
-    if (hooks().fp8_tile.load(std::memory_order_relaxed) >= 0 || !fp8_may_split(g.M, g.K)) return 1;
-    const int cus = dev.cus < kSplitTiles ? dev.cus : kSplitTiles, nu = g.K / 128;
-    const int64_t tiles = int64_t((g.M + 63) / 64) * ((g.N + 63) / 64);
-    if (2 * tiles > cus) return 1;
-    int splits = int(cus / tiles) < nu / 8 ? int(cus / tiles) : nu / 8;
-    while (splits > 1 && nu % splits) --splits;
-    if (splits == 1) return 1;
-    const float whole = g.M <= kGemvMaxM && gemv_us(g, dev) < gemm_us(g, dev) ? gemv_us(g, dev) : gemm_us(g, dev);
-    return split_us(g, splits) < whole ? splits : 1;
+// Measured (us of fq_fp8_linear, in parts / whole): K = 16384, N = 2048: 16.5 / 20.6
+// with 23 tokens, 17.6 / 41.4 with 64, 25.1 / 42.6 with 256; K = 18944, N = 3584:
+// 23.5 / 27.3 with 16, 28.7 / 56.5 with 64, 42.2 / 57.7 with 256; K = 32768, N
+// = 1024: 65.5 / 91.9 with 811; K = 4096, N = 1024: 11.1 / 8.6 with 16, 11.8 / 14.5
+// with 64, 14.6 / 16.3 with 256.
+Fp8Split fp8_split(const Fp8Args& g, const DeviceInfo& dev) {
+    if (hooks().fp8_tile.load(std::memory_order_relaxed) >= 0 || !fp8_may_split(g.M, g.K)) return Fp8Split{1, 0};
+    Fp8Split best{1, 0};
+    float least = gemm_us(g, dev);
+    if (g.M <= kGemvMaxM && gemv_us(g, dev) < least) least = gemv_us(g, dev);
+    for (int edge = 64; edge <= 128; edge += 64) {
+        const int splits = parts_of(g, dev, edge);
+        const float us = split_us(g, splits, edge);
+        if (splits > 1 && us < least) best = Fp8Split{splits, edge}, least = us;
+    }
+    return best;
 }
 
-hipError_t launch_fp8_split(const Fp8Args& g, int splits, float* part, const DeviceInfo& dev, hipStream_t stream) {
-    using CF = Fp8Cfg<64, 64, 2, 2, 4, 2, 8>;
-    const int tiles_m = (g.M + 63) / 64, tiles_n = (g.N + 63) / 64;
-    hipLaunchKernelGGL((fp8_gemm_kernel<CF, true>), dim3(tiles_m * tiles_n * splits), dim3(CF::THREADS), 0, stream, g,
+namespace {
+template <class CF>
+hipError_t launch_parts(const Fp8Args& g, int splits, float* part, hipStream_t st) {
+    const int tiles_m = (g.M + CF::BM - 1) / CF::BM, tiles_n = (g.N + CF::BN - 1) / CF::BN;
+    hipLaunchKernelGGL((fp8_gemm_kernel<CF, true>), dim3(tiles_m * tiles_n * splits), dim3(CF::THREADS), 0, st, g,
                        tiles_m, tiles_n, 8, splits, part);
-    const hipError_t e = hipGetLastError();
+    return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_fp8_split(const Fp8Args& g, Fp8Split how, float* part, hipStream_t stream) {
+    const hipError_t e = how.edge == 64 ? launch_parts<Fp8Cfg<64, 64, 2, 2, 4, 2, 8>>(g, how.splits, part, stream)
+                                        : launch_parts<Fp8Cfg<128, 128, 2, 2, 4, 2, 4>>(g, how.splits, part, stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(fp8_join_kernel, dim3((g.M * (g.N / 8) + 255) / 256), dim3(256), 0, stream, g, splits, part);
+    hipLaunchKernelGGL(fp8_join_kernel, dim3((g.M * (g.N / 8) + 255) / 256), dim3(256), 0, stream, g, how.splits, part);
     return hipGetLastError();
 }
 

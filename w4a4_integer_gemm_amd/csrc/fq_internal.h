@@ -170,11 +170,15 @@ struct Fp8Args {
 };
 hipError_t launch_fp8_gemm(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
 // K in parts (fq_fp8_linear's workspace has room for kSplitTiles partial tiles of
-// 64 x 64 floats where fp8_may_split): how many, and the two launches.
-constexpr int kSplitTiles = 256;
+// 128 x 128 floats where fp8_may_split): how many and on which tiles (1: whole), and
+// the two launches.
+constexpr int kSplitTiles = 256, kSplitEdge = 128;
+struct Fp8Split {
+    int splits, edge;
+};
 inline bool fp8_may_split(int32_t M, int32_t K) { return M > 1 && M <= 1024 && K >= 4096; }
-int fp8_split(const Fp8Args& g, const DeviceInfo& dev);
-hipError_t launch_fp8_split(const Fp8Args& g, int splits, float* part, const DeviceInfo& dev, hipStream_t stream);
+Fp8Split fp8_split(const Fp8Args& g, const DeviceInfo& dev);
+hipError_t launch_fp8_split(const Fp8Args& g, Fp8Split how, float* part, hipStream_t stream);
 bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev);
 hipError_t launch_fp8_gemv(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
 // A few tokens with their prologue in one launch (fq_fp8_decode.hip), and whether it takes a call.
