@@ -316,10 +316,11 @@ fq_status fq_fp8_gemm(const void* act_codes, const float* act_scale, int32_t M, 
                       int64_t ldr, int32_t head_dim, void* y_bf16, int64_t ldy, void* stream);
 
 /* Device: prologue and GEMM on one stream, in one launch for a few tokens.
- * workspace: at least fq_fp8_linear_workspace_bytes(M, K) bytes, 256-byte aligned;
+ * workspace: at least fq_fp8_linear_workspace_bytes(M, K) bytes (never fewer for a
+ * larger M or K), 256-byte aligned;
  * it holds the codes and, at the next 256-byte boundary, the scales after the
- * call (for 2 to 1024 tokens and K >= 4096 16 MiB more, for partial sums of
- * layers of few tiles), and belongs to one call at a time.  y may be the residual
+ * call (from 2 tokens and K = 4096 on 16 MiB more, for partial sums of layers of
+ * few tiles), and belongs to one call at a time.  y may be the residual
  * (with equal strides); it overlaps neither x nor the workspace. */
 size_t fq_fp8_linear_workspace_bytes(int32_t M, int32_t K);
 fq_status fq_fp8_linear(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, const float* gamma, float eps,

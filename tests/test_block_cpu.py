@@ -82,14 +82,19 @@ def test_fp8_sizes():
 
 
 def test_fp8_workspace_has_room_for_parts():
-    """Long sums of up to 1024 tokens: 256 tiles of 128 x 128 floats behind the codes and scales."""
+    """Long sums of two tokens and more: 256 tiles of 128 x 128 floats behind the codes and scales."""
     for M, K in ((2, 4096), (1024, 65536), (37, 5120)):
         codes = -(-M * K // 256) * 256
         scales = -(-4 * fq.fq_fp8_ascale_count(M, K) // 256) * 256
         assert fq.fq_fp8_linear_workspace_bytes(M, K) == codes + scales + (16 << 20)
     assert fq.fq_fp8_linear_workspace_bytes(1, 4096) == 4096 + 512
-    assert fq.fq_fp8_linear_workspace_bytes(1025, 4096) < 4 << 21
     assert fq.fq_fp8_linear_workspace_bytes(64, 3968) < 1 << 20
+    sizes = [fq.fq_fp8_linear_workspace_bytes(M, K) for M in (1, 2, 3, 31, 32, 33, 64, 1024, 1025, 5000)
+             for K in (128, 3968, 4096, 4224, 65536)]
+    for at in range(5):  # a workspace for the most tokens and the longest K serves every call
+        assert sizes[at::5] == sorted(sizes[at::5])
+    for at in range(0, len(sizes), 5):
+        assert sizes[at:at + 5] == sorted(sizes[at:at + 5])
 
 
 def test_fp8_tile_hook_parses_and_rejects():

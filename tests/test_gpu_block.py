@@ -140,3 +140,25 @@ def test_on_another_stream_and_two_at_once(M):
     for b, w in zip(blocks, want):
         for got, one in zip(b.outputs(), w):
             assert np.array_equal(host(got), one)
+
+
+def test_a_captured_site_keeps_its_workspace():
+    """A graph of a small call replays right after a larger call made the site's workspace grow."""
+    rng = np.random.default_rng(0)
+    K, N = 512, 264
+    site = fq.Fp8Site((rng.standard_normal((N, K)) * 0.02).astype(np.float32))
+    x, y = dev(ref.bf16(rng, 40, K)), torch.empty((40, N), dtype=torch.int16, device="cuda")
+    want = host(site.linear(x)).copy()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        site.linear(x, y=y)
+    big = dev(ref.bf16(rng, 3000, K))
+    for _ in range(3):
+        want_big = host(site.linear(big)).copy()
+        filler = [torch.full((40 * K + 256,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(host(y), want)
+        assert np.array_equal(host(site.linear(big)), want_big)
+        assert all(bool((t == 255).all()) for t in filler)
+        y.fill_(7)

@@ -176,7 +176,7 @@ constexpr int kSplitTiles = 256, kSplitEdge = 128;
 struct Fp8Split {
     int splits, edge;
 };
-inline bool fp8_may_split(int32_t M, int32_t K) { return M > 1 && M <= 1024 && K >= 4096; }
+inline bool fp8_may_split(int32_t M, int32_t K) { return M > 1 && K >= 4096; }
 Fp8Split fp8_split(const Fp8Args& g, const DeviceInfo& dev);
 hipError_t launch_fp8_split(const Fp8Args& g, Fp8Split how, float* part, hipStream_t stream);
 bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev);

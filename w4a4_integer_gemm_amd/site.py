@@ -143,7 +143,12 @@ class Fp8Site:
 
     W float32 [N][K], or codes [N][K] and wscale [ceil(N / 128)][K / 128] as a
     checkpoint stores them (numpy arrays, or torch tensors already on the
-    device); gamma: RMSNorm gain (None for a quant-only site)."""
+    device); gamma: RMSNorm gain (None for a quant-only site).
+
+    linear() uses the site's own workspace, which belongs to one call at a time: calls
+    on two streams at once take two sites (of the same codes and wscale).  A
+    workspace that grew leaves the one before allocated, since a captured graph may
+    still use it."""
 
     def __init__(self, W: Optional[np.ndarray] = None, gamma=None, bias=None, eps: float = 1e-6, device="cuda",
                  codes=None, wscale=None):
@@ -165,6 +170,7 @@ class Fp8Site:
         self.gamma = _to_dev(None if gamma is None else np.ascontiguousarray(gamma, np.float32), self.device)
         self.bias = _to_dev(None if bias is None else np.ascontiguousarray(bias, np.float32), self.device)
         self._ws = None
+        self._ws_before = []
         self._ws_bytes = {}  # M -> fq_fp8_linear_workspace_bytes
 
     # -- buffers
@@ -173,8 +179,11 @@ class Fp8Site:
         nbytes = self._ws_bytes.get(M)
         if nbytes is None:
             nbytes = self._ws_bytes[M] = B.fq_fp8_linear_workspace_bytes(M, self.K)
-        if self._ws is None or self._ws.numel() < nbytes:
+        if self._ws is None:
             self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        elif self._ws.numel() < nbytes:
+            self._ws_before.append(self._ws)
+            self._ws = torch.empty(max(nbytes, 2 * self._ws.numel()), dtype=torch.uint8, device=self.device)
         return self._ws
 
     def workspace_codes(self, M: int):
