@@ -329,7 +329,7 @@ def test_two_token_tiles_of_narrow_layers(M, N, K):
 
 
 @pytest.mark.parametrize("M,K,N", [(2, 4096, 64), (17, 16384, 136), (23, 18944, 72), (40, 4096, 1032), (64, 8192, 520), (65, 5120, 264),
-                                   (130, 9728, 896), (200, 16384, 512), (33, 5248, 264), (1024, 8192, 64), (2050, 4096, 16)])
+                                   (130, 9728, 896), (200, 16384, 512), (33, 5248, 264), (1024, 8192, 64), (2050, 4096, 16), (3, 65536, 40)])
 @pytest.mark.parametrize("head_dim", [0, 8])
 def test_long_narrow_layers(M, K, N, head_dim):
     """Few tiles of long sums: K in parts that meet in the workspace."""
