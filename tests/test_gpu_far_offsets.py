@@ -107,3 +107,20 @@ def test_rope_heads_and_tokens():
     fq.fq_rope(v, FAR, D, M, H, H, D, D, 0, dev(freq.view(np.int64)), att, None, 5, 0, w, D, 3 * FAR)
     want, mag = ref.rope(bf16_to_f64(bits), np.arange(5, 5 + M), freq, att, H, D, 0, False)
     ref.assert_bf16(host(w.contiguous(), np.uint16), want, mag, "rope")
+
+
+def test_more_rows_than_a_launch_takes_along_x():
+    """8.4 million short rows without a norm: sampled codes and scales, the last rows among them."""
+    M, K = (1 << 23) + 77, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randint(-2 ** 15, 2 ** 15, (M, K), generator=g, device="cuda", dtype=torch.int16)
+    x = torch.where((x & 0x7F80) == 0x7F80, torch.full_like(x, 0x3F80), x)  # finite
+    codes = torch.empty((M, K), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((1, -(-M // 4) * 4), dtype=torch.float32, device="cuda")
+    fq.fq_fp8_prologue(x, M, K, K, None, 0.0, codes, scales)
+    rows = torch.tensor([0, 1, 12345, (1 << 23) - 1, 1 << 23, M - 1], device="cuda")
+    v = synth.bf16_bits_to_f32(host(x[rows], np.uint16))
+    s = (np.abs(v).max(-1) / np.float32(448)).astype(np.float32)
+    assert np.array_equal(host(scales[0, rows]), s)
+    q = ref.e4m3_round((v / s[:, None]).astype(np.float64))
+    assert np.array_equal(ref.TABLE[host(codes[rows])], ref.TABLE[q])

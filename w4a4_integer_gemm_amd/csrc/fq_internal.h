@@ -123,7 +123,7 @@ struct NormArgs {
     void* r_out;  // nullptr: not written
     int64_t ld_rout;
     int32_t stream_f32;
-    int32_t pre_norm;        // 0: h = r' (the FP8 prologue of a quant-only site)
+    int32_t pre_norm;        // 0: h = r_in (the FP8 prologue of a quant-only site: no x, modulation or h)
     const float* pre_gamma;  // nullptr: unit gain
     float pre_eps;
     const uint16_t* mod_scale;  // nullptr: 0
