@@ -44,7 +44,6 @@
 #include "fq_device.h"
 #include "fq_fp8_tile.h"
 #include "fq_internal.h"
-#include "fq_row_norm.h"
 #include "fq_ring.h"
 
 namespace fq {
@@ -386,33 +385,35 @@ hipError_t launch_cfg(const Fp8Args& g, const DeviceInfo& dev, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Joins the parts of K in their order and runs the epilogue: a thread for 8
-// features of one token.
+// Joins the parts of K in their order and runs the epilogue: a thread for 4
+// features of one token, A parts requested at once (eight parts of 23 x 2048
+// outputs: 3.1 us; one after the other 3.9).
+template <int A>
 __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Args g, int splits, const float* part) {
-    const int per_row = g.N / 8, i = blockIdx.x * 256 + threadIdx.x;
+    const int per_row = g.N / 4, i = blockIdx.x * 256 + threadIdx.x;
     if (i >= g.M * per_row) return;
-    const int m = i / per_row, n = 8 * (i - m * per_row);
-    const float* p = part + int64_t(m) * g.N + n;
+    const int m = i / per_row, n = 4 * (i - m * per_row);
+    const float* const p = part + int64_t(m) * g.N + n;
     const int64_t step = int64_t(g.M) * g.N;
-    float s[8], v[8];
-    unpack4({*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)}, s);
-    for (int k = 1; k < splits; ++k) {
-        const float* const q = p + k * step;
-        unpack4({*reinterpret_cast<const float4*>(q), *reinterpret_cast<const float4*>(q + 4)}, v);
+    float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+    uint2 res = make_uint2(0, 0);
+    if (g.bias) bias = *reinterpret_cast<const float4*>(g.bias + n);
+    if (g.residual) res = *reinterpret_cast<const uint2*>(g.residual + int64_t(m) * g.ldr + n);
+    v4f s = {0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < splits; k0 += A) {
+        v4f v[A];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] += v[e];
-    }
-    if (g.bias) {
-        unpack4({*reinterpret_cast<const float4*>(g.bias + n), *reinterpret_cast<const float4*>(g.bias + n + 4)}, v);
+        for (int k = 0; k < A; ++k) {  // (past the last part: the last again, not added)
+            const int at = k0 + k < splits ? k0 + k : splits - 1;
+            v[k] = *reinterpret_cast<const v4f*>(p + at * step);
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] += v[e];
+        for (int k = 0; k < A; ++k)
+            if (k0 + k < splits) s = k0 + k == 0 ? v[0] : s + v[k];
     }
-    if (g.residual) {
-        unpack8(*reinterpret_cast<const uint4*>(g.residual + int64_t(m) * g.ldr + n), v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] += v[e];
-    }
-    *reinterpret_cast<uint4*>(fp8_out_ptr(g, m, n)) = pack8(s);
+    if (g.bias) s += v4f{bias.x, bias.y, bias.z, bias.w};
+    if (g.residual) s += v4f{bf16_lo(res.x), bf16_hi(res.x), bf16_lo(res.y), bf16_hi(res.y)};
+    *reinterpret_cast<uint2*>(fp8_out_ptr(g, m, n)) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
 }
 
 struct Tile {
@@ -500,7 +501,7 @@ int parts_of(const Fp8Args& g, const DeviceInfo& dev, int edge) {
     return splits;
 }
 float split_us(const Fp8Args& g, int splits, int edge) {
-    const float stage_us = edge == 64 ? kStage64 : kStage128, fixed = edge == 64 ? 7.5f : 9.5f;
+    const float stage_us = edge == 64 ? kStage64 : kStage128, fixed = edge == 64 ? 6.5f : 9.0f;
     const float parts = 8e-6f * float(splits) * float(g.M) * float(g.N);  // (written and read)
     return fixed + larger(float(g.K / 128 / splits) * stage_us, weights_us(g)) + parts / kCopyRate;
 }
@@ -517,11 +518,11 @@ bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev) {
     return gemv_us(g, dev) <= gemm_us(g, dev);
 }
 
-// Measured (us of fq_fp8_linear, in parts / whole): K = 16384, N = 2048: 16.5 / 20.6
-// with 23 tokens, 17.6 / 41.4 with 64, 25.1 / 42.6 with 256; K = 18944, N = 3584:
-// 23.5 / 27.3 with 16, 28.7 / 56.5 with 64, 42.2 / 57.7 with 256; K = 32768, N
-// = 1024: 65.5 / 91.9 with 811; K = 4096, N = 1024: 11.1 / 8.6 with 16, 11.8 / 14.5
-// with 64, 14.6 / 16.3 with 256.
+// Measured (us of fq_fp8_linear, in parts / whole): K = 16384, N = 2048: 13.5 / 16.7
+// with 8 tokens, 15.3 / 40.3 with 64, 23.4 / 42.1 with 256; K = 18944, N = 3584: 21.2
+// / 25.3 with 16, 26.8 / 55.0 with 64, 41.5 / 56.4 with 256; K = 32768, N = 1024: 60.4
+// / 86.8 with 811; K = 4096, N = 1024: 11.3 / 14.3 with 64, 14.9 / 16.1 with 256, and
+// whole 8.1 with 16, where parts took 11.
 Fp8Split fp8_split(const Fp8Args& g, const DeviceInfo& dev) {
     if (hooks().fp8_tile.load(std::memory_order_relaxed) >= 0 || !fp8_may_split(g.M, g.K)) return Fp8Split{1, 0};
     Fp8Split best{1, 0};
@@ -549,7 +550,13 @@ hipError_t launch_fp8_split(const Fp8Args& g, Fp8Split how, float* part, hipStre
     const hipError_t e = how.edge == 64 ? launch_parts<Fp8Cfg<64, 64, 2, 2, 4, 2, 8>>(g, how.splits, part, stream)
                                         : launch_parts<Fp8Cfg<128, 128, 2, 2, 4, 2, 4>>(g, how.splits, part, stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(fp8_join_kernel, dim3((g.M * (g.N / 8) + 255) / 256), dim3(256), 0, stream, g, how.splits, part);
+    const dim3 grid((g.M * (g.N / 4) + 255) / 256), block(256);
+    if (how.splits <= 2)
+        hipLaunchKernelGGL(fp8_join_kernel<2>, grid, block, 0, stream, g, how.splits, part);
+    else if (how.splits <= 4)
+        hipLaunchKernelGGL(fp8_join_kernel<4>, grid, block, 0, stream, g, how.splits, part);
+    else
+        hipLaunchKernelGGL(fp8_join_kernel<8>, grid, block, 0, stream, g, how.splits, part);
     return hipGetLastError();
 }
 
