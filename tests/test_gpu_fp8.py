@@ -364,3 +364,15 @@ def test_output_over_its_residual(M, K, N):
     want = host(site.gemm(codes, scales, M, residual=residual))
     y = residual.clone()
     assert np.array_equal(host(site.gemm(codes, scales, M, residual=y, y=y)), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(33, 264, 384), (47, 1024, 640), (64, 2048, 256), (65, 512, 1152), (100, 1024, 384),
+                                   (128, 512, 2176), (255, 256, 512), (300, 64, 128), (1000, 24, 384)])
+def test_many_tokens_of_narrow_layers(M, N, K):
+    """More than 32 tokens that the GEMV may take, in tiles of 16 or 32, the last one ragged."""
+    rng = np.random.default_rng(M + N + K)
+    qa, sa, qw, sw = rand_site(rng, M, N, K)
+    bias, residual = rng.standard_normal(N).astype(np.float32), ref.bf16(rng, M, N)
+    y, tol = ref.fp8_gemm(qa, sa, qw, sw, bias, residual)
+    ref.assert_gemm(run_gemm(qa, sa, qw, sw, bias, residual), y, tol, f"gemm {M}x{N}x{K}")
+    ref.assert_gemm(run_gemm(qa, sa, qw, sw, bias, residual, head_dim=8), y, tol, f"gemm {M}x{N}x{K} heads")

@@ -472,19 +472,19 @@ int fp8_tile_id(const char* name) {
 
 // Estimates (us) that choose between the GEMV, the GEMM and the GEMM with K in
 // parts.  All stream the weights, at 5.1 TB/s; the GEMV reads the codes again from
-// L2 for every 16 weight rows (8 TB/s in all, less where row groups are fewer than
-// CUs; a second tile of 16 tokens then runs beside the first); the GEMM takes its
-// rounds of tiles; parts of K are written, read and joined by a launch more.
+// L2 for every 16 weight rows (8 TB/s in all, less where workgroups are fewer than
+// CUs); the GEMM takes its rounds of tiles; parts of K are written, read and joined by a launch more.
 namespace {
 constexpr float kCopyRate = 5.1f, kReadRate = 8.0f;  // MB per us
 
 float weights_us(const Fp8Args& g) { return float(g.N) * float(g.K) * 1e-6f / kCopyRate; }
 float larger(float a, float b) { return a > b ? a : b; }
 
-float gemv_us(const Fp8Args& g, const DeviceInfo& dev) {
-    const int groups = (g.N + 15) / 16, rows = 2 * groups <= dev.cus && g.M > 16 ? 16 : g.M;
+float gemv_us(const Fp8Args& g, const DeviceInfo& dev) {  // (of a call that it takes)
+    const int tokens = fp8_gemv_tokens(g.M, g.N, dev.cus);
+    const int groups = (g.N + 15) / 16 * ((g.M + tokens - 1) / tokens), read = g.M < tokens ? g.M : tokens;
     const float fill = groups < dev.cus ? float(groups) / float(dev.cus) : 1.0f;
-    const float bytes = (float(g.N) + float(groups) * float(rows)) * float(g.K) * 1e-6f;
+    const float bytes = float(groups) * float(16 + read) * float(g.K) * 1e-6f;
     return 2.5f + larger(bytes / (kReadRate * fill), weights_us(g));
 }
 float gemm_us(const Fp8Args& g, const DeviceInfo& dev) {
@@ -513,8 +513,9 @@ float split_us(const Fp8Args& g, int splits, int edge) {
 //   K = 8192, N = 8192: 18.7 / 22.0 with 16, 25.7 / 23.9 with 32
 //   K = 16384, N = 2048: 16.8 / 35.2 with 16, 16.7 / 35.4 with 32
 //   K = 1024, N = 16384: 5.6 / 6.5 with 8, 8.4 / 6.8 with 32
+//   K = 3584, N = 1024: 5.4 / 10.9 with 64, 7.1 / 10.9 with 128
 bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev) {
-    if (g.M > kGemvMaxM || hooks().fp8_tile.load(std::memory_order_relaxed) >= 0) return false;
+    if (!fp8_gemv_tokens(g.M, g.N, dev.cus) || hooks().fp8_tile.load(std::memory_order_relaxed) >= 0) return false;
     return gemv_us(g, dev) <= gemm_us(g, dev);
 }
 
@@ -527,7 +528,7 @@ Fp8Split fp8_split(const Fp8Args& g, const DeviceInfo& dev) {
     if (hooks().fp8_tile.load(std::memory_order_relaxed) >= 0 || !fp8_may_split(g.M, g.K)) return Fp8Split{1, 0};
     Fp8Split best{1, 0};
     float least = gemm_us(g, dev);
-    if (g.M <= kGemvMaxM && gemv_us(g, dev) < least) least = gemv_us(g, dev);
+    if (fp8_gemv_tokens(g.M, g.N, dev.cus) && gemv_us(g, dev) < least) least = gemv_us(g, dev);
     for (int edge = 64; edge <= 128; edge += 64) {
         const int splits = parts_of(g, dev, edge);
         const float us = split_us(g, splits, edge);

@@ -1,5 +1,5 @@
-// FP8 sites for decode-sized M (at most 32 tokens): the weight-streaming GEMV
-// that reads the tokens' codes from L2.
+// FP8 sites for decode-sized M (at most 32 tokens, more for narrow layers): the
+// weight-streaming GEMV that reads the tokens' codes from L2.
 //
 // Bound by reading the weight codes once.  S waves of a workgroup share the K
 // range of a group of 16 weight rows, in units of 128 (one scale group): per
@@ -98,18 +98,18 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_gemv_kernel(Fp8Args g, int pe
     }
 }
 
-// More than 16 tokens: both tiles in one workgroup share its weights, two
-// workgroups where that only fills idle CUs (K = 16384, N = 2048, 23 tokens: 16.7 us
+// More than 16 tokens: two tiles of 16 in one workgroup share its weights; one tile
+// each where that only fills idle CUs (K = 16384, N = 2048, 23 tokens: 16.7 us
 // against 21.0; K = N = 4096: 9.1 against 7.4).
 template <int S, int C>
 hipError_t launch_c(const Fp8Args& g, const DeviceInfo& dev, int per, hipStream_t st) {
     constexpr int rows = 16 * (kWaves / S);
-    const int blocks = (g.N + rows - 1) / rows, tiles = (g.M + 15) / 16;
+    const int blocks = (g.N + rows - 1) / rows;
     const dim3 block(64 * kWaves);
-    if (tiles == 1 || 2 * ((g.N + 15) / 16) <= dev.cus)
-        hipLaunchKernelGGL((fp8_gemv_kernel<1, S, C>), dim3(blocks, tiles), block, 0, st, g, per);
+    if (fp8_gemv_tokens(g.M, g.N, dev.cus) == 16)
+        hipLaunchKernelGGL((fp8_gemv_kernel<1, S, C>), dim3(blocks, (g.M + 15) / 16), block, 0, st, g, per);
     else
-        hipLaunchKernelGGL((fp8_gemv_kernel<2, S, C>), dim3(blocks), block, 0, st, g, per);
+        hipLaunchKernelGGL((fp8_gemv_kernel<2, S, C>), dim3(blocks, (g.M + 31) / 32), block, 0, st, g, per);
     return hipGetLastError();
 }
 
@@ -128,7 +128,7 @@ hipError_t launch_s(const Fp8Args& g, const DeviceInfo& dev, hipStream_t st) {
 // N = 32768: 22.6 us with 8, 14.0 with 4, 15.5 with 2; K = 1024, N = 16384: 9.2, 7.2,
 // 5.2; K = 3584, N = 37888: 26.0, 29.0, 33.9; K = 896, N = 1024: 3.5, 4.1, 4.3).
 hipError_t launch_fp8_gemv(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream) {
-    if (g.M > kGemvMaxM) return hipErrorInvalidValue;
+    if (!fp8_gemv_tokens(g.M, g.N, dev.cus)) return hipErrorInvalidValue;
     const int nu = g.K / 128, groups = (g.N + 15) / 16;
     if (nu > 16 || groups <= dev.cus) return launch_s<8>(g, dev, stream);
     if (nu > 8) return launch_s<4>(g, dev, stream);

@@ -176,9 +176,17 @@ constexpr int kSplitTiles = 256, kSplitEdge = 128;
 struct Fp8Split {
     int splits, edge;
 };
+// (shorter K gained nothing: K = N = 3584 with 64 tokens 13.9 us in parts, 14.0 whole)
 inline bool fp8_may_split(int32_t M, int32_t K) { return M > 1 && K >= 4096; }
 Fp8Split fp8_split(const Fp8Args& g, const DeviceInfo& dev);
 hipError_t launch_fp8_split(const Fp8Args& g, Fp8Split how, float* part, hipStream_t stream);
+// Tokens of a GEMV workgroup: 16, or 32, which share its weights; 0 where it takes no
+// call.  More than 32 tokens need workgroups for all of them at once.
+inline int fp8_gemv_tokens(int32_t M, int32_t N, int cus) {
+    const int64_t groups = (int64_t(N) + 15) / 16;
+    if (M <= 16 || groups * ((M + 15) / 16) <= cus) return 16;
+    return M <= 32 || groups * ((M + 31) / 32) <= cus ? 32 : 0;
+}
 bool fp8_gemv_takes(const Fp8Args& g, const DeviceInfo& dev);
 hipError_t launch_fp8_gemv(const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
 // A few tokens with their prologue in one launch (fq_fp8_decode.hip), and whether it takes a call.
