@@ -79,6 +79,7 @@ def test_fp8_sizes():
     assert fq.fq_fp8_linear_workspace_bytes(3, 256) == 768 + 256
     assert fq.fq_fp8_linear_workspace_bytes(70000, 65536) >= 70000 * 65536  # past 32 bits
     assert fq.fq_fp8_linear_workspace_bytes(3, 200) == 0
+    assert fq.fq_fp8_ascale_count(2 ** 31 - 513, 128) == 2 ** 31 - 512 and fq.fq_fp8_ascale_count(2 ** 31 - 512, 128) == 0
 
 
 def test_fp8_workspace_has_room_for_parts():

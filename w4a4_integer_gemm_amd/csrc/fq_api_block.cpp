@@ -14,6 +14,7 @@
 namespace {
 
 constexpr int64_t kMaxThreads = int64_t(1) << 32;  // of one launch, along x
+constexpr int32_t kMaxM = INT32_MAX - 512;         // (rounded up to whole tiles it is an int32 still)
 
 fq_status check_eps(const char* fn, const char* name, float eps) {
     if (!(eps >= 0.0f && eps < 1e30f))
@@ -49,7 +50,7 @@ fq_status check_norm_launch(const char* fn, int32_t M, int32_t K, bool f32) {
 size_t scale_bytes(int32_t M, int32_t K) { return size_t(K / 128) * size_t(fq::fp8_scale_ld(M)) * sizeof(float); }
 
 fq_status check_m(const char* fn, int32_t M) {
-    if (M < 1 || M > INT32_MAX - 4) return fail(FQ_ERR_SHAPE, fmt("%s: M=%d must be >= 1 and < 2^31 - 4", fn, M));
+    if (M < 1 || M > kMaxM) return fail(FQ_ERR_SHAPE, fmt("%s: M=%d must be in [1, %d]", fn, M, kMaxM));
     return FQ_OK;
 }
 
@@ -126,7 +127,7 @@ fq_status run_fp8_gemm(const char* fn, const fq::Fp8Args& g, const fq::DeviceInf
 extern "C" {
 
 size_t fq_fp8_ascale_count(int32_t M, int32_t K) {
-    if (M < 1 || M > INT32_MAX - 4 || K < 128 || K > kMaxK || K % 128) return 0;
+    if (M < 1 || M > kMaxM || K < 128 || K > kMaxK || K % 128) return 0;
     return scale_bytes(M, K) / sizeof(float);
 }
 
