@@ -8,16 +8,29 @@
 
 namespace fq {
 
-// Sum over the workgroup; every thread gets the same value.  `red` is used by
-// one call only (no barrier separates two uses).
+// Sum over the workgroup (of at most 16 waves) in the order of its waves; every
+// thread gets the same value.  `red` has 16 entries and is used by one call only
+// (no barrier separates two uses).  Up to 4 or 8 waves the entries past the last
+// hold 0 and all reads go out at once (one row of 2048 with both norms 3.06 us,
+// 3.26 with a read after the other; rows of 16 waves took 0.1 us longer that way).
+template <int N>
+__device__ __forceinline__ double sum_entries(const double* red) {
+    double v = red[0];
+#pragma unroll
+    for (int w = 1; w < N; ++w) v += red[w];
+    return v;
+}
 __device__ __forceinline__ double block_sum(double v, int nwaves, double* red) {
     v = wave_sum(v);
-    if (nwaves > 1) {
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.0;
-        for (int w = 0; w < nwaves; ++w) v += red[w];
-    }
+    if (nwaves == 1) return v;
+    const int t = threadIdx.x;
+    if ((t & 63) == 0) red[t >> 6] = v;
+    if (t >= nwaves && t < 8) red[t] = 0.0;
+    __syncthreads();
+    if (nwaves <= 4) return sum_entries<4>(red);
+    if (nwaves <= 8) return sum_entries<8>(red);
+    v = 0.0;
+    for (int w = 0; w < nwaves; ++w) v += red[w];
     return v;
 }
 
