@@ -376,3 +376,15 @@ def test_many_tokens_of_narrow_layers(M, N, K):
     y, tol = ref.fp8_gemm(qa, sa, qw, sw, bias, residual)
     ref.assert_gemm(run_gemm(qa, sa, qw, sw, bias, residual), y, tol, f"gemm {M}x{N}x{K}")
     ref.assert_gemm(run_gemm(qa, sa, qw, sw, bias, residual, head_dim=8), y, tol, f"gemm {M}x{N}x{K} heads")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 72, 4224), (1, 264, 8192), (2, 136, 5120), (3, 40, 5248), (1, 24, 16384), (2, 16, 8192),
+                                   (1, 4104, 4352), (1, 8, 32768), (1, 8, 32896), (4, 24, 4224), (3, 16, 8192)])
+def test_few_tokens_of_long_sums(M, N, K):
+    """A few tokens' codes through LDS where K is long, and the calls beside that choice."""
+    rng = np.random.default_rng(M + N + K)
+    qa, sa, qw, sw = rand_site(rng, M, N, K)
+    bias, residual = rng.standard_normal(N).astype(np.float32), ref.bf16(rng, M, N)
+    y, tol = ref.fp8_gemm(qa, sa, qw, sw, bias, residual)
+    ref.assert_gemm(run_gemm(qa, sa, qw, sw, bias, residual), y, tol, f"gemm {M}x{N}x{K}")
+    ref.assert_gemm(run_gemm(qa, sa, qw, sw, bias, residual, head_dim=8), y, tol, f"gemm {M}x{N}x{K} heads")

@@ -118,6 +118,7 @@ fq::NormArgs prologue_args(const void* x, int32_t M, int32_t K, int64_t ldx, con
 }
 
 fq_status run_fp8_gemm(const char* fn, const fq::Fp8Args& g, const fq::DeviceInfo& dev, hipStream_t stream) {
+    if (fq::fp8_decode_codes_takes(g)) return device_status(fn, fq::launch_fp8_decode_codes(g, stream));
     return device_status(fn, fq::fp8_gemv_takes(g, dev) ? fq::launch_fp8_gemv(g, dev, stream)
                                                         : fq::launch_fp8_gemm(g, dev, stream));
 }

@@ -2,6 +2,8 @@
 // weight-streaming GEMV fused, so that the tokens' quantisation overlaps the
 // weight stream instead of preceding it.
 //
+// (fq_fp8_gemm runs the same kernel from codes where K is long.)
+//
 // Every workgroup quantises the tokens itself, with the prologue's arithmetic in
 // the prologue's order (pieces of 8 values, 64 consecutive ones of a token to a
 // wave; fq_row_norm.h, fq_fp8.h: the same codes bit for bit), while its weight
@@ -35,11 +37,15 @@ constexpr int kSpan = kWaves * 64 * 8;  // values in one piece of every lane
 // Waves of 64 pieces that hold one token.
 __host__ __device__ inline int token_waves(int K) { return (K + 511) / 512; }
 
+// What the tokens come as: rows to quantise, rows to normalise and quantise, codes.
+constexpr int kRows = 0, kNorm = 1, kCodes = 2;
+
 // S waves share the K range of each of the 8 / S sets of R row groups; MT tiles
 // of 16 tokens; P pieces per lane: piece j of wave w is wave v = 8 j + w of all
 // tokens' waves, token v / token_waves(K); C units requested at once.
-template <bool NORM, int MT, int S, int R, int P, int C>
+template <int SRC, int MT, int S, int R, int P, int C>
 __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(NormArgs p, Fp8Args g, double rk) {
+    constexpr bool NORM = SRC == kNorm;
     constexpr int G = kWaves / S;
     __shared__ double red_d[kWaves * (NORM ? P : 1)];
     __shared__ __attribute__((aligned(16))) uint8_t codes[kSpan * P];
@@ -65,7 +71,13 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(NormArgs p, Fp8
         on[j] = tok[j] < g.M && k[j] < K;
         if (!on[j]) k[j] = 0;
         if (tok[j] >= g.M) tok[j] = 0;
-        xr[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.r_in) + tok[j] * p.ld_rin + k[j]);
+        if constexpr (SRC == kCodes) {
+            const uint2 c = *reinterpret_cast<const uint2*>(g.act + int64_t(tok[j]) * K + k[j]);
+            const float s = g.act_scale[int64_t(k[j] / 128) * fp8_scale_ld(g.M) + tok[j]];
+            xr[j] = make_uint4(c.x, c.y, __float_as_uint(s), 0);
+        } else {
+            xr[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.r_in) + tok[j] * p.ld_rin + k[j]);
+        }
     }
     if constexpr (NORM) {
 #pragma unroll
@@ -116,6 +128,14 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(NormArgs p, Fp8
     }
 #pragma unroll
     for (int j = 0; j < P; ++j) {
+        if constexpr (SRC == kCodes) {
+            if (on[j]) {
+                const int u = k[j] / 128;
+                *reinterpret_cast<uint2*>(codes + slot(tok[j], u, (k[j] / 16) & 7) + (k[j] & 8)) = make_uint2(xr[j].x, xr[j].y);
+                if ((lane & 15) == 0) scales[u * g.M + tok[j]] = __uint_as_float(xr[j].z);
+            }
+            continue;
+        }
         float h[8];
         unpack8(xr[j], h);
         if constexpr (NORM) {
@@ -194,42 +214,49 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(NormArgs p, Fp8
         }
 }
 
-template <bool NORM, int MT, int S, int R, int P, int C>
+template <int SRC, int MT, int S, int R, int P, int C>
 hipError_t launch(const NormArgs& p, const Fp8Args& g, hipStream_t st) {
     constexpr int rows = 16 * R * (kWaves / S);
-    hipLaunchKernelGGL((fp8_decode_kernel<NORM, MT, S, R, P, C>), dim3((g.N + rows - 1) / rows), dim3(64 * kWaves), 0,
-                       st, p, g, 1.0 / double(p.K));
+    hipLaunchKernelGGL((fp8_decode_kernel<SRC, MT, S, R, P, C>), dim3((g.N + rows - 1) / rows), dim3(64 * kWaves), 0,
+                       st, p, g, 1.0 / double(g.K));
     return hipGetLastError();
 }
 
+// K beyond four units a wave: three units at a time where that requests fewer past
+// a wave's share, as in the GEMV (fq_fp8_gemv.hip).
+template <int SRC, int P>
+hipError_t launch_long(const NormArgs& p, const Fp8Args& g, hipStream_t st) {
+    const int per = (g.K / 128 + kWaves - 1) / kWaves;
+    return (per + 2) / 3 * 3 < (per + 3) / 4 * 4 ? launch<SRC, 1, 8, 1, P, 3>(p, g, st)
+                                                 : launch<SRC, 1, 8, 1, P, 4>(p, g, st);
+}
+
 // One row group a workgroup where there is at most one for each CU, else two; S
-// and C as in the GEMV (fq_fp8_gemv.hip).
-template <bool NORM, int MT, int P>
+// as in the GEMV.
+template <int SRC, int MT, int P>
 hipError_t launch_p(const NormArgs& p, const Fp8Args& g, const DeviceInfo& dev, hipStream_t st) {
     const int nu = g.K / 128, groups = (g.N + 15) / 16, per = (nu + kWaves - 1) / kWaves;
-    if constexpr (P > 1 && MT == 1) {  // (one piece per lane, or more than 16 tokens: short K)
-        const bool three = (per + 2) / 3 * 3 < (per + 3) / 4 * 4;
-        if (per > 4) return three ? launch<NORM, MT, 8, 1, P, 3>(p, g, st) : launch<NORM, MT, 8, 1, P, 4>(p, g, st);
-    }
+    if constexpr (P > 1 && MT == 1)  // (one piece per lane, or more than 16 tokens: short K)
+        if (per > 4) return launch_long<SRC, P>(p, g, st);
     if constexpr (P > 4) return hipErrorInvalidValue;  // (one token of more than 16384 values)
     if constexpr (MT == 1 && P <= 4) {
-        if (groups > dev.cus && nu > 16) return launch<NORM, MT, 8, 2, P, 4>(p, g, st);
-        if (groups > dev.cus && nu > 8) return launch<NORM, MT, 4, 2, P, 4>(p, g, st);
+        if (groups > dev.cus && nu > 16) return launch<SRC, MT, 8, 2, P, 4>(p, g, st);
+        if (groups > dev.cus && nu > 8) return launch<SRC, MT, 4, 2, P, 4>(p, g, st);
     }
     if constexpr (P <= 4) {
-        if (groups > dev.cus) return launch<NORM, MT, 2, 2, P, 4>(p, g, st);
-        return launch<NORM, MT, 8, 1, P, 4>(p, g, st);
+        if (groups > dev.cus) return launch<SRC, MT, 2, 2, P, 4>(p, g, st);
+        return launch<SRC, MT, 8, 1, P, 4>(p, g, st);
     }
 }
 
-template <bool NORM>
+template <int SRC>
 hipError_t launch_n(const NormArgs& p, const Fp8Args& g, const DeviceInfo& dev, hipStream_t st) {
     const int waves = g.M * token_waves(g.K);
-    if (waves <= 8) return launch_p<NORM, 1, 1>(p, g, dev, st);
-    if (waves <= 16) return launch_p<NORM, 1, 2>(p, g, dev, st);
-    if constexpr (!NORM) {
-        if (waves <= 32) return g.M > 16 ? launch_p<NORM, 2, 4>(p, g, dev, st) : launch_p<NORM, 1, 4>(p, g, dev, st);
-        return launch_p<NORM, 1, 8>(p, g, dev, st);
+    if (waves <= 8) return launch_p<SRC, 1, 1>(p, g, dev, st);
+    if (waves <= 16) return launch_p<SRC, 1, 2>(p, g, dev, st);
+    if constexpr (SRC == kRows) {
+        if (waves <= 32) return g.M > 16 ? launch_p<SRC, 2, 4>(p, g, dev, st) : launch_p<SRC, 1, 4>(p, g, dev, st);
+        return launch_p<SRC, 1, 8>(p, g, dev, st);
     }
     return hipErrorInvalidValue;
 }
@@ -250,7 +277,24 @@ bool fp8_decode_takes(const NormArgs& p, const Fp8Args& g) {
 
 hipError_t launch_fp8_decode(const NormArgs& p, const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream) {
     if (!fp8_decode_takes(p, g)) return hipErrorInvalidValue;
-    return p.pre_norm ? launch_n<true>(p, g, dev, stream) : launch_n<false>(p, g, dev, stream);
+    return p.pre_norm ? launch_n<kNorm>(p, g, dev, stream) : launch_n<kRows>(p, g, dev, stream);
+}
+
+// From codes the LDS copy is worth its barrier where K is long: one token K = 5120,
+// N = 5120 8.4 us against 9.4 with the codes read from L2, K = 18944, N = 3584 15.4
+// against 17.7, two tokens 5120 x 5120 8.8 against 9.7; K = 2048, N = 8192 6.5 against
+// 5.2.
+bool fp8_decode_codes_takes(const Fp8Args& g) {
+    if (g.K <= kSpan || g.M > 16 || hooks().fp8_tile.load(std::memory_order_relaxed) >= 0) return false;
+    return g.M * token_waves(g.K) <= (g.M > 1 ? 32 : 64);
+}
+
+hipError_t launch_fp8_decode_codes(const Fp8Args& g, hipStream_t stream) {
+    if (!fp8_decode_codes_takes(g)) return hipErrorInvalidValue;
+    const int waves = g.M * token_waves(g.K);
+    const NormArgs none{};
+    if (waves <= 16) return launch_long<kCodes, 2>(none, g, stream);
+    return waves <= 32 ? launch_long<kCodes, 4>(none, g, stream) : launch_long<kCodes, 8>(none, g, stream);
 }
 
 }  // namespace fq

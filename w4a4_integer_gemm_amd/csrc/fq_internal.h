@@ -192,6 +192,9 @@ hipError_t launch_fp8_gemv(const Fp8Args& g, const DeviceInfo& dev, hipStream_t 
 // A few tokens with their prologue in one launch (fq_fp8_decode.hip), and whether it takes a call.
 bool fp8_decode_takes(const NormArgs& p, const Fp8Args& g);
 hipError_t launch_fp8_decode(const NormArgs& p, const Fp8Args& g, const DeviceInfo& dev, hipStream_t stream);
+// The same from codes.
+bool fp8_decode_codes_takes(const Fp8Args& g);
+hipError_t launch_fp8_decode_codes(const Fp8Args& g, hipStream_t stream);
 
 // Rotary positions (fq_rope.hip).
 struct RopeArgs {
