@@ -15,8 +15,8 @@
 // the partial tiles meet in LDS.
 //
 // Measured (us, this launch / the two; one token): K = 3584, N = 37888 with the
-// norm 26.8 / 29.2, K = 3584, N = 4608 6.7 / 10.2, K = 8192, N = 14336 27.1 / 29.0,
-// without the norm 24.3 / 27.4; K = 16384, N = 2048 without 11.4 / 14.1.  One row
+// norm 26.7 / 29.2, K = 3584, N = 4608 6.8 / 9.6, K = 8192, N = 14336 27.1 / 28.2,
+// without the norm 24.4 / 26.6; K = 16384, N = 2048 without 11.4 / 12.6.  One row
 // group a workgroup instead of two: 27.7 at N = 37888, 6.5 against 6.2 at N =
 // 6144; below one group for each CU the other way round (K = 896, N = 1024: 3.8
 // against 5.3).
@@ -265,9 +265,9 @@ hipError_t launch_n(const NormArgs& p, const Fp8Args& g, const DeviceInfo& dev, 
 
 // By the pieces that every workgroup quantises, and one token always.  Measured
 // (us, this launch / the two): with the norm and two pieces per lane 2 x 3584 x
-// 37888 29.1 / 29.7, 4 x 2048 x 8192 8.1 / 8.5, 16 x 256 x 512 4.9 / 5.0; with four
+// 37888 29.0 / 29.4, 4 x 2048 x 8192 8.1 / 8.5, 16 x 256 x 512 4.9 / 5.0; with four
 // 4 x 3584 x 37888 48.6 / 30.7, 16 x 896 x 1024 7.0 / 6.4, 2 x 8192 x 8192 17.7 /
-// 19.4.  Without it and four 4 x 3584 x 37888 28.6 / 29.7, 16 x 896 x 1024 4.9 / 5.9.  (With the norm beyond 8192
+// 18.8.  Without it and four 4 x 3584 x 37888 28.7 / 29.9, 16 x 896 x 1024 4.9 / 5.9.  (With the norm beyond 8192
 // values the order of the prologue's sum is another.)
 bool fp8_decode_takes(const NormArgs& p, const Fp8Args& g) {
     if (g.M > kGemvMaxM || hooks().fp8_tile.load(std::memory_order_relaxed) >= 0) return false;
