@@ -89,8 +89,8 @@ struct Fp8Cfg {
 // (v_readfirstlane, or v_readlane of a spilled register), which the compiler
 // does not see being read by a memory instruction here, and the M0 write.
 //
-// 16 bytes from a buffer descriptor at voff + soff; what lies past its end
-// reads as zero.
+// 16 bytes from a buffer descriptor at voff + soff; a lane whose voff lies past
+// the descriptor's end reads zero (soff need not be part of that check).
 __device__ __forceinline__ void copy16_buffer(const v4i& rsrc, uint32_t voff, uint32_t soff, uint32_t lds_dst) {
     asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                  :
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
     // fills the slot of row 8 c + l / 8, chunk (l % 8) ^ swizzle (the same for
     // every c: the swizzle has period 16 rows, a wave's copies are 8 CW apart).
     // Rows past M or N read as zeros (their results are not stored).
-    const uint32_t voff = uint32_t((lane >> 3) * g.K + 16 * ((lane & 7) ^ fp8_swizzle(8 * (cw & 1) + (lane >> 3))));
+    const uint32_t copy_lane = fp8_copy_lane(lane, cw & 1, g.K);
     uint32_t sc_off = 0;
     v4i ra{}, rw{};
     const uint8_t* psc = nullptr;
@@ -190,8 +190,8 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
     auto copy_part = [&](int i) {
         const int c = chunk(i);
         const bool act = CF::EVEN ? i < CF::BM / 8 / CF::CW : 8 * c < CF::BM;
-        const uint32_t soff = uint32_t((8 * c - (act ? 0 : CF::BM)) * g.K + 128 * ((SPLIT ? copy_u0 : 0) + copy_s));
-        copy16_buffer(act ? ra : rw, voff, soff, copy_dst + c * 1024);
+        const Fp8CopyOffset at = fp8_copy_at(copy_lane, 8 * c - (act ? 0 : CF::BM), (SPLIT ? copy_u0 : 0) + copy_s, g.K);
+        copy16_buffer(act ? ra : rw, at.lane, at.common, copy_dst + c * 1024);
     };
     auto copy_scales = [&]() {
         if (cw == 0)
@@ -216,6 +216,7 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(CF:
         } else {
             ra[2] = 0;
             rw[2] = 0;
+            copy_u0 = 0;  // (the wave's offset is zero too: no lane is in range of no bytes)
         }
     };
     // Waits until all but the newest k stages of this wave's copies have landed

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "fq_device.h"
+#include "fq_fp8_copy.h"
 #include "fq_internal.h"
 
 namespace fq {
@@ -26,8 +27,6 @@ __device__ __forceinline__ v4f mfma_e4m3(const v8i& w, const v8i& a, const v4f& 
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, 0, 0, 0, 0, 0);
 }
 
-// LDS layout of a 128-byte row rho: chunk c of 16 bytes at slot 8 rho + (c ^ swizzle).
-__device__ __forceinline__ int fp8_swizzle(int rho) { return (rho >> 1) & 7; }
 // Byte offset of chunk q (0 .. 3) of a row; chunk q + 4 is at this offset ^ 64
 // (the swizzle flips bits of the chunk number).
 __device__ __forceinline__ uint32_t fp8_slot(int rho, int q) {
