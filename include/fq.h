@@ -310,7 +310,9 @@ fq_status fq_fp8_prologue(const void* x_bf16, int32_t M, int32_t K, int64_t ldx,
 
 /* Device: the GEMM and its epilogue.  head_dim 0: y is [M][ldy]; a positive
  * multiple of 8 dividing N: y is [N / head_dim][M][head_dim] (ldy unused).
- * y may be the residual (with equal strides), other overlaps are not allowed. */
+ * y may be the residual in the same layout (equal strides, or one head of N values
+ * and ldr = N); over a residual of another layout the call is refused (FQ_ERR_SHAPE),
+ * and other overlaps are not allowed. */
 fq_status fq_fp8_gemm(const void* act_codes, const float* act_scale, int32_t M, const void* w_codes,
                       const float* wscale, int32_t N, int32_t K, const float* bias, const void* residual_bf16,
                       int64_t ldr, int32_t head_dim, void* y_bf16, int64_t ldy, void* stream);
@@ -321,7 +323,7 @@ fq_status fq_fp8_gemm(const void* act_codes, const float* act_scale, int32_t M, 
  * it holds the codes and, at the next 256-byte boundary, the scales after the
  * call (from 2 tokens and K = 4096 on 16 MiB more, for partial sums of layers of
  * few tiles), and belongs to one call at a time.  y may be the residual
- * (with equal strides); it overlaps neither x nor the workspace. */
+ * as in fq_fp8_gemm; it overlaps neither x nor the workspace. */
 size_t fq_fp8_linear_workspace_bytes(int32_t M, int32_t K);
 fq_status fq_fp8_linear(const void* x_bf16, int32_t M, int32_t K, int64_t ldx, const float* gamma, float eps,
                         const void* w_codes, const float* wscale, int32_t N, const float* bias,

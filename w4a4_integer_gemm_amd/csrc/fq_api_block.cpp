@@ -94,6 +94,10 @@ fq_status validate_fp8_gemm(const char* fn, const void* act, const float* act_sc
     else
         FQ_TRY(check_vector(fn, "y_bf16", y));
     if (residual) FQ_TRY(check_rows(fn, "residual_bf16", "ldr", residual, ldr, N, 8));
+    // y over the residual: each output has to replace the value that it adds (one token has one layout)
+    if (residual == y && M > 1 && (head_dim == 0 ? ldr != ldy : head_dim != N || ldr != N))
+        return fail(FQ_ERR_SHAPE, fmt("%s: y_bf16 is residual_bf16 in another layout (M=%d, ldr=%lld, ldy=%lld, head_dim=%d)",
+                                      fn, M, (long long)ldr, (long long)ldy, head_dim));
     FQ_TRY(check_vector(fn, "act_codes", act));
     FQ_TRY(check_vector(fn, "act_scale", act_scale));
     FQ_TRY(check_vector(fn, "w_codes", w));
