@@ -23,6 +23,29 @@ def _to_dev(a: Optional[np.ndarray], device):
     return torch.from_numpy(a).to(device)
 
 
+def _bf16_types():
+    """What holds bf16 values: the type itself, or its bits."""
+    import torch
+    return torch.bfloat16, torch.int16, torch.uint16
+
+
+def _rows(site, t, name: str, rows: int, cols: int, exact: bool = False) -> int:
+    """The row stride of t, bf16 rows of contiguous values on the site's device, at least
+    rows x cols of them (exactly cols with `exact`): what the C ABI takes its pointer for."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype not in site._bf16:
+        raise ValueError(f"{name} has dtype {t.dtype}, not bfloat16 (or its bits as int16 or uint16)")
+    if len(shape) != 2:
+        raise ValueError(f"{name} has {len(shape)} dimensions, not 2")
+    if shape[0] < rows or shape[1] < cols or (exact and shape[1] != cols):
+        raise ValueError(f"{name} is {shape[0]} x {shape[1]}, not {rows} x {cols}")
+    if stride[1] != 1:
+        raise ValueError(f"{name} has stride {stride[1]} along its rows, not 1")
+    if t.device != site.device:
+        raise ValueError(f"{name} is on {t.device}, the site on {site.device}")
+    return stride[0]
+
+
 class DeviceSite:
     """One linear site: x [M][K] bf16 -> y [M][N] bf16.
 
@@ -145,6 +168,11 @@ class Fp8Site:
     checkpoint stores them (numpy arrays, or torch tensors already on the
     device); gamma: RMSNorm gain (None for a quant-only site).
 
+    Tensors hold bf16 or its bits (int16, uint16); x is M x K, a residual or an output
+    given for the row layout has M rows and N columns or more, one given for the head
+    layout is [N / head_dim][M][head_dim], contiguous.  All are on the site's device,
+    which is the current one; ValueError otherwise.
+
     linear() uses the site's own workspace, which belongs to one call at a time: calls
     on two streams at once take two sites (of the same codes and wscale).  A
     workspace that grew leaves the one before allocated, since a captured graph may
@@ -153,13 +181,18 @@ class Fp8Site:
     def __init__(self, W: Optional[np.ndarray] = None, gamma=None, bias=None, eps: float = 1e-6, device="cuda",
                  codes=None, wscale=None):
         import torch
-        self.device = torch.device(device)
         self.eps = float(eps)
+        self._bf16 = _bf16_types()
         if codes is None:
             codes, wscale = B.fq_fp8_pack_weights(W)
+        if wscale is None or len(codes.shape) != 2:
+            raise ValueError("codes are a matrix and come with wscale")
         self.N, self.K = codes.shape
-        self.codes = codes if isinstance(codes, torch.Tensor) else _to_dev(codes, self.device)
+        self.codes = codes if isinstance(codes, torch.Tensor) else _to_dev(codes, torch.device(device))
+        self.device = self.codes.device
         self.wscale = wscale if isinstance(wscale, torch.Tensor) else _to_dev(np.asarray(wscale, np.float32), self.device)
+        if self.wscale.device != self.device:
+            raise ValueError(f"wscale is on {self.wscale.device}, codes on {self.device}")
         if not (self.codes.is_contiguous() and self.wscale.is_contiguous()):
             raise ValueError("codes and wscale must be contiguous")
         if self.codes.element_size() != 1 or self.wscale.dtype != torch.float32:
@@ -167,6 +200,9 @@ class Fp8Site:
         if self.wscale.numel() != B.fq_fp8_wscale_count(self.N, self.K):
             raise ValueError(f"wscale has {self.wscale.numel()} values, not {B.fq_fp8_wscale_count(self.N, self.K)} "
                              f"for N={self.N} K={self.K}")
+        for name, v, n in (("gamma", gamma, self.K), ("bias", bias, self.N)):
+            if v is not None and np.shape(v) != (n,):
+                raise ValueError(f"{name} has shape {np.shape(v)}, not ({n},)")
         self.gamma = _to_dev(None if gamma is None else np.ascontiguousarray(gamma, np.float32), self.device)
         self.bias = _to_dev(None if bias is None else np.ascontiguousarray(bias, np.float32), self.device)
         self._ws = None
@@ -205,28 +241,67 @@ class Fp8Site:
         shape = (self.N // head_dim, M, head_dim) if head_dim else (M, self.N)
         return torch.empty(shape, dtype=torch.int16, device=self.device)
 
+    # -- checks
+    def _check_device(self):
+        import torch
+        if self.device.index is not None and torch.cuda.current_device() != self.device.index:
+            raise ValueError(f"the site is on {self.device}, the current device is {torch.cuda.current_device()}")
+
+    def _check_codes(self, codes, scales, M: int):
+        import torch
+        if codes.element_size() != 1 or codes.shape != (M, self.K) or not codes.is_contiguous():
+            raise ValueError(f"codes are {M} x {self.K} bytes, contiguous, not {tuple(codes.shape)} of {codes.dtype}")
+        ld = -(-M // 4) * 4
+        if (scales.dtype != torch.float32 or scales.dim() != 2 or scales.shape[0] != self.K // 128 or scales.shape[1] < M
+                or scales.stride() != (ld, 1)):
+            raise ValueError(f"scales are float32 {self.K // 128} x {M} in rows of {ld}, not {tuple(scales.shape)} of "
+                             f"{scales.dtype} with strides {scales.stride()}")
+        if codes.device != self.device or scales.device != self.device:
+            raise ValueError(f"codes are on {codes.device} and scales on {scales.device}, the site on {self.device}")
+
+    def _out_strides(self, residual, head_dim: int, y, M: int):
+        """(ldr, ldy) of a call."""
+        ldr = 0 if residual is None else _rows(self, residual, "residual", M, self.N)
+        if not head_dim:
+            return ldr, _rows(self, y, "y", M, self.N)
+        if y.dtype not in self._bf16 or y.device != self.device:
+            raise ValueError(f"y is {y.dtype} on {y.device}, not bfloat16 (or its bits) on {self.device}")
+        if y.shape != (self.N // head_dim, M, head_dim) or not y.is_contiguous():
+            raise ValueError(f"y is {tuple(y.shape)} with strides {y.stride()}, not {(self.N // head_dim, M, head_dim)}, "
+                             "contiguous")
+        return ldr, 0
+
     # -- calls
     def prologue(self, x, codes=None, scales=None, stream=None):
         M = x.shape[0]
+        ldx = _rows(self, x, "x", M, self.K, exact=True)
+        self._check_device()
         if codes is None:
             codes, scales = self.empty_codes(M)
-        B.fq_fp8_prologue(x, M, self.K, x.stride(0), self.gamma, self.eps, codes, scales, stream)
+        else:
+            self._check_codes(codes, scales, M)
+        B.fq_fp8_prologue(x, M, self.K, ldx, self.gamma, self.eps, codes, scales, stream)
         return codes, scales
 
     def gemm(self, codes, scales, M: int, residual=None, head_dim: int = 0, y=None, stream=None):
         """y [M][N], or [N / head_dim][M][head_dim], from codes that a prologue or fq_block_norm wrote."""
+        self._check_codes(codes, scales, M)
+        self._check_device()
         if y is None:
             y = self._out(M, head_dim)
-        B.fq_fp8_gemm(codes, scales, M, self.codes, self.wscale, self.N, self.K, self.bias, residual,
-                      0 if residual is None else residual.stride(0), head_dim, y, 0 if head_dim else y.stride(0), stream)
+        ldr, ldy = self._out_strides(residual, head_dim, y, M)
+        B.fq_fp8_gemm(codes, scales, M, self.codes, self.wscale, self.N, self.K, self.bias, residual, ldr, head_dim, y, ldy,
+                      stream)
         return y
 
     def linear(self, x, residual=None, head_dim: int = 0, y=None, stream=None):
         M = x.shape[0]
+        ldx = _rows(self, x, "x", M, self.K, exact=True)
+        self._check_device()
         if y is None:
             y = self._out(M, head_dim)
+        ldr, ldy = self._out_strides(residual, head_dim, y, M)
         ws = self.workspace(M)
-        B.fq_fp8_linear(x, M, self.K, x.stride(0), self.gamma, self.eps, self.codes, self.wscale, self.N, self.bias,
-                        residual, 0 if residual is None else residual.stride(0), head_dim, y,
-                        0 if head_dim else y.stride(0), ws, ws.numel(), stream)
+        B.fq_fp8_linear(x, M, self.K, ldx, self.gamma, self.eps, self.codes, self.wscale, self.N, self.bias, residual, ldr,
+                        head_dim, y, ldy, ws, ws.numel(), stream)
         return y
