@@ -120,3 +120,75 @@ def test_a_call_on_another_current_device_is_refused(site, monkeypatch):
 def test_parameters_are_refused(kw, match):
     with pytest.raises(ValueError, match=match):
         fq.Fp8Site(device="cpu", **kw)
+
+
+# ------------------------------------------------------------------ the integer sites
+@pytest.fixture(scope="module", params=[(8, 8), (4, 4)])
+def integer_site(request):
+    wbits, abits = request.param
+    return fq.DeviceSite(np.ones((N, K), np.float32), 64, wbits, abits, gamma=np.ones(K, np.float32), device="cpu")
+
+
+@pytest.mark.parametrize("x", GOOD_X + [bf16(M, K + 8)])
+def test_good_integer_calls_reach_the_binding(integer_site, x):
+    s, m = integer_site, x.shape[0]
+    codes, scales = s.empty_codes(m)
+    y, res = bf16(m + 1, N + 16), bf16(m, N + 8)
+    for call in (lambda: s.prologue(x), lambda: s.prologue(x, codes, scales), lambda: s.linear(x, residual=res, y=y),
+                 lambda: s.linear_noalloc(x), lambda: s.linear_heads(x, 8, residual=res),
+                 lambda: s.linear_heads(x, 8, y=bf16(N // 8, m, 8)), lambda: s.gemm(codes, scales, m, residual=res, y=y),
+                 lambda: s.gemm(codes, scales, m, acc=torch.zeros(m, N, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="GPU tensors"):
+            call()
+
+
+@pytest.mark.parametrize("x,match", [
+    (torch.zeros(M, K), "x has dtype torch.float32"),
+    (bf16(M, K - 64), f"x is {M} x {K - 64}, not {M} x {K}"),
+    (bf16(1, M, K), "x has 3 dimensions"),
+    (bf16(K, M).t(), "x has stride"),
+    (bf16(M, K).to("meta"), "x is on meta, the site on cpu"),
+])
+def test_integer_rows_are_refused(integer_site, x, match):
+    s = integer_site
+    for call in (s.linear, s.linear_noalloc, s.prologue, lambda v: s.linear_heads(v, 8)):
+        with pytest.raises(ValueError, match=match):
+            call(x)
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(residual=torch.zeros(M, N)), "residual has dtype torch.float32"),
+    (dict(residual=bf16(M - 1, N)), f"residual is {M - 1} x {N}, not {M} x {N}"),
+    (dict(y=bf16(M - 1, N)), f"y is {M - 1} x {N}"),
+    (dict(y=bf16(M, N - 8)), f"y is {M} x {N - 8}"),
+])
+def test_integer_outputs_and_residuals_are_refused(integer_site, kw, match):
+    s, x = integer_site, bf16(M, K)
+    codes, scales = s.empty_codes(M)
+    for call in (lambda: s.linear(x, **kw), lambda: s.linear_noalloc(x, **kw), lambda: s.gemm(codes, scales, M, **kw)):
+        with pytest.raises(ValueError, match=match):
+            call()
+
+
+def test_integer_codes_heads_and_sums_are_refused(integer_site):
+    s, x = integer_site, bf16(M, K)
+    codes, scales = s.empty_codes(M)
+    for c, sc, match in ((codes[:-1], scales, "codes are"), (codes, scales[:-1], "scales are"),
+                         (codes, scales.to(torch.float64), "scales are"), (codes, scales.to("meta"), "the site on cpu")):
+        with pytest.raises(ValueError, match=match):
+            s.prologue(x, c, sc)
+        with pytest.raises(ValueError, match=match):
+            s.gemm(c, sc, M)
+    with pytest.raises(ValueError, match=f"acc is {M} x {N} int32"):
+        s.gemm(codes, scales, M, acc=torch.zeros(M - 1, N, dtype=torch.int32))
+    with pytest.raises(ValueError, match="contiguous"):
+        s.linear_heads(x, 8, y=bf16(N // 8, M, 16)[..., :8])
+    with pytest.raises(ValueError, match=r"y is \(33, 4, 8\)"):
+        s.linear_heads(x, 8, y=bf16(N // 8, M - 1, 8))
+
+
+@pytest.mark.parametrize("kw", [dict(gamma=np.ones(K - 64, np.float32)), dict(bias=np.ones(N + 8, np.float32)),
+                                dict(ascale=np.ones(K + 64, np.float32))])
+def test_integer_parameters_are_refused(kw):
+    with pytest.raises(ValueError, match=f"{next(iter(kw))} has shape"):
+        fq.DeviceSite(np.ones((N, K), np.float32), 64, 8, 8, device="cpu", **kw)

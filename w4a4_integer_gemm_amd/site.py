@@ -46,12 +46,31 @@ def _rows(site, t, name: str, rows: int, cols: int, exact: bool = False) -> int:
     return stride[0]
 
 
+def _check_vectors(**vectors):
+    for name, (v, n) in vectors.items():
+        if v is not None and np.shape(v) != (n,):
+            raise ValueError(f"{name} has shape {np.shape(v)}, not ({n},)")
+
+
+def _check_heads(site, y, M: int, head_dim: int):
+    """y is [N / head_dim][M][head_dim], contiguous bf16, on the site's device."""
+    if y.dtype not in site._bf16 or y.device != site.device:
+        raise ValueError(f"y is {y.dtype} on {y.device}, not bfloat16 (or its bits) on {site.device}")
+    if y.shape != (site.N // head_dim, M, head_dim) or not y.is_contiguous():
+        raise ValueError(f"y is {tuple(y.shape)} with strides {y.stride()}, not {(site.N // head_dim, M, head_dim)}, "
+                         "contiguous")
+
+
 class DeviceSite:
     """One linear site: x [M][K] bf16 -> y [M][N] bf16.
 
     gamma: RMSNorm gain (None for a quant-only site); ascale: smoothing vector;
     fold_into_gain: carry ascale inside the gain (gamma / a, fold before) rather
-    than as an explicit divide in the prologue."""
+    than as an explicit divide in the prologue.
+
+    Tensors hold bf16 or its bits (int16, uint16): x M x K, a residual and an output
+    M x N, each or more (the first rows and columns are taken), the head layout's output
+    [N / head_dim][M][head_dim], contiguous, all on the site's device; ValueError otherwise."""
 
     def __init__(self, W: np.ndarray, hblock: int, wbits: int, abits: int, gamma=None, ascale=None,
                  fold_after: int = 0, fold_into_gain: bool = True, bias=None, eps: float = 1e-6,
@@ -61,11 +80,14 @@ class DeviceSite:
         self.N, self.K = W.shape if W is not None else (codes.shape[0], codes.shape[1] * 8 // wbits)
         self.hblock, self.wbits, self.abits = hblock, wbits, abits
         self.eps, self.fold_after = float(eps), int(fold_after)
+        self._bf16 = _bf16_types()
+        _check_vectors(gamma=(gamma, self.K), ascale=(ascale, self.K), bias=(bias, self.N))
         self.device = torch.device(device)
         if codes is None:
             codes, wscale = B.fq_pack_weights(W, ascale, fold_after, hblock, wbits)
         self.codes_host, self.wscale_host = codes, wscale
         self.codes = _to_dev(codes, self.device)
+        self.device = self.codes.device
         self.wscale = _to_dev(wscale, self.device)
         if gamma is not None and fold_into_gain:
             if fold_after:
@@ -100,30 +122,55 @@ class DeviceSite:
         return (torch.empty(B.fq_act_bytes(M, self.K, self.abits), dtype=torch.uint8, device=self.device),
                 torch.empty(M, dtype=torch.float32, device=self.device))
 
+    # -- checks
+    def _check_codes(self, codes, scales, M: int):
+        need = M * (self.K * self.abits // 8)
+        if codes.numel() * codes.element_size() < need or not codes.is_contiguous():
+            raise ValueError(f"codes are {need} contiguous bytes for M={M}, not {tuple(codes.shape)} of {codes.dtype}")
+        if scales.element_size() != 4 or scales.numel() < M or not scales.is_contiguous():
+            raise ValueError(f"scales are {M} float32 values, not {tuple(scales.shape)} of {scales.dtype}")
+        if codes.device != self.device or scales.device != self.device:
+            raise ValueError(f"codes are on {codes.device} and scales on {scales.device}, the site on {self.device}")
+
+    def _residual_stride(self, residual, M: int) -> int:
+        return 0 if residual is None else _rows(self, residual, "residual", M, self.N)
+
+    def _strides(self, x, residual, y, M: int):
+        """(ldx, ldr, ldy) of a call."""
+        return _rows(self, x, "x", M, self.K), self._residual_stride(residual, M), _rows(self, y, "y", M, self.N)
+
     # -- calls
     def prologue(self, x, codes=None, scales=None, stream=None):
         M = x.shape[0]
+        ldx = _rows(self, x, "x", M, self.K)
         if codes is None:
             codes, scales = self.empty_codes(M)
-        B.fq_prologue(x, M, self.K, x.stride(0), self.gamma, self.eps, self.ascale, self.fold_after,
+        else:
+            self._check_codes(codes, scales, M)
+        B.fq_prologue(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after,
                       self.hblock, self.abits, codes, scales, stream)
         return codes, scales
 
     def gemm(self, codes, scales, M: int, residual=None, y=None, acc=None, stream=None):
         if y is None:
             y = self.empty_out(M)
+        self._check_codes(codes, scales, M)
+        ldr, ldy = self._residual_stride(residual, M), _rows(self, y, "y", M, self.N)
+        if acc is not None and (acc.element_size() != 4 or acc.numel() < M * self.N or not acc.is_contiguous()):
+            raise ValueError(f"acc is {M} x {self.N} int32, not {tuple(acc.shape)} of {acc.dtype}")
         B.fq_gemm(codes, scales, M, self.abits, self.codes, self.wscale, self.N, self.K, self.wbits, self.bias,
-                  residual, 0 if residual is None else residual.stride(0), y, y.stride(0), acc, stream)
+                  residual, ldr, y, ldy, acc, stream)
         return y
 
     def linear(self, x, residual=None, y=None, stream=None):
         M = x.shape[0]
         if y is None:
             y = self.empty_out(M)
+        ldx, ldr, ldy = self._strides(x, residual, y, M)
         ws = self.workspace(M)
-        B.fq_linear(x, M, self.K, x.stride(0), self.gamma, self.eps, self.ascale, self.fold_after, self.hblock,
+        B.fq_linear(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after, self.hblock,
                     self.abits, self.codes, self.wscale, self.N, self.wbits, self.bias, residual,
-                    0 if residual is None else residual.stride(0), y, y.stride(0), ws, ws.numel(), stream)
+                    ldr, y, ldy, ws, ws.numel(), stream)
         return y
 
     def linear_noalloc(self, x, residual=None, y=None, stream=None):
@@ -131,9 +178,10 @@ class DeviceSite:
         M = x.shape[0]
         if y is None:
             y = self.empty_out(M)
-        B.fq_linear_noalloc(x, M, self.K, x.stride(0), self.gamma, self.eps, self.ascale, self.fold_after,
+        ldx, ldr, ldy = self._strides(x, residual, y, M)
+        B.fq_linear_noalloc(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after,
                             self.hblock, self.abits, self.codes, self.wscale, self.N, self.wbits, self.bias, residual,
-                            0 if residual is None else residual.stride(0), y, y.stride(0), stream)
+                            ldr, y, ldy, stream)
         return y
 
     def linear_heads(self, x, head_dim: int, residual=None, y=None, stream=None):
@@ -142,10 +190,12 @@ class DeviceSite:
         M = x.shape[0]
         if y is None:
             y = torch.empty((self.N // head_dim, M, head_dim), dtype=torch.int16, device=self.device)
+        ldx, ldr = _rows(self, x, "x", M, self.K), self._residual_stride(residual, M)
+        _check_heads(self, y, M, head_dim)
         ws = self.workspace(M)
-        B.fq_linear_heads(x, M, self.K, x.stride(0), self.gamma, self.eps, self.ascale, self.fold_after, self.hblock,
+        B.fq_linear_heads(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after, self.hblock,
                           self.abits, self.codes, self.wscale, self.N, self.wbits, self.bias, residual,
-                          0 if residual is None else residual.stride(0), head_dim, y, ws, ws.numel(), stream)
+                          ldr, head_dim, y, ws, ws.numel(), stream)
         return y
 
     def workspace_codes(self, M: int):
@@ -200,9 +250,7 @@ class Fp8Site:
         if self.wscale.numel() != B.fq_fp8_wscale_count(self.N, self.K):
             raise ValueError(f"wscale has {self.wscale.numel()} values, not {B.fq_fp8_wscale_count(self.N, self.K)} "
                              f"for N={self.N} K={self.K}")
-        for name, v, n in (("gamma", gamma, self.K), ("bias", bias, self.N)):
-            if v is not None and np.shape(v) != (n,):
-                raise ValueError(f"{name} has shape {np.shape(v)}, not ({n},)")
+        _check_vectors(gamma=(gamma, self.K), bias=(bias, self.N))
         self.gamma = _to_dev(None if gamma is None else np.ascontiguousarray(gamma, np.float32), self.device)
         self.bias = _to_dev(None if bias is None else np.ascontiguousarray(bias, np.float32), self.device)
         self._ws = None
@@ -264,11 +312,7 @@ class Fp8Site:
         ldr = 0 if residual is None else _rows(self, residual, "residual", M, self.N)
         if not head_dim:
             return ldr, _rows(self, y, "y", M, self.N)
-        if y.dtype not in self._bf16 or y.device != self.device:
-            raise ValueError(f"y is {y.dtype} on {y.device}, not bfloat16 (or its bits) on {self.device}")
-        if y.shape != (self.N // head_dim, M, head_dim) or not y.is_contiguous():
-            raise ValueError(f"y is {tuple(y.shape)} with strides {y.stride()}, not {(self.N // head_dim, M, head_dim)}, "
-                             "contiguous")
+        _check_heads(self, y, M, head_dim)
         return ldr, 0
 
     # -- calls
