@@ -6,6 +6,7 @@ libfq's host packer; everything else runs in libfq's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import numpy as np
@@ -21,6 +22,13 @@ def _to_dev(a: Optional[np.ndarray], device):
     if a.dtype == np.uint16:
         a = a.view(np.int16)
     return torch.from_numpy(a).to(device)
+
+
+def _allocating_on(stream):
+    """Allocations for a call on `stream` (None: the current one) come from that stream's
+    memory: a block that another stream's queued work still uses is not handed out."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _bf16_types():
@@ -104,23 +112,26 @@ class DeviceSite:
         self._ws_bytes = {}  # M -> fq_linear_workspace_bytes
 
     # -- buffers
-    def workspace(self, M: int):
+    def workspace(self, M: int, stream=None):
         import torch
         nbytes = self._ws_bytes.get(M)
         if nbytes is None:
             nbytes = self._ws_bytes[M] = B.fq_linear_workspace_bytes(M, self.K, self.abits)
         if self._ws is None or self._ws.numel() < nbytes:
-            self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            with _allocating_on(stream):
+                self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         return self._ws
 
-    def empty_out(self, M: int):
+    def empty_out(self, M: int, stream=None):
         import torch
-        return torch.empty((M, self.N), dtype=torch.int16, device=self.device)
+        with _allocating_on(stream):
+            return torch.empty((M, self.N), dtype=torch.int16, device=self.device)
 
-    def empty_codes(self, M: int):
+    def empty_codes(self, M: int, stream=None):
         import torch
-        return (torch.empty(B.fq_act_bytes(M, self.K, self.abits), dtype=torch.uint8, device=self.device),
-                torch.empty(M, dtype=torch.float32, device=self.device))
+        with _allocating_on(stream):
+            return (torch.empty(B.fq_act_bytes(M, self.K, self.abits), dtype=torch.uint8, device=self.device),
+                    torch.empty(M, dtype=torch.float32, device=self.device))
 
     # -- checks
     def _check_codes(self, codes, scales, M: int):
@@ -144,7 +155,7 @@ class DeviceSite:
         M = x.shape[0]
         ldx = _rows(self, x, "x", M, self.K)
         if codes is None:
-            codes, scales = self.empty_codes(M)
+            codes, scales = self.empty_codes(M, stream)
         else:
             self._check_codes(codes, scales, M)
         B.fq_prologue(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after,
@@ -153,7 +164,7 @@ class DeviceSite:
 
     def gemm(self, codes, scales, M: int, residual=None, y=None, acc=None, stream=None):
         if y is None:
-            y = self.empty_out(M)
+            y = self.empty_out(M, stream)
         self._check_codes(codes, scales, M)
         ldr, ldy = self._residual_stride(residual, M), _rows(self, y, "y", M, self.N)
         if acc is not None and (acc.element_size() != 4 or acc.numel() < M * self.N or not acc.is_contiguous()):
@@ -165,9 +176,9 @@ class DeviceSite:
     def linear(self, x, residual=None, y=None, stream=None):
         M = x.shape[0]
         if y is None:
-            y = self.empty_out(M)
+            y = self.empty_out(M, stream)
         ldx, ldr, ldy = self._strides(x, residual, y, M)
-        ws = self.workspace(M)
+        ws = self.workspace(M, stream)
         B.fq_linear(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after, self.hblock,
                     self.abits, self.codes, self.wscale, self.N, self.wbits, self.bias, residual,
                     ldr, y, ldy, ws, ws.numel(), stream)
@@ -177,7 +188,7 @@ class DeviceSite:
         """fq_linear_noalloc: as linear(), with the library's per-GPU scratch array as the workspace."""
         M = x.shape[0]
         if y is None:
-            y = self.empty_out(M)
+            y = self.empty_out(M, stream)
         ldx, ldr, ldy = self._strides(x, residual, y, M)
         B.fq_linear_noalloc(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after,
                             self.hblock, self.abits, self.codes, self.wscale, self.N, self.wbits, self.bias, residual,
@@ -189,10 +200,11 @@ class DeviceSite:
         import torch
         M = x.shape[0]
         if y is None:
-            y = torch.empty((self.N // head_dim, M, head_dim), dtype=torch.int16, device=self.device)
+            with _allocating_on(stream):
+                y = torch.empty((self.N // head_dim, M, head_dim), dtype=torch.int16, device=self.device)
         ldx, ldr = _rows(self, x, "x", M, self.K), self._residual_stride(residual, M)
         _check_heads(self, y, M, head_dim)
-        ws = self.workspace(M)
+        ws = self.workspace(M, stream)
         B.fq_linear_heads(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after, self.hblock,
                           self.abits, self.codes, self.wscale, self.N, self.wbits, self.bias, residual,
                           ldr, head_dim, y, ws, ws.numel(), stream)
@@ -224,7 +236,8 @@ class Fp8Site:
     which is the current one; ValueError otherwise.
 
     linear() uses the site's own workspace, which belongs to one call at a time: calls
-    on two streams at once take two sites (of the same codes and wscale).  A
+    on two streams at once take two sites (of the same codes and wscale).  What a call
+    with stream= allocates belongs to that stream.  A
     workspace that grew leaves the one before allocated, since a captured graph may
     still use it."""
 
@@ -258,16 +271,17 @@ class Fp8Site:
         self._ws_bytes = {}  # M -> fq_fp8_linear_workspace_bytes
 
     # -- buffers
-    def workspace(self, M: int):
+    def workspace(self, M: int, stream=None):
         import torch
         nbytes = self._ws_bytes.get(M)
         if nbytes is None:
             nbytes = self._ws_bytes[M] = B.fq_fp8_linear_workspace_bytes(M, self.K)
-        if self._ws is None:
-            self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        elif self._ws.numel() < nbytes:
-            self._ws_before.append(self._ws)
-            self._ws = torch.empty(max(nbytes, 2 * self._ws.numel()), dtype=torch.uint8, device=self.device)
+        if self._ws is None or self._ws.numel() < nbytes:
+            if self._ws is not None:
+                self._ws_before.append(self._ws)
+                nbytes = max(nbytes, 2 * self._ws.numel())
+            with _allocating_on(stream):
+                self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         return self._ws
 
     def workspace_codes(self, M: int):
@@ -279,15 +293,17 @@ class Fp8Site:
         sc = ws[off:off + 4 * B.fq_fp8_ascale_count(M, self.K)].view(torch.float32)
         return ws[:nb].view(M, self.K), sc.view(self.K // 128, -1)[:, :M]
 
-    def empty_codes(self, M: int):
+    def empty_codes(self, M: int, stream=None):
         import torch
-        return (torch.empty((M, self.K), dtype=torch.uint8, device=self.device),
-                torch.empty((self.K // 128, -(-M // 4) * 4), dtype=torch.float32, device=self.device))
+        with _allocating_on(stream):
+            return (torch.empty((M, self.K), dtype=torch.uint8, device=self.device),
+                    torch.empty((self.K // 128, -(-M // 4) * 4), dtype=torch.float32, device=self.device))
 
-    def _out(self, M: int, head_dim: int):
+    def _out(self, M: int, head_dim: int, stream):
         import torch
         shape = (self.N // head_dim, M, head_dim) if head_dim else (M, self.N)
-        return torch.empty(shape, dtype=torch.int16, device=self.device)
+        with _allocating_on(stream):
+            return torch.empty(shape, dtype=torch.int16, device=self.device)
 
     # -- checks
     def _check_device(self):
@@ -321,7 +337,7 @@ class Fp8Site:
         ldx = _rows(self, x, "x", M, self.K, exact=True)
         self._check_device()
         if codes is None:
-            codes, scales = self.empty_codes(M)
+            codes, scales = self.empty_codes(M, stream)
         else:
             self._check_codes(codes, scales, M)
         B.fq_fp8_prologue(x, M, self.K, ldx, self.gamma, self.eps, codes, scales, stream)
@@ -332,7 +348,7 @@ class Fp8Site:
         self._check_codes(codes, scales, M)
         self._check_device()
         if y is None:
-            y = self._out(M, head_dim)
+            y = self._out(M, head_dim, stream)
         ldr, ldy = self._out_strides(residual, head_dim, y, M)
         B.fq_fp8_gemm(codes, scales, M, self.codes, self.wscale, self.N, self.K, self.bias, residual, ldr, head_dim, y, ldy,
                       stream)
@@ -343,9 +359,9 @@ class Fp8Site:
         ldx = _rows(self, x, "x", M, self.K, exact=True)
         self._check_device()
         if y is None:
-            y = self._out(M, head_dim)
+            y = self._out(M, head_dim, stream)
         ldr, ldy = self._out_strides(residual, head_dim, y, M)
-        ws = self.workspace(M)
+        ws = self.workspace(M, stream)
         B.fq_fp8_linear(x, M, self.K, ldx, self.gamma, self.eps, self.codes, self.wscale, self.N, self.bias, residual, ldr,
                         head_dim, y, ldy, ws, ws.numel(), stream)
         return y
