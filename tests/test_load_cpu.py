@@ -1,0 +1,31 @@
+"""Loading the library: a host-only caller does not pay torch's import, and a process that imports torch later has
+one HIP runtime, torch's."""
+import os
+import subprocess
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+CODE = """
+import sys
+import numpy as np
+import w4a4_integer_gemm_amd as fq
+fq.fq_rope_freqs(64)
+fq.fq_fp8_pack_weights(np.ones((8, 128), np.float32))
+fq.fq_pack_weights(np.ones((8, 128), np.float32), None, 0, 64, 8)
+print("torch imported:", "torch" in sys.modules)
+import torch
+paths = {line.split()[-1] for line in open("/proc/self/maps") if "libamdhip64" in line}
+print("runtimes:", sorted(paths))
+print("of torch:", all(p.startswith(torch.__path__[0]) for p in paths) if len(paths) else None)
+"""
+
+
+def test_host_calls_do_not_import_torch_and_leave_one_runtime():
+    r = subprocess.run([sys.executable, "-c", CODE], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    out = dict(line.split(": ", 1) for line in r.stdout.splitlines() if ": " in line)
+    assert out["torch imported"] == "False"
+    import torch
+    if os.path.exists(os.path.join(torch.__path__[0], "lib", "libamdhip64.so")):
+        assert out["runtimes"].count("libamdhip64") == 1 and out["of torch"] == "True", out

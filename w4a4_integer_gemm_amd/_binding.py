@@ -8,7 +8,9 @@ fallback: if libfq.so is missing or a call fails, an exception says why.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import sys
 from typing import Optional
 
 import numpy as np
@@ -80,6 +82,19 @@ class FqError(RuntimeError):
 _lib = None
 
 
+def _load_hip_runtime():
+    """torch brings a HIP runtime of its own, and a host call of this library before `import
+    torch` (a packer, a rotary plan) would load the system's, which then sees no device.
+    The one that torch will use is loaded first, without torch's import (1 to 2 s, which
+    callers of the host entry points alone do not need)."""
+    if "torch" in sys.modules:
+        return
+    spec = importlib.util.find_spec("torch")
+    path = spec and spec.origin and os.path.join(os.path.dirname(spec.origin), "lib", "libamdhip64.so")
+    if path and os.path.exists(path):
+        ctypes.CDLL(path)
+
+
 def lib() -> ctypes.CDLL:
     """Load libfq.so from the package directory (built by build.py)."""
     global _lib
@@ -87,13 +102,7 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"libfq.so not found at {LIB_PATH}; build it with "
                                "`python w4a4_integer_gemm_amd/build.py` (hipcc, gfx950)")
-        # torch first: it brings its own HIP runtime, and a host call of this
-        # library before `import torch` (a packer, a rotary plan) would load the
-        # system's, which then sees no device
-        try:
-            import torch  # noqa: F401
-        except ImportError:
-            pass  # the host entry points need no torch
+        _load_hip_runtime()
         L = ctypes.CDLL(LIB_PATH)
         for name, (args, res) in SIGNATURES.items():
             fn = getattr(L, name)
