@@ -32,7 +32,7 @@ from w4a4_integer_gemm_amd.build import SOURCES as _LIB_SOURCES  # noqa: E402
 
 DEVICE_OBJECTS = [os.path.splitext(s)[0] + ".o" for s in _LIB_SOURCES if s.endswith(".hip")]
 TESTS = ["tests/test_abi_cpu.py", "tests/test_oracle_pins.py", "tests/test_fold_consistency.py",
-         "tests/test_block_cpu.py"]
+         "tests/test_block_cpu.py", "tests/test_fp8_refusals_cpu.py"]
 
 
 def run(cmd):

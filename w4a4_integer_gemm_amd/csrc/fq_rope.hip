@@ -24,6 +24,7 @@
 
 #include "fq_device.h"
 #include "fq_internal.h"
+#include "fq_row_norm.h"
 #include "fq_token.h"
 
 namespace fq {
@@ -64,11 +65,6 @@ __device__ __forceinline__ void angles(const RopeArgs& a, int32_t pos, int i0, i
         c[j] *= a.attn_scale;
         s[j] *= a.inverse ? -a.attn_scale : a.attn_scale;
     }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                      pack_bf16x2(v[6], v[7]));
 }
 
 // Rotates the pieces u, v (halves) or u alone (interleaved).
@@ -153,18 +149,17 @@ __global__ __launch_bounds__(256) void rope_pairs_kernel(RopeArgs a) {
         s *= a.inverse ? -a.attn_scale : a.attn_scale;
         if (!a.interleaved) e0 = i, e1 = i + rh;
     }
-    for (int h = blockIdx.y; h < a.heads; h += gridDim.y) {
-        const uint16_t* xp = a.x + m * a.x_token + h * a.x_head;
-        uint16_t* yp = a.y + m * a.y_token + h * a.y_head;
-        const uint16_t u = xp[e0], v = xp[e1];
-        if (rot && h < a.rot_heads) {
-            const float p = bf16_value(u), q = bf16_value(v);
-            yp[e0] = to_bf16(__builtin_fmaf(p, c, -(q * s)));
-            yp[e1] = to_bf16(__builtin_fmaf(q, c, p * s));
-        } else if (xp != yp) {
-            yp[e0] = u;
-            yp[e1] = v;
-        }
+    const int h = blockIdx.y;
+    const uint16_t* xp = a.x + m * a.x_token + h * a.x_head;
+    uint16_t* yp = a.y + m * a.y_token + h * a.y_head;
+    const uint16_t u = xp[e0], v = xp[e1];
+    if (rot && h < a.rot_heads) {
+        const float p = bf16_value(u), q = bf16_value(v);
+        yp[e0] = to_bf16(__builtin_fmaf(p, c, -(q * s)));
+        yp[e1] = to_bf16(__builtin_fmaf(q, c, p * s));
+    } else if (xp != yp) {
+        yp[e0] = u;
+        yp[e1] = v;
     }
 }
 
