@@ -32,13 +32,15 @@ def test_good_outputs_and_residuals_reach_the_binding(site):
     x = bf16(M, K)
     codes, scales = site.empty_codes(M)
     for kw in (dict(y=bf16(M, N)), dict(y=bf16(M + 1, N + 16)), dict(residual=bf16(M, N + 8)), dict(head_dim=8),
-               dict(head_dim=8, y=bf16(N // 8, M, 8), residual=bf16(M, N))):
+               dict(head_dim=8, y=bf16(N // 8, M, 8), residual=bf16(M, N)), dict(head_dim=8, y=bf16(M * N))):
         with pytest.raises(ValueError, match="GPU tensors"):
             site.linear(x, **kw)
         with pytest.raises(ValueError, match="GPU tensors"):
             site.gemm(codes, scales, M, **kw)
         with pytest.raises(ValueError, match="GPU tensors"):
             site.gemm(codes.view(torch.float8_e4m3fn), scales[:, :M], M, **kw)
+        with pytest.raises(ValueError, match="GPU tensors"):
+            site.gemm(codes.flatten(), scales.flatten(), M, **kw)
 
 
 @pytest.mark.parametrize("x,match", [
@@ -69,6 +71,7 @@ def test_rows_are_refused(site, x, match, call):
     (dict(y=bf16(M, N), head_dim=8), r"y is \(5, 264\)"),
     (dict(y=bf16(N // 8, M - 1, 8), head_dim=8), r"y is \(33, 4, 8\)"),
     (dict(y=bf16(N // 8, M, 16)[..., :8], head_dim=8), "contiguous"),
+    (dict(y=bf16(M * N - 1), head_dim=8), r"y is \(1319,\)"),
     (dict(y=bf16(M, N).to("meta")), "y is on meta"),
     (dict(y=torch.zeros(N // 8, M, 8), head_dim=8), "y is torch.float32 on cpu"),
 ])
@@ -88,7 +91,9 @@ def test_outputs_and_residuals_are_refused(site, kw, match):
     (torch.zeros(M, K, dtype=torch.uint8), torch.zeros(2, 5), "scales are"),
     (torch.zeros(M, K, dtype=torch.uint8), torch.zeros(1, 8), "scales are"),
     (torch.zeros(M, K, dtype=torch.uint8), torch.zeros(2, 8)[:, :4], "scales are"),
-    (torch.zeros(M, K, dtype=torch.uint8), torch.zeros(16), "scales are"),
+    (torch.zeros(M, K, dtype=torch.uint8), torch.zeros(15), "scales are"),
+    (torch.zeros(M, K, dtype=torch.uint8), torch.zeros(32)[::2], "scales are"),
+    (torch.zeros(M * K - 1, dtype=torch.uint8), torch.zeros(2, 8), "codes are"),
     (torch.zeros(M, K, dtype=torch.uint8), torch.zeros(2, 8, device="meta"), "the site on cpu"),
 ])
 def test_codes_and_scales_are_refused(site, codes, scales, match):

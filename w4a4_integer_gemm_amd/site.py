@@ -61,12 +61,12 @@ def _check_vectors(**vectors):
 
 
 def _check_heads(site, y, M: int, head_dim: int):
-    """y is [N / head_dim][M][head_dim], contiguous bf16, on the site's device."""
+    """y is [N / head_dim][M][head_dim], contiguous bf16, on the site's device (or a flat buffer of them)."""
     if y.dtype not in site._bf16 or y.device != site.device:
         raise ValueError(f"y is {y.dtype} on {y.device}, not bfloat16 (or its bits) on {site.device}")
-    if y.shape != (site.N // head_dim, M, head_dim) or not y.is_contiguous():
-        raise ValueError(f"y is {tuple(y.shape)} with strides {y.stride()}, not {(site.N // head_dim, M, head_dim)}, "
-                         "contiguous")
+    shape = (site.N // head_dim, M, head_dim)
+    if not (y.shape == shape or (y.dim() == 1 and y.numel() >= M * site.N)) or not y.is_contiguous():
+        raise ValueError(f"y is {tuple(y.shape)} with strides {y.stride()}, not {shape}, contiguous")
 
 
 class DeviceSite:
@@ -232,8 +232,9 @@ class Fp8Site:
 
     Tensors hold bf16 or its bits (int16, uint16); x is M x K, a residual or an output
     given for the row layout has M rows and N columns or more, one given for the head
-    layout is [N / head_dim][M][head_dim], contiguous.  All are on the site's device,
-    which is the current one; ValueError otherwise.
+    layout is [N / head_dim][M][head_dim], contiguous; codes, scales and the head layout's
+    output may be flat buffers of that size.  All are on the site's device, which is the
+    current one; ValueError otherwise.
 
     linear() uses the site's own workspace, which belongs to one call at a time: calls
     on two streams at once take two sites (of the same codes and wscale).  What a call
@@ -313,13 +314,15 @@ class Fp8Site:
 
     def _check_codes(self, codes, scales, M: int):
         import torch
-        if codes.element_size() != 1 or codes.shape != (M, self.K) or not codes.is_contiguous():
+        flat = codes.dim() == 1 and codes.numel() >= M * self.K
+        if codes.element_size() != 1 or not (codes.shape == (M, self.K) or flat) or not codes.is_contiguous():
             raise ValueError(f"codes are {M} x {self.K} bytes, contiguous, not {tuple(codes.shape)} of {codes.dtype}")
-        ld = -(-M // 4) * 4
-        if (scales.dtype != torch.float32 or scales.dim() != 2 or scales.shape[0] != self.K // 128 or scales.shape[1] < M
-                or scales.stride() != (ld, 1)):
-            raise ValueError(f"scales are float32 {self.K // 128} x {M} in rows of {ld}, not {tuple(scales.shape)} of "
-                             f"{scales.dtype} with strides {scales.stride()}")
+        g, ld = self.K // 128, -(-M // 4) * 4
+        flat = scales.dim() == 1 and scales.numel() >= g * ld and scales.stride() == (1,)
+        rows = scales.dim() == 2 and scales.shape[0] == g and scales.shape[1] >= M and scales.stride() == (ld, 1)
+        if scales.dtype != torch.float32 or not (rows or flat):
+            raise ValueError(f"scales are float32 {g} x {M} in rows of {ld}, not {tuple(scales.shape)} of {scales.dtype} "
+                             f"with strides {scales.stride()}")
         if codes.device != self.device or scales.device != self.device:
             raise ValueError(f"codes are on {codes.device} and scales on {scales.device}, the site on {self.device}")
 
