@@ -16,7 +16,9 @@
 // values, so every access of a wave covers contiguous memory and the 128
 // values of one scale group sit in 16 consecutive lanes, whose maximum takes
 // four DPP steps.  The row stays in registers between the two norms: x and r
-// are read once, r' and h written once.
+// are read once, r' and h written once.  (Rows of more than 32768 values, eight
+// pieces a lane, spill 14 to 63 registers to scratch on the way: 1024 x 40960 to bf16
+// 47 us, 3.6 TB/s, to codes 83 us, where 1024 x 32768 takes 29, 4.7 TB/s, and 30.)
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

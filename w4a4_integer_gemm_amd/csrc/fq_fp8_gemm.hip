@@ -29,8 +29,8 @@
 // tiles with the copies going on into the next tile, so that only a tile's
 // epilogue interrupts the products.
 //
-// Measured (4096 x 3584 x 37888, 256 x 256 tiles): 530 us, 2100 TFLOP/s, against
-// 890 us for the first version, whose stages waited for their scales from
+// Measured (4096 x 3584 x 37888, 256 x 256 tiles): 530 to 570 us by card, 2000 to
+// 2100 TFLOP/s, against 890 us for the first version, whose stages waited for their scales from
 // global memory.  What bounds it is power and the copies: without copies the same
 // loop takes 430 us, and the clock falls to 1.6 GHz from 2.4 with both.  A
 // prefetch of later stages into L2 (one dword of each line) made it slower
@@ -448,6 +448,12 @@ constexpr float kTileUs = 2.0f;  // a tile's epilogue and first loads
 // 23.9, 256x128 27.2, 128x128 30.3; 811 x 16384 x 2048: 128x64 45.7, 64x128 46.1,
 // 128x96 50.7, 256x256 165; 4096 x 3584 x 37888: 256x256 530, 256x128 538, 128x128
 // 740.  Tiles of 32 tokens were no faster than those of 64 at 32 tokens.
+//
+// The stage times are of a tile alone: with every CU copying a 128 x 128 stage takes
+// 0.5 us, and the estimate of a large product is mostly 15 to 40 % below its time
+// (1024 x 3584 x 4608: 17.7, measured 22.3; 200 x 3584 x 37888: 32.6, measured 48).
+// The order among the tiles holds; against the other paths' estimates below, taken
+// from whole calls, it leans to the product in one piece.
 struct Pick {
     int tile;
     float us;
@@ -493,6 +499,9 @@ float gemm_us(const Fp8Args& g, const DeviceInfo& dev) {
 }
 // K in parts on tiles of `edge` squared: as many parts as the CUs take at once,
 // each of at least 8 units, all alike, so that every workgroup has as many stages.
+// (A number of units with few divisors gets fewer parts than would fit: 64 tokens of
+// N = 2048 take 15.7 us at K = 16384, in 8 parts, 20.8 at 11008, in 2, 25.4 at 13696,
+// whole.  Tiles for more than half of the CUs are not cut: 811 x 18944 x 3584 77 us.)
 int parts_of(const Fp8Args& g, const DeviceInfo& dev, int edge) {
     const int cus = dev.cus < kSplitTiles ? dev.cus : kSplitTiles, nu = g.K / 128;
     const int64_t tiles = int64_t((g.M + edge - 1) / edge) * ((g.N + edge - 1) / edge);

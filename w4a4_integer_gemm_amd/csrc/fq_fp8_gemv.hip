@@ -11,9 +11,11 @@
 // What costs beside the weights is the codes, read again for every row group:
 // K = 3584, N = 37888 (26.6 us at copy rate): 25.7 us with one token, 26.9 with
 // 4, 30 with 8, beyond which the tiled GEMM takes over (fp8_gemv_takes).
-// Narrow layers keep it up to 32 tokens: K = 16384, N = 2048 12.0 us with one
-// token, 16.7 with 32 (the GEMM 35), bound by what a CU keeps in flight: 16 waves
+// From codes narrow layers keep it up to 32 tokens: K = 16384, N = 2048 16.9 us with
+// 16 tokens, 17.1 with 32 (the GEMM 35), bound by what a CU keeps in flight: 16 waves
 // on a row group took the same time, and so did groups of 8 rows on twice the CUs.
+// (fq_fp8_linear has a workspace and cuts K there: 14.3 and 14.7 with its prologue; one
+// or two tokens of such K take the kernel of fq_fp8_decode.hip.)
 #include <hip/hip_runtime.h>
 
 #include "fq_device.h"

@@ -11,7 +11,7 @@
 // angle's fraction of a turn with no rounding at all, at any position; its top
 // 32 bits give the angle to 2^-32 turns.  cos and sin come from their Taylor
 // series on an eighth of a turn around the nearest quarter (remainders below
-// 2^-28), in float32.
+// 2^-28), in float32: its conversion moves the angle by up to 2^-26 turns.
 //
 // Bound by reading and writing the heads once.  A thread owns one item of one
 // token: with halves the 16-byte piece of 8 `a` elements and the piece of their
@@ -19,7 +19,9 @@
 // It computes the item's angles once and applies them to its share of the heads,
 // UN heads' loads ahead of their stores.  (rot_dim not a multiple of 16, or of 8
 // interleaved, has pieces that are neither: those sizes, and small calls, take
-// a thread per pair of every head.)
+// a thread per pair of every head.  Where such a call is large, its two-byte accesses
+// and an angle for every head cost twice the time: 24571 tokens x 18 heads x 80 with
+// halves of rot_dim 40 70 us, 2.0 TB/s, against 31 us with rot_dim 32.)
 #include <hip/hip_runtime.h>
 
 #include "fq_device.h"
