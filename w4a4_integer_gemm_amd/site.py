@@ -108,18 +108,19 @@ class DeviceSite:
         self.gamma = _to_dev(self.gamma_host, self.device)
         self.ascale = _to_dev(self.ascale_host, self.device)
         self.bias = _to_dev(None if bias is None else np.ascontiguousarray(bias, np.float32), self.device)
-        self._ws = None
+        self._ws, self._ws_size = None, 0
         self._ws_bytes = {}  # M -> fq_linear_workspace_bytes
 
     # -- buffers
     def workspace(self, M: int, stream=None):
-        import torch
         nbytes = self._ws_bytes.get(M)
         if nbytes is None:
             nbytes = self._ws_bytes[M] = B.fq_linear_workspace_bytes(M, self.K, self.abits)
-        if self._ws is None or self._ws.numel() < nbytes:
+        if self._ws is None or self._ws_size < nbytes:
+            import torch
             with _allocating_on(stream):
                 self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            self._ws_size = nbytes
         return self._ws
 
     def empty_out(self, M: int, stream=None):
@@ -143,13 +144,6 @@ class DeviceSite:
         if codes.device != self.device or scales.device != self.device:
             raise ValueError(f"codes are on {codes.device} and scales on {scales.device}, the site on {self.device}")
 
-    def _residual_stride(self, residual, M: int) -> int:
-        return 0 if residual is None else _rows(self, residual, "residual", M, self.N)
-
-    def _strides(self, x, residual, y, M: int):
-        """(ldx, ldr, ldy) of a call."""
-        return _rows(self, x, "x", M, self.K), self._residual_stride(residual, M), _rows(self, y, "y", M, self.N)
-
     # -- calls
     def prologue(self, x, codes=None, scales=None, stream=None):
         M = x.shape[0]
@@ -163,10 +157,9 @@ class DeviceSite:
         return codes, scales
 
     def gemm(self, codes, scales, M: int, residual=None, y=None, acc=None, stream=None):
-        if y is None:
-            y = self.empty_out(M, stream)
         self._check_codes(codes, scales, M)
-        ldr, ldy = self._residual_stride(residual, M), _rows(self, y, "y", M, self.N)
+        ldr = 0 if residual is None else _rows(self, residual, "residual", M, self.N)
+        y, ldy = (self.empty_out(M, stream), self.N) if y is None else (y, _rows(self, y, "y", M, self.N))
         if acc is not None and (acc.element_size() != 4 or acc.numel() < M * self.N or not acc.is_contiguous()):
             raise ValueError(f"acc is {M} x {self.N} int32, not {tuple(acc.shape)} of {acc.dtype}")
         B.fq_gemm(codes, scales, M, self.abits, self.codes, self.wscale, self.N, self.K, self.wbits, self.bias,
@@ -175,21 +168,21 @@ class DeviceSite:
 
     def linear(self, x, residual=None, y=None, stream=None):
         M = x.shape[0]
-        if y is None:
-            y = self.empty_out(M, stream)
-        ldx, ldr, ldy = self._strides(x, residual, y, M)
+        ldx = _rows(self, x, "x", M, self.K)
+        ldr = 0 if residual is None else _rows(self, residual, "residual", M, self.N)
+        y, ldy = (self.empty_out(M, stream), self.N) if y is None else (y, _rows(self, y, "y", M, self.N))
         ws = self.workspace(M, stream)
         B.fq_linear(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after, self.hblock,
                     self.abits, self.codes, self.wscale, self.N, self.wbits, self.bias, residual,
-                    ldr, y, ldy, ws, ws.numel(), stream)
+                    ldr, y, ldy, ws, self._ws_size, stream)
         return y
 
     def linear_noalloc(self, x, residual=None, y=None, stream=None):
         """fq_linear_noalloc: as linear(), with the library's per-GPU scratch array as the workspace."""
         M = x.shape[0]
-        if y is None:
-            y = self.empty_out(M, stream)
-        ldx, ldr, ldy = self._strides(x, residual, y, M)
+        ldx = _rows(self, x, "x", M, self.K)
+        ldr = 0 if residual is None else _rows(self, residual, "residual", M, self.N)
+        y, ldy = (self.empty_out(M, stream), self.N) if y is None else (y, _rows(self, y, "y", M, self.N))
         B.fq_linear_noalloc(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after,
                             self.hblock, self.abits, self.codes, self.wscale, self.N, self.wbits, self.bias, residual,
                             ldr, y, ldy, stream)
@@ -199,15 +192,17 @@ class DeviceSite:
         """fq_linear_heads: y is [N / head_dim][M][head_dim] (int16 tensor of bf16 bits)."""
         import torch
         M = x.shape[0]
+        ldx = _rows(self, x, "x", M, self.K)
+        ldr = 0 if residual is None else _rows(self, residual, "residual", M, self.N)
         if y is None:
             with _allocating_on(stream):
                 y = torch.empty((self.N // head_dim, M, head_dim), dtype=torch.int16, device=self.device)
-        ldx, ldr = _rows(self, x, "x", M, self.K), self._residual_stride(residual, M)
-        _check_heads(self, y, M, head_dim)
+        else:
+            _check_heads(self, y, M, head_dim)
         ws = self.workspace(M, stream)
         B.fq_linear_heads(x, M, self.K, ldx, self.gamma, self.eps, self.ascale, self.fold_after, self.hblock,
                           self.abits, self.codes, self.wscale, self.N, self.wbits, self.bias, residual,
-                          ldr, head_dim, y, ws, ws.numel(), stream)
+                          ldr, head_dim, y, ws, self._ws_size, stream)
         return y
 
     def workspace_codes(self, M: int):
@@ -267,22 +262,23 @@ class Fp8Site:
         _check_vectors(gamma=(gamma, self.K), bias=(bias, self.N))
         self.gamma = _to_dev(None if gamma is None else np.ascontiguousarray(gamma, np.float32), self.device)
         self.bias = _to_dev(None if bias is None else np.ascontiguousarray(bias, np.float32), self.device)
-        self._ws = None
+        self._ws, self._ws_size = None, 0
         self._ws_before = []
         self._ws_bytes = {}  # M -> fq_fp8_linear_workspace_bytes
 
     # -- buffers
     def workspace(self, M: int, stream=None):
-        import torch
         nbytes = self._ws_bytes.get(M)
         if nbytes is None:
             nbytes = self._ws_bytes[M] = B.fq_fp8_linear_workspace_bytes(M, self.K)
-        if self._ws is None or self._ws.numel() < nbytes:
+        if self._ws is None or self._ws_size < nbytes:
+            import torch
             if self._ws is not None:
                 self._ws_before.append(self._ws)
-                nbytes = max(nbytes, 2 * self._ws.numel())
+                nbytes = max(nbytes, 2 * self._ws_size)
             with _allocating_on(stream):
                 self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            self._ws_size = nbytes
         return self._ws
 
     def workspace_codes(self, M: int):
@@ -299,12 +295,6 @@ class Fp8Site:
         with _allocating_on(stream):
             return (torch.empty((M, self.K), dtype=torch.uint8, device=self.device),
                     torch.empty((self.K // 128, -(-M // 4) * 4), dtype=torch.float32, device=self.device))
-
-    def _out(self, M: int, head_dim: int, stream):
-        import torch
-        shape = (self.N // head_dim, M, head_dim) if head_dim else (M, self.N)
-        with _allocating_on(stream):
-            return torch.empty(shape, dtype=torch.int16, device=self.device)
 
     # -- checks
     def _check_device(self):
@@ -326,13 +316,17 @@ class Fp8Site:
         if codes.device != self.device or scales.device != self.device:
             raise ValueError(f"codes are on {codes.device} and scales on {scales.device}, the site on {self.device}")
 
-    def _out_strides(self, residual, head_dim: int, y, M: int):
-        """(ldr, ldy) of a call."""
-        ldr = 0 if residual is None else _rows(self, residual, "residual", M, self.N)
+    def _out(self, head_dim: int, y, M: int, stream):
+        """(y, ldy) of a call: y as given, or a new one."""
+        if y is None:
+            import torch
+            shape = (self.N // head_dim, M, head_dim) if head_dim else (M, self.N)
+            with _allocating_on(stream):
+                return torch.empty(shape, dtype=torch.int16, device=self.device), 0 if head_dim else self.N
         if not head_dim:
-            return ldr, _rows(self, y, "y", M, self.N)
+            return y, _rows(self, y, "y", M, self.N)
         _check_heads(self, y, M, head_dim)
-        return ldr, 0
+        return y, 0
 
     # -- calls
     def prologue(self, x, codes=None, scales=None, stream=None):
@@ -350,9 +344,8 @@ class Fp8Site:
         """y [M][N], or [N / head_dim][M][head_dim], from codes that a prologue or fq_block_norm wrote."""
         self._check_codes(codes, scales, M)
         self._check_device()
-        if y is None:
-            y = self._out(M, head_dim, stream)
-        ldr, ldy = self._out_strides(residual, head_dim, y, M)
+        ldr = 0 if residual is None else _rows(self, residual, "residual", M, self.N)
+        y, ldy = self._out(head_dim, y, M, stream)
         B.fq_fp8_gemm(codes, scales, M, self.codes, self.wscale, self.N, self.K, self.bias, residual, ldr, head_dim, y, ldy,
                       stream)
         return y
@@ -361,10 +354,9 @@ class Fp8Site:
         M = x.shape[0]
         ldx = _rows(self, x, "x", M, self.K, exact=True)
         self._check_device()
-        if y is None:
-            y = self._out(M, head_dim, stream)
-        ldr, ldy = self._out_strides(residual, head_dim, y, M)
+        ldr = 0 if residual is None else _rows(self, residual, "residual", M, self.N)
+        y, ldy = self._out(head_dim, y, M, stream)
         ws = self.workspace(M, stream)
         B.fq_fp8_linear(x, M, self.K, ldx, self.gamma, self.eps, self.codes, self.wscale, self.N, self.bias, residual, ldr,
-                        head_dim, y, ldy, ws, ws.numel(), stream)
+                        head_dim, y, ldy, ws, self._ws_size, stream)
         return y
