@@ -29,3 +29,13 @@ def test_host_calls_do_not_import_torch_and_leave_one_runtime():
     import torch
     if os.path.exists(os.path.join(torch.__path__[0], "lib", "libamdhip64.so")):
         assert out["runtimes"].count("libamdhip64") == 1 and out["of torch"] == "True", out
+
+
+def test_a_torch_that_cannot_be_loaded_leaves_the_host_calls(tmp_path):
+    lib = tmp_path / "torch" / "lib"
+    lib.mkdir(parents=True)
+    (tmp_path / "torch" / "__init__.py").write_text("raise ImportError('broken')")
+    (lib / "libamdhip64.so").write_text("no library")
+    code = "import sys; sys.path.insert(0, %r)\nimport w4a4_integer_gemm_amd as fq\nprint(len(fq.fq_rope_freqs(64)[0]))" % str(tmp_path)
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["32"], r.stderr[-2000:]

@@ -92,7 +92,10 @@ def _load_hip_runtime():
     spec = importlib.util.find_spec("torch")
     path = spec and spec.origin and os.path.join(os.path.dirname(spec.origin), "lib", "libamdhip64.so")
     if path and os.path.exists(path):
-        ctypes.CDLL(path)
+        try:
+            ctypes.CDLL(path)
+        except OSError:
+            pass  # a torch that cannot be loaded: the host entry points need none
 
 
 def lib() -> ctypes.CDLL:
