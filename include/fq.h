@@ -411,6 +411,93 @@ fq_status fq_rope(const void* x_bf16, int64_t x_token, int64_t x_head, int32_t M
                   const int32_t* positions, int32_t pos0, int32_t inverse, void* y_bf16, int64_t y_token,
                   int64_t y_head, void* stream);
 
+/* ------------------------------------------------------------------ from the qkv site to the o site
+ *
+ * Heads are addressed as in fq_rope: element d of head h of token m is
+ * t[m * t_token + h * t_head + d], strides multiples of 8 and at least head_dim
+ * (a row-major output has t_token = ld, t_head = head_dim, the head layout
+ * t_token = head_dim, t_head = M * head_dim).  Outputs' heads do not overlap, and
+ * outputs overlap no input unless a call allows it.
+ *
+ * Norm of the query and key heads and their rotation in one pass.  Of every
+ * token heads 0 .. q_heads - 1 take q_gamma, the k_heads behind them k_gamma,
+ * the others are copied (values):
+ *   n = x * (1/sqrt(mean(x^2) + eps)) * gamma      over the head's head_dim values; gamma NULL: unit gain
+ *   y = fq_rope's rotation of n                    rot_dim 0: y = n (freq may be NULL)
+ * float32 arithmetic with one rounding to bf16 (none between norm and rotation).
+ * head_dim is a multiple of 16, at most 256; rot_dim even, 0 <= rot_dim <=
+ * head_dim; freq, attn_scale, positions, pos0, interleaved, strides and an output
+ * over its input as in fq_rope.  Gains are float32 [head_dim]. */
+fq_status fq_qk_norm_rope(const void* x_bf16, int64_t x_token, int64_t x_head, int32_t M, int32_t heads,
+                          int32_t q_heads, int32_t k_heads, int32_t head_dim, const float* q_gamma,
+                          const float* k_gamma, float eps, int32_t rot_dim, int32_t interleaved, const uint64_t* freq,
+                          float attn_scale, const int32_t* positions, int32_t pos0, void* y_bf16, int64_t y_token,
+                          int64_t y_head, void* stream);
+
+/* Paged cache of keys and values.  A page holds page_size consecutive tokens (a
+ * multiple of 16, at most 32768) of one sequence for every kv head:
+ *   k_cache, v_cache  [pages][kv_heads][page_size][head_dim]: bf16 (kv_bits 16) or e4m3 codes (kv_bits 8)
+ *   k_scale, v_scale  float32 [pages][kv_heads][page_size] with kv_bits 8, NULL with 16
+ * head_dim is a multiple of 16, at most 256; pages * page_size < 2^31.  Codes of
+ * a token's head are made as in fq_fp8_prologue, its head_dim values sharing one
+ * scale: s = max|h| / 448, q = e4m3(h / s).  All buffers are 16-byte aligned.
+ *
+ * fq_kv_write stores token m at slot slots[m] = page * page_size + its place in
+ * the page (device int32 [M]); a token whose slot is negative or past the last
+ * page is left out, everything else of the cache stays as it is.  The slots of a
+ * call's tokens differ: of two tokens with one slot either may be stored, each of
+ * its pieces of 16 or 8 bytes from either. */
+fq_status fq_kv_write(const void* k_bf16, int64_t k_token, int64_t k_head, const void* v_bf16, int64_t v_token,
+                      int64_t v_head, const int32_t* slots, int32_t M, int32_t kv_heads, int32_t head_dim,
+                      int32_t kv_bits, int32_t pages, int32_t page_size, void* k_cache, void* v_cache, float* k_scale,
+                      float* v_scale, void* stream);
+
+/* Tokens at slots[m] read back into bf16 heads, bf16_rne(s q) of codes; zeros
+ * for a slot that is negative or past the last page. */
+fq_status fq_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                     int32_t kv_bits, int32_t pages, int32_t page_size, const int32_t* slots, int32_t M,
+                     int32_t kv_heads, int32_t head_dim, void* k_bf16, int64_t k_token, int64_t k_head, void* v_bf16,
+                     int64_t v_token, int64_t v_head, void* stream);
+
+/* Attention of whole prompts, packed one behind another:
+ *   o[i][h] = sum_j p_ij v[j][h'] / sum_j p_ij,  p_ij = exp(scale * <q[i][h], k[j][h']> - max_j),  h' = h / (q_heads / kv_heads)
+ * Sequence s has the queries cu_q[s] .. cu_q[s + 1] - 1 of q's M rows and the keys
+ * cu_k[s] .. cu_k[s + 1] - 1 of the M_k rows of k and v (cu_k NULL: those of cu_q).
+ * With causal = 1 query i of L_q sees the keys j <= i + L_k - L_q, so that the last
+ * query sees all keys (a prompt that continues a cached prefix); a query that sees
+ * none gets zeros.  Rows of o outside every sequence stay as they are.
+ *   cu_q, cu_k  device int32 [seqs + 1], not decreasing, within [0, M] and [0, M_k] (what
+ *               lies outside is cut off)
+ * head_dim is a multiple of 16, at most 256; kv_heads divides q_heads; k_token and
+ * v_token are at most 2^24; scale is finite.  Scores, maximum and sums are float32, the weights p of a product are
+ * rounded to bf16, as its operand; one rounding to bf16 at the end.  k and v must be
+ * finite within a sequence; rows outside of it may hold anything. */
+fq_status fq_attn_prefill(const void* q_bf16, int64_t q_token, int64_t q_head, const void* k_bf16, int64_t k_token,
+                          int64_t k_head, const void* v_bf16, int64_t v_token, int64_t v_head, int32_t M, int32_t M_k,
+                          const int32_t* cu_q, const int32_t* cu_k, int32_t seqs, int32_t q_heads, int32_t kv_heads,
+                          int32_t head_dim, float scale, int32_t causal, void* o_bf16, int64_t o_token, int64_t o_head,
+                          void* stream);
+
+/* Attention of one new token of each sequence over the paged cache (its own key
+ * and value already written): row s of q sees the first lens[s] tokens of
+ * sequence s, token j of which is in page page_table[s][j / page_size].
+ *   page_table  device int32 [seqs][max_pages]; tokens of a page outside [0, pages) are not seen
+ *   lens        device int32 [seqs]; more than max_pages * page_size counts as that, fewer than 1 as none
+ * A row that sees no token gets zeros.  What the cache holds behind a sequence's
+ * last token does not matter.  max_pages * page_size <= 2^30; other rules as in
+ * fq_attn_prefill and fq_kv_write.  A code's value times its scale is never rounded:
+ * the key's scale multiplies the score, the value's the weight p.
+ * workspace: at least fq_attn_decode_workspace_bytes(seqs, q_heads, kv_heads, head_dim,
+ * max_pages * page_size) bytes (never fewer for more sequences or tokens), 256-byte
+ * aligned; the parts of a long sequence meet there.  It belongs to one call at a time,
+ * and needs no contents before the call. */
+size_t fq_attn_decode_workspace_bytes(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_len);
+fq_status fq_attn_decode(const void* q_bf16, int64_t q_token, int64_t q_head, int32_t seqs, int32_t q_heads,
+                         int32_t kv_heads, int32_t head_dim, float scale, const void* k_cache, const void* v_cache,
+                         const float* k_scale, const float* v_scale, int32_t kv_bits, int32_t pages, int32_t page_size,
+                         const int32_t* page_table, int32_t max_pages, const int32_t* lens, void* o_bf16,
+                         int64_t o_token, int64_t o_head, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

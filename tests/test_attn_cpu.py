@@ -1,0 +1,231 @@
+"""The operators between the qkv site and the o site without a GPU: refusals, sizes, and where the paged cache's reads
+go, for every lane of a decode call."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import w4a4_integer_gemm_amd as fq
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "w4a4_integer_gemm_amd", "csrc")
+DEV, BAD = 0x10000, 0x10004  # "device pointers", aligned and not; validation never reads them
+ARG, SHAPE, UNSUPPORTED, ALIGN = 1, 2, 3, 4
+NAN, INF = float("nan"), float("inf")
+
+
+def norm(x=DEV, xt=512, xh=64, M=8, heads=8, q=4, k=2, D=64, gq=DEV, gk=DEV, eps=1e-6, rot=64, inter=0, freq=DEV, att=1.0, pos=DEV,
+         pos0=0, y=2 * DEV, yt=512, yh=64):
+    return fq.lib().fq_qk_norm_rope(x, xt, xh, M, heads, q, k, D, gq, gk, eps, rot, inter, freq, att, pos, pos0, y, yt, yh, None)
+
+
+@pytest.mark.parametrize("kw,code,text", [
+    (dict(x=None), ARG, "x_bf16 is NULL"), (dict(y=None), ARG, "y_bf16 is NULL"), (dict(freq=None), ARG, "freq is NULL"),
+    (dict(M=0), SHAPE, "M=0"), (dict(M=2 ** 31 - 1), SHAPE, "M=2147483647"), (dict(M=2 ** 26), SHAPE, "too large for one launch"),
+    (dict(D=24), SHAPE, "head_dim=24"), (dict(D=8), SHAPE, "head_dim=8"), (dict(D=272), SHAPE, "head_dim=272"),
+    (dict(heads=0, q=0, k=0), SHAPE, "heads=0"), (dict(heads=70000), SHAPE, "heads=70000"),
+    (dict(q=-1), SHAPE, "q_heads=-1"), (dict(k=-1), SHAPE, "k_heads=-1"), (dict(q=7, k=2), SHAPE, "at most heads=8"),
+    (dict(q=2 ** 31 - 1, k=2 ** 31 - 1), SHAPE, "at most heads=8"),
+    (dict(eps=-1.0), ARG, "eps=-1"), (dict(eps=NAN), ARG, "eps=nan"), (dict(rot=66), SHAPE, "rot_dim=66"),
+    (dict(rot=7), SHAPE, "rot_dim=7"), (dict(rot=-2), SHAPE, "rot_dim=-2"), (dict(inter=2), ARG, "interleaved=2"),
+    (dict(att=INF), ARG, "attn_scale=inf"), (dict(pos=None, pos0=2 ** 31 - 5), ARG, "passes the last position"),
+    (dict(xt=56), SHAPE, "x_token=56 < head_dim=64"), (dict(xh=68), ALIGN, "x_head=68 is not a multiple of 8"),
+    (dict(yt=64, yh=64), SHAPE, "make 8 heads of 8 tokens overlap"), (dict(x=BAD), ALIGN, "x_bf16"), (dict(y=BAD), ALIGN, "y_bf16"),
+    (dict(y=DEV, yt=520), SHAPE, "in place"), (dict(gq=BAD), ALIGN, "q_gamma"), (dict(gk=BAD), ALIGN, "k_gamma"),
+    (dict(freq=BAD), ALIGN, "freq"), (dict(pos=DEV + 2), ALIGN, "positions"),
+])
+def test_qk_norm_rope_refuses(kw, code, text):
+    assert norm(**kw) == code and text in fq.last_error(), fq.last_error()
+
+
+def write(k=DEV, kt=256, kh=64, v=DEV, vt=256, vh=64, slots=DEV, M=8, kv=4, D=64, bits=8, pages=10, page=16, kc=DEV, vc=DEV, ks=DEV,
+          vs=DEV):
+    return fq.lib().fq_kv_write(k, kt, kh, v, vt, vh, slots, M, kv, D, bits, pages, page, kc, vc, ks, vs, None)
+
+
+def read(k=DEV, kt=256, kh=64, v=2 * DEV, vt=256, vh=64, slots=DEV, M=8, kv=4, D=64, bits=8, pages=10, page=16, kc=DEV, vc=DEV,
+         ks=DEV, vs=DEV):
+    return fq.lib().fq_kv_read(kc, vc, ks, vs, bits, pages, page, slots, M, kv, D, k, kt, kh, v, vt, vh, None)
+
+
+CACHE = [
+    (dict(kc=None), ARG, "k_cache is NULL"), (dict(vc=None), ARG, "v_cache is NULL"), (dict(bits=4), UNSUPPORTED, "kv_bits=4"),
+    (dict(ks=None), ARG, "kv_bits=8 needs"), (dict(vs=None), ARG, "kv_bits=8 needs"), (dict(bits=16), ARG, "kv_bits=16 takes no"),
+    (dict(D=72), SHAPE, "head_dim=72"), (dict(kv=0), SHAPE, "kv_heads=0"), (dict(kv=40000), SHAPE, "kv_heads=40000"),
+    (dict(page=8), SHAPE, "page_size=8"), (dict(page=40), SHAPE, "page_size=40"), (dict(page=65536), SHAPE, "page_size=65536"),
+    (dict(pages=0), SHAPE, "pages=0"), (dict(pages=1 << 27), SHAPE, "fewer than 2^31 tokens"), (dict(kc=BAD), ALIGN, "k_cache"),
+    (dict(vc=BAD), ALIGN, "v_cache"), (dict(ks=BAD), ALIGN, "k_scale"), (dict(vs=BAD), ALIGN, "v_scale"),
+]
+ROWS = [
+    (dict(M=0), SHAPE, "M=0"), (dict(M=2 ** 31 - 600), SHAPE, "too large for one launch"), (dict(slots=None), ARG, "slots is NULL"),
+    (dict(slots=DEV + 2), ALIGN, "slots"), (dict(k=None), ARG, "k_bf16 is NULL"), (dict(v=None), ARG, "v_bf16 is NULL"),
+    (dict(kt=56), SHAPE, "k_token=56"), (dict(vh=60), SHAPE, "v_head=60"), (dict(vt=260), ALIGN, "v_token=260"),
+    (dict(k=BAD), ALIGN, "k_bf16"), (dict(v=BAD), ALIGN, "v_bf16"),
+]
+
+
+@pytest.mark.parametrize("call", [write, read])
+@pytest.mark.parametrize("kw,code,text", CACHE + ROWS)
+def test_cache_calls_refuse(call, kw, code, text):
+    assert call(**kw) == code and text in fq.last_error(), fq.last_error()
+
+
+@pytest.mark.parametrize("kw,code,text", [(dict(kt=64), SHAPE, "overlap"), (dict(vt=128), SHAPE, "overlap"),
+                                          (dict(v=DEV), ARG, "k_bf16 and v_bf16 are the same")])
+def test_cache_read_refuses_outputs(kw, code, text):
+    assert read(**kw) == code and text in fq.last_error(), fq.last_error()
+
+
+def prefill(q=DEV, qt=512, qh=64, k=DEV, kt=128, kh=64, v=DEV, vt=128, vh=64, M=100, Mk=100, cu=DEV, cuk=None, seqs=3, H=8, kv=2, D=64,
+            scale=0.125, causal=1, o=2 * DEV, ot=512, oh=64):
+    return fq.lib().fq_attn_prefill(q, qt, qh, k, kt, kh, v, vt, vh, M, Mk, cu, cuk, seqs, H, kv, D, scale, causal, o, ot, oh, None)
+
+
+@pytest.mark.parametrize("kw,code,text", [
+    (dict(q=None), ARG, "q_bf16 is NULL"), (dict(k=None), ARG, "k_bf16 is NULL"), (dict(v=None), ARG, "v_bf16 is NULL"),
+    (dict(o=None), ARG, "o_bf16 is NULL"), (dict(cu=None), ARG, "cu_q is NULL"), (dict(M=0), SHAPE, "M=0"), (dict(Mk=0), SHAPE, "M_k=0"),
+    (dict(M=2 ** 31 - 1), SHAPE, "M=2147483647"), (dict(Mk=2 ** 31 - 1), SHAPE, "M_k=2147483647"), (dict(seqs=0), SHAPE, "seqs=0"),
+    (dict(seqs=2 ** 21), SHAPE, "seqs=2097152"), (dict(M=2 ** 30), SHAPE, "too many for one launch"),
+    (dict(H=0), SHAPE, "q_heads=0"), (dict(H=65536), SHAPE, "q_heads=65536"), (dict(kv=0), SHAPE, "kv_heads=0"),
+    (dict(kv=3), SHAPE, "whole number of groups"), (dict(kv=16), SHAPE, "whole number of groups"), (dict(D=40), SHAPE, "head_dim=40"),
+    (dict(D=512), SHAPE, "head_dim=512"), (dict(scale=INF), ARG, "scale=inf"), (dict(scale=NAN), ARG, "scale=nan"),
+    (dict(causal=2), ARG, "causal=2"), (dict(qt=8), SHAPE, "q_token=8"), (dict(kh=72, D=64, kt=68), ALIGN, "k_token=68"),
+    (dict(vt=1 << 25), SHAPE, "at most 2^24"), (dict(kt=(1 << 24) + 8), SHAPE, "at most 2^24"), (dict(ot=64), SHAPE, "overlap"),
+    (dict(q=BAD), ALIGN, "q_bf16"), (dict(k=BAD), ALIGN, "k_bf16"), (dict(v=BAD), ALIGN, "v_bf16"), (dict(o=BAD), ALIGN, "o_bf16"),
+    (dict(cu=DEV + 1), ALIGN, "cu_q"), (dict(cuk=DEV + 2), ALIGN, "cu_k"),
+])
+def test_prefill_refuses(kw, code, text):
+    assert prefill(**kw) == code and text in fq.last_error(), fq.last_error()
+
+
+def decode(q=DEV, qt=512, qh=64, seqs=3, H=8, kv=2, D=64, scale=0.125, kc=DEV, vc=DEV, ks=DEV, vs=DEV, bits=8, pages=10, page=16,
+           table=DEV, width=4, lens=DEV, o=2 * DEV, ot=512, oh=64, ws=DEV, nbytes=1 << 30):
+    return fq.lib().fq_attn_decode(q, qt, qh, seqs, H, kv, D, scale, kc, vc, ks, vs, bits, pages, page, table, width, lens, o, ot, oh,
+                                   ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw,code,text", CACHE + [
+    (dict(q=None), ARG, "q_bf16 is NULL"), (dict(o=None), ARG, "o_bf16 is NULL"), (dict(table=None), ARG, "page_table is NULL"),
+    (dict(lens=None), ARG, "lens is NULL"), (dict(ws=None), ARG, "workspace is NULL"), (dict(ws=DEV + 16), ALIGN, "256-byte"),
+    (dict(nbytes=100), ARG, "workspace_bytes=100 <"), (dict(seqs=0), SHAPE, "seqs=0"), (dict(seqs=2 ** 24), SHAPE, "too many for one launch"),
+    (dict(H=7), SHAPE, "whole number of groups"), (dict(width=0), SHAPE, "max_pages=0"), (dict(width=1 << 27), SHAPE, "at most 2^30"),
+    (dict(scale=NAN), ARG, "scale=nan"), (dict(table=DEV + 2), ALIGN, "page_table"), (dict(lens=DEV + 2), ALIGN, "lens"),
+    (dict(ot=64), SHAPE, "overlap"), (dict(qt=60), SHAPE, "q_token=60"), (dict(q=BAD), ALIGN, "q_bf16"), (dict(o=BAD), ALIGN, "o_bf16"),
+])
+def test_decode_refuses(kw, code, text):
+    assert decode(**kw) == code and text in fq.last_error(), fq.last_error()
+
+
+@pytest.mark.parametrize("call", [norm, write, read, prefill, decode])
+def test_good_arguments_reach_the_device(call):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are none of this device's")
+    assert call() == 5, fq.last_error()
+
+
+def test_decode_workspace_never_shrinks():
+    size = fq.fq_attn_decode_workspace_bytes
+    for H, kv, D in ((1, 1, 16), (28, 4, 128), (8, 1, 256), (40, 2, 80), (64, 64, 64)):
+        for seqs in (1, 2, 3, 7, 64, 127, 128, 129, 300, 5000):
+            last = 0
+            for n in (1, 16, 127, 128, 129, 1000, 4096, 100000, 1 << 20, 1 << 30):
+                now = size(seqs, H, kv, D, n)
+                assert now >= last and now % 256 == 0 and now >= seqs * H * (D + 2) * 4
+                assert size(seqs + 1, H, kv, D, n) >= now
+                last = now
+    assert size(0, 8, 2, 64, 10) == 0 and size(1, 8, 3, 64, 10) == 0 and size(1, 8, 2, 20, 10) == 0 and size(1, 8, 2, 64, 0) == 0
+    assert size(1, 8, 2, 64, (1 << 30) + 1) == 0
+
+
+SRC = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+#include "fq_paged.h"
+using namespace fq;
+
+int main() {
+    long units = 0, wrong = 0;
+    srand(1);
+    // pages by multiplication
+    for (int ps = 16; ps <= 32768; ps += 16) {
+        const uint64_t magic = paged_magic(ps);
+        const int most = kDecodeMaxLen;
+        for (int k = 0; k < 400; ++k) {
+            long t = k < 200 ? long(k) * ps / 16 / 16 * 16 : (long(rand()) << 10 ^ rand()) % most;
+            if (k % 4 == 1) t = long(ps) * (k + rand() % (most / ps - k > 0 ? most / ps - k : 1));
+            if (k % 4 == 2) t = long(ps) * (1 + rand() % (most / ps)) - 16;
+            if (k % 4 == 3) t = most - 16 * (1 + k / 4);
+            if (t < 0 || t >= most) continue;
+            t = t / 16 * 16;
+            wrong += paged_entry(int(t), most, magic) != t / ps;
+            wrong += paged_entry(most - 1, most, magic) != (most - 1) / ps;
+            wrong += paged_entry(int(t) + 64 < most ? int(t) + 64 : int(t), int(t) + 1, magic) != t / ps;
+        }
+    }
+    // every token of a sequence in one part, one wave, one tile; every row inside the cache
+    const int lens[] = {-5, 0, 1, 15, 16, 17, 31, 33, 127, 128, 129, 500, 1023, 2000, 3001, 4097};
+    const int sizes[] = {16, 48, 64, 112, 256};
+    for (int ps : sizes)
+        for (int want : lens)
+            for (int64_t pairs : {1, 3, 100, 1024, 5000}) {
+                const int max_pages = 4097 / ps + 1, pages = 7, kv_heads = 3;
+                const int len = paged_len(want, max_pages, ps);
+                if (len < 0 || len > max_pages * ps || (want > 0 && want <= max_pages * ps && len != want)) ++wrong;
+                const int splits = decode_splits(pairs, max_pages * ps);
+                if (splits < 1 || splits > kDecodeWgs) ++wrong;
+                const DecodeParts parts = decode_parts(len, splits);
+                if (parts.count > splits || (len > 0) != (parts.count > 0)) ++wrong;
+                std::vector<int> table(max_pages), seen(len, 0);
+                for (int& p : table) p = rand() % (pages + 4) - 2;  // some outside the cache
+                const uint64_t magic = paged_magic(ps);
+                for (int split = 0; split < parts.count; ++split) {
+                    const int begin = split * parts.len, end = begin + parts.len < len ? begin + parts.len : len;
+                    for (int wave = 0; wave < kDecodeWaves; ++wave)
+                        for (int t = begin + kDecodeTile * wave; t < end; t += kDecodeTile * kDecodeWaves)
+                            for (int i = 0; i < 2; ++i, ++units) {
+                                const int ti = t + kDecodeUnit * i, entry = paged_entry(ti, len, magic);
+                                if (entry < 0 || entry >= max_pages) { ++wrong; continue; }
+                                const PagedUnit u = paged_unit(table[entry], entry, ti, len, pages, ps);
+                                // 16 rows are read, whatever is valid
+                                const int64_t rows = int64_t(pages) * kv_heads * ps;
+                                for (int h = 0; h < kv_heads; ++h) {
+                                    const int64_t row = paged_row(u.page, u.first, h, kv_heads, ps);
+                                    if (row < 0 || row + kDecodeUnit > rows || u.first + kDecodeUnit > ps || u.first % 4) ++wrong;
+                                }
+                                for (int j = 0; j < kDecodeUnit; ++j) {
+                                    const int tok = ti + j, p = tok < len ? table[tok / ps] : -1;
+                                    const bool there = tok < len && p >= 0 && p < pages;
+                                    if (there != (j < u.valid)) ++wrong;
+                                    if (there && (u.page != p || u.first + j != tok % ps)) ++wrong;
+                                    if (tok < len) ++seen[tok];
+                                }
+                            }
+                }
+                for (int n : seen) wrong += n != 1;
+            }
+    // parts fit the workspace
+    for (int seqs : {1, 2, 7, 64, 1000})
+        for (int kv : {1, 2, 8})
+            for (int group : {1, 7, 16, 17, 40})
+                for (int max_len : {16, 128, 129, 4096, 1 << 20, 1 << 30}) {
+                    const int64_t pairs = int64_t(seqs) * kv * ((group + kDecodeHeads - 1) / kDecodeHeads);
+                    const int splits = decode_splits(pairs, max_len);
+                    if (decode_part_rows(seqs, kv * group, kv, max_len) < size_t(seqs) * kv * group * splits) ++wrong;
+                }
+    printf("%ld %ld\n", units, wrong);
+    return 0;
+}
+"""
+
+
+def test_paged_reads_stay_inside_the_cache_and_cover_every_token_once(tmp_path):
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no g++")
+    src, exe = tmp_path / "paged.cpp", tmp_path / "paged"
+    src.write_text(SRC)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", f"-I{CSRC}", str(src), "-o", str(exe)], check=True)
+    units, wrong = (int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split())
+    assert units > 10000 and wrong == 0

@@ -67,6 +67,17 @@ SIGNATURES = {
                       ctypes.c_int),
     "fq_rope": ([_P, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _P, _F, _P, _I32, _I32, _P, _I64, _I64, _P],
                 ctypes.c_int),
+    "fq_qk_norm_rope": ([_P, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _F, _I32, _I32, _P, _F, _P, _I32, _P, _I64,
+                         _I64, _P], ctypes.c_int),
+    "fq_kv_write": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P],
+                    ctypes.c_int),
+    "fq_kv_read": ([_P, _P, _P, _P, _I32, _I32, _I32, _P, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P],
+                   ctypes.c_int),
+    "fq_attn_prefill": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _P, _I32, _I32, _I32, _I32, _F,
+                         _I32, _P, _I64, _I64, _P], ctypes.c_int),
+    "fq_attn_decode_workspace_bytes": ([_I32, _I32, _I32, _I32, _I32], _SZ),
+    "fq_attn_decode": ([_P, _I64, _I64, _I32, _I32, _I32, _I32, _F, _P, _P, _P, _P, _I32, _I32, _I32, _P, _I32, _P, _P,
+                        _I64, _I64, _P, _SZ, _P], ctypes.c_int),
 }
 
 
@@ -343,3 +354,46 @@ def fq_rope(x, x_token: int, x_head: int, M: int, heads: int, rot_heads: int, he
             stream=None):
     _check(lib().fq_rope(_dptr(x), x_token, x_head, M, heads, rot_heads, head_dim, rot_dim, interleaved, _dptr(freq),
                          attn_scale, _dptr(positions), pos0, inverse, _dptr(y), y_token, y_head, _stream(stream)))
+
+
+def fq_qk_norm_rope(x, x_token: int, x_head: int, M: int, heads: int, q_heads: int, k_heads: int, head_dim: int, q_gamma,
+                    k_gamma, eps: float, rot_dim: int, interleaved: int, freq, attn_scale: float, positions, pos0: int, y,
+                    y_token: int, y_head: int, stream=None):
+    _check(lib().fq_qk_norm_rope(_dptr(x), x_token, x_head, M, heads, q_heads, k_heads, head_dim, _dptr(q_gamma),
+                                 _dptr(k_gamma), eps, rot_dim, interleaved, _dptr(freq), attn_scale, _dptr(positions), pos0,
+                                 _dptr(y), y_token, y_head, _stream(stream)))
+
+
+def fq_kv_write(k, k_token: int, k_head: int, v, v_token: int, v_head: int, slots, M: int, kv_heads: int, head_dim: int,
+                kv_bits: int, pages: int, page_size: int, k_cache, v_cache, k_scale, v_scale, stream=None):
+    _check(lib().fq_kv_write(_dptr(k), k_token, k_head, _dptr(v), v_token, v_head, _dptr(slots), M, kv_heads, head_dim,
+                             kv_bits, pages, page_size, _dptr(k_cache), _dptr(v_cache), _dptr(k_scale), _dptr(v_scale),
+                             _stream(stream)))
+
+
+def fq_kv_read(k_cache, v_cache, k_scale, v_scale, kv_bits: int, pages: int, page_size: int, slots, M: int, kv_heads: int,
+               head_dim: int, k, k_token: int, k_head: int, v, v_token: int, v_head: int, stream=None):
+    _check(lib().fq_kv_read(_dptr(k_cache), _dptr(v_cache), _dptr(k_scale), _dptr(v_scale), kv_bits, pages, page_size,
+                            _dptr(slots), M, kv_heads, head_dim, _dptr(k), k_token, k_head, _dptr(v), v_token, v_head,
+                            _stream(stream)))
+
+
+def fq_attn_prefill(q, q_token: int, q_head: int, k, k_token: int, k_head: int, v, v_token: int, v_head: int, M: int,
+                    M_k: int, cu_q, cu_k, seqs: int, q_heads: int, kv_heads: int, head_dim: int, scale: float, causal: int,
+                    o, o_token: int, o_head: int, stream=None):
+    _check(lib().fq_attn_prefill(_dptr(q), q_token, q_head, _dptr(k), k_token, k_head, _dptr(v), v_token, v_head, M, M_k,
+                                 _dptr(cu_q), _dptr(cu_k), seqs, q_heads, kv_heads, head_dim, scale, causal, _dptr(o),
+                                 o_token, o_head, _stream(stream)))
+
+
+def fq_attn_decode_workspace_bytes(seqs: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int) -> int:
+    return lib().fq_attn_decode_workspace_bytes(seqs, q_heads, kv_heads, head_dim, max_len)
+
+
+def fq_attn_decode(q, q_token: int, q_head: int, seqs: int, q_heads: int, kv_heads: int, head_dim: int, scale: float,
+                   k_cache, v_cache, k_scale, v_scale, kv_bits: int, pages: int, page_size: int, page_table, max_pages: int,
+                   lens, o, o_token: int, o_head: int, workspace, workspace_bytes: int, stream=None):
+    _check(lib().fq_attn_decode(_dptr(q), q_token, q_head, seqs, q_heads, kv_heads, head_dim, scale, _dptr(k_cache),
+                                _dptr(v_cache), _dptr(k_scale), _dptr(v_scale), kv_bits, pages, page_size,
+                                _dptr(page_table), max_pages, _dptr(lens), _dptr(o), o_token, o_head, _dptr(workspace),
+                                workspace_bytes, _stream(stream)))

@@ -25,7 +25,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libfq_san.so")
 ORACLE_LIB = os.path.join(ROOT, "oracle", "liboracle_san.so")
 SAN = ["-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer", "-g"]
-HOST_SOURCES = ["fq_api.cpp", "fq_pack.cpp", "fq_api_block.cpp", "fq_fp8_pack.cpp", "fq_rope_plan.cpp"]
+HOST_SOURCES = ["fq_api.cpp", "fq_pack.cpp", "fq_api_block.cpp", "fq_fp8_pack.cpp", "fq_rope_plan.cpp",
+                "fq_api_attn.cpp"]
 # the library's kernels, as the ordinary build compiled them (its list of sources)
 sys.path.insert(0, ROOT)
 from w4a4_integer_gemm_amd.build import SOURCES as _LIB_SOURCES  # noqa: E402

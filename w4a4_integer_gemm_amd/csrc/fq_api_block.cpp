@@ -13,32 +13,6 @@
 
 namespace {
 
-constexpr int64_t kMaxThreads = int64_t(1) << 32;  // of one launch, along x
-constexpr int32_t kMaxM = INT32_MAX - 512;         // (rounded up to whole tiles it is an int32 still)
-
-fq_status check_eps(const char* fn, const char* name, float eps) {
-    if (!(eps >= 0.0f && eps < 1e30f))
-        return fail(FQ_ERR_ARG, fmt("%s: %s=%g must be finite and >= 0", fn, name, double(eps)));
-    return FQ_OK;
-}
-
-// Rows of `width` elements with leading dimension ld (a multiple of `mult`
-// elements, 16 bytes) and a 16-byte aligned base.
-fq_status check_rows(const char* fn, const char* name, const char* ld_name, const void* p, int64_t ld, int64_t width,
-                     int mult) {
-    if (ld < width) return fail(FQ_ERR_SHAPE, fmt("%s: %s=%lld < %lld", fn, ld_name, (long long)ld, (long long)width));
-    if (ld % mult)
-        return fail(FQ_ERR_ALIGN, fmt("%s: %s=%lld is not a multiple of %d elements (16 bytes)", fn, ld_name,
-                                      (long long)ld, mult));
-    if (!aligned(p, 16)) return fail(FQ_ERR_ALIGN, fmt("%s: %s is not 16-byte aligned", fn, name));
-    return FQ_OK;
-}
-
-fq_status check_vector(const char* fn, const char* name, const void* p) {
-    if (p && !aligned(p, 16)) return fail(FQ_ERR_ALIGN, fmt("%s: %s is not 16-byte aligned", fn, name));
-    return FQ_OK;
-}
-
 // One workgroup per row.
 fq_status check_norm_launch(const char* fn, int32_t M, int32_t K, bool f32) {
     if (int64_t(M) * fq::block_norm_threads(K, M, f32) >= kMaxThreads)
@@ -48,11 +22,6 @@ fq_status check_norm_launch(const char* fn, int32_t M, int32_t K, bool f32) {
 }
 
 size_t scale_bytes(int32_t M, int32_t K) { return size_t(K / 128) * size_t(fq::fp8_scale_ld(M)) * sizeof(float); }
-
-fq_status check_m(const char* fn, int32_t M) {
-    if (M < 1 || M > kMaxM) return fail(FQ_ERR_SHAPE, fmt("%s: M=%d must be in [1, %d]", fn, M, kMaxM));
-    return FQ_OK;
-}
 
 fq_status validate_fp8_prologue(const char* fn, const void* x, int32_t M, int32_t K, int64_t ldx, const float* gamma,
                                 float eps, const void* codes, const float* scale) {
@@ -286,20 +255,9 @@ fq_status fq_rope(const void* x_bf16, int64_t x_token, int64_t x_head, int32_t M
         return fail(FQ_ERR_ARG, fmt("%s: attn_scale=%g must be finite", fn, double(attn_scale)));
     if (!positions && int64_t(pos0) + M - 1 > INT32_MAX)
         return fail(FQ_ERR_ARG, fmt("%s: pos0=%d + M=%d passes the last position 2^31 - 1", fn, pos0, M));
-    struct {
-        const char* name;
-        int64_t v;
-    } strides[4] = {{"x_token", x_token}, {"x_head", x_head}, {"y_token", y_token}, {"y_head", y_head}};
-    for (const auto& s : strides) {
-        if (s.v < head_dim)
-            return fail(FQ_ERR_SHAPE, fmt("%s: %s=%lld < head_dim=%d", fn, s.name, (long long)s.v, head_dim));
-        if (s.v % 8) return fail(FQ_ERR_ALIGN, fmt("%s: %s=%lld is not a multiple of 8 bf16", fn, s.name, (long long)s.v));
-    }
-    // y's heads must not overlap: all heads of a token inside its stride, or all tokens of a head inside the head's
-    using wide = __int128;
-    if (wide(y_token) < wide(heads - 1) * y_head + head_dim && wide(y_head) < wide(M - 1) * y_token + head_dim)
-        return fail(FQ_ERR_SHAPE, fmt("%s: y_token=%lld and y_head=%lld make %d heads of %d tokens overlap", fn,
-                                      (long long)y_token, (long long)y_head, heads, M));
+    FQ_TRY(check_head_strides(fn, "x_token", x_token, "x_head", x_head, head_dim));
+    FQ_TRY(check_head_strides(fn, "y_token", y_token, "y_head", y_head, head_dim));
+    FQ_TRY(check_heads_apart(fn, "y_token", y_token, "y_head", y_head, heads, M, head_dim));
     if (x_bf16 == y_bf16 && (x_token != y_token || x_head != y_head))
         return fail(FQ_ERR_SHAPE, fmt("%s: a rotation in place needs the strides of x and y equal", fn));
     FQ_TRY(check_vector(fn, "x_bf16", x_bf16));

@@ -1,0 +1,51 @@
+// Pieces shared by the attention kernels (gfx950, wave64): matrix instructions
+// on bf16, lane exchanges, the softmax's base.
+//
+// Scores are kept in the base of two: p = 2^(s - max), s = scale log2(e) <q, k>.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fq_device.h"
+
+namespace fq {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 0x1.715476p+0f;
+
+// D[16][16] (+)= A[16][32] B[32][16]: lane l gives row (column) l % 16 and the same
+// 8 of the 32 k on both sides, and holds D[4 (l / 16) + i][l % 16] in register i.
+__device__ __forceinline__ v4f mfma_bf16_16(v8bf a, v8bf b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// D[32][32] (+)= A[32][16] B[16][32]: lane l gives row (column) l % 32 and 8 of the 16
+// k, and holds D[8 (i / 4) + 4 (l / 32) + i % 4][l % 32] in register i.
+__device__ __forceinline__ v16f mfma_bf16_32(v8bf a, v8bf b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ v8bf as_bf(uint4 v) { return __builtin_bit_cast(v8bf, v); }
+
+// The value of lane l xor 32 (16) joined with the own one.
+__device__ __forceinline__ float max_over_halves(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_int(x), __float_as_int(x), false, false);
+    return fmaxf(__int_as_float(a[0]), __int_as_float(a[1]));
+}
+__device__ __forceinline__ float sum_over_halves(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_int(x), __float_as_int(x), false, false);
+    return __int_as_float(a[0]) + __int_as_float(a[1]);
+}
+__device__ __forceinline__ float max_over_rows(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_int(x), __float_as_int(x), false, false);
+    return max_over_halves(fmaxf(__int_as_float(a[0]), __int_as_float(a[1])));
+}
+__device__ __forceinline__ float sum_over_rows(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_int(x), __float_as_int(x), false, false);
+    return sum_over_halves(__int_as_float(a[0]) + __int_as_float(a[1]));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+}  // namespace fq

@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <climits>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -11,6 +12,12 @@
 
 #include "../../include/fq.h"
 #include "fq_internal.h"
+
+#define FQ_TRY(expr)                     \
+    do {                                 \
+        fq_status _s = (expr);           \
+        if (_s != FQ_OK) return _s;      \
+    } while (0)
 
 namespace {
 
@@ -70,15 +77,65 @@ inline fq_status device_status(const char* fn, hipError_t e) {
     return FQ_OK;
 }
 
+constexpr int64_t kMaxThreads = int64_t(1) << 32;  // of one launch, along x
+constexpr int32_t kMaxM = INT32_MAX - 512;         // (rounded up to whole tiles it is an int32 still)
+
+inline fq_status check_eps(const char* fn, const char* name, float eps) {
+    if (!(eps >= 0.0f && eps < 1e30f))
+        return fail(FQ_ERR_ARG, fmt("%s: %s=%g must be finite and >= 0", fn, name, double(eps)));
+    return FQ_OK;
+}
+
+// Rows of `width` elements with leading dimension ld (a multiple of `mult`
+// elements, 16 bytes) and a 16-byte aligned base.
+inline fq_status check_rows(const char* fn, const char* name, const char* ld_name, const void* p, int64_t ld, int64_t width,
+                     int mult) {
+    if (ld < width) return fail(FQ_ERR_SHAPE, fmt("%s: %s=%lld < %lld", fn, ld_name, (long long)ld, (long long)width));
+    if (ld % mult)
+        return fail(FQ_ERR_ALIGN, fmt("%s: %s=%lld is not a multiple of %d elements (16 bytes)", fn, ld_name,
+                                      (long long)ld, mult));
+    if (!aligned(p, 16)) return fail(FQ_ERR_ALIGN, fmt("%s: %s is not 16-byte aligned", fn, name));
+    return FQ_OK;
+}
+
+inline fq_status check_vector(const char* fn, const char* name, const void* p) {
+    if (p && !aligned(p, 16)) return fail(FQ_ERR_ALIGN, fmt("%s: %s is not 16-byte aligned", fn, name));
+    return FQ_OK;
+}
+
+inline fq_status check_m(const char* fn, int32_t M) {
+    if (M < 1 || M > kMaxM) return fail(FQ_ERR_SHAPE, fmt("%s: M=%d must be in [1, %d]", fn, M, kMaxM));
+    return FQ_OK;
+}
+
+// Strides of heads of head_dim values: element d of head h of token m at m * token + h * head + d.
+inline fq_status check_head_strides(const char* fn, const char* token_name, int64_t token, const char* head_name,
+                                    int64_t head, int32_t head_dim) {
+    const struct {
+        const char* name;
+        int64_t v;
+    } strides[2] = {{token_name, token}, {head_name, head}};
+    for (const auto& s : strides) {
+        if (s.v < head_dim)
+            return fail(FQ_ERR_SHAPE, fmt("%s: %s=%lld < head_dim=%d", fn, s.name, (long long)s.v, head_dim));
+        if (s.v % 8) return fail(FQ_ERR_ALIGN, fmt("%s: %s=%lld is not a multiple of 8 bf16", fn, s.name, (long long)s.v));
+    }
+    return FQ_OK;
+}
+
+// Outputs' heads must not overlap: all heads of a token inside its stride, or all tokens of a head inside the head's.
+inline fq_status check_heads_apart(const char* fn, const char* token_name, int64_t token, const char* head_name,
+                                   int64_t head, int32_t heads, int32_t M, int32_t head_dim) {
+    using wide = __int128;
+    if (wide(token) < wide(heads - 1) * head + head_dim && wide(head) < wide(M - 1) * token + head_dim)
+        return fail(FQ_ERR_SHAPE, fmt("%s: %s=%lld and %s=%lld make %d heads of %d tokens overlap", fn, token_name,
+                                      (long long)token, head_name, (long long)head, heads, M));
+    return FQ_OK;
+}
+
 // The device set-up every device entry point runs before it queues anything.
 inline fq_status prepare(const char* fn, const fq::DeviceInfo** info) {
     return device_status(fn, fq::prepare_device(info));
 }
 
 }  // namespace
-
-#define FQ_TRY(expr)                     \
-    do {                                 \
-        fq_status _s = (expr);           \
-        if (_s != FQ_OK) return _s;      \
-    } while (0)

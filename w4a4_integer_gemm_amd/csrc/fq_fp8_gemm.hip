@@ -97,10 +97,7 @@ __device__ __forceinline__ void copy16_buffer(const v4i& rsrc, uint32_t voff, ui
                  : "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_dst)
                  : "memory");
 }
-// 16 or 4 bytes from base + voff.
-__device__ __forceinline__ void copy16_base(const uint8_t* base, uint32_t voff, uint32_t lds_dst) {
-    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds_dst) : "memory");
-}
+// 4 bytes from base + voff.
 __device__ __forceinline__ void copy4_base(const uint8_t* base, uint32_t voff, uint32_t lds_dst) {
     asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds_dst) : "memory");
 }

@@ -211,6 +211,75 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 
+// Norm of query and key heads with their rotation (fq_qk_norm.hip).
+struct QkNormArgs {
+    const uint16_t* x;
+    int64_t x_token, x_head;
+    int32_t M, heads, q_heads, k_heads, head_dim;
+    const float *q_gamma, *k_gamma;  // nullptr: unit gain
+    float eps;
+    int32_t rot_dim, interleaved;  // rot_dim 0: no rotation
+    const uint64_t* freq;
+    float attn_scale;
+    const int32_t* positions;  // nullptr: pos0 + m
+    int32_t pos0;
+    uint16_t* y;
+    int64_t y_token, y_head;
+};
+hipError_t launch_qk_norm(const QkNormArgs& a, hipStream_t stream);
+
+// The paged cache, and the tokens written to it or read from it (fq_kv_cache.hip).
+struct KvCache {
+    void *k, *v;                // bf16 or e4m3 [pages][kv_heads][page_size][head_dim]
+    float *k_scale, *v_scale;   // [pages][kv_heads][page_size]; nullptr: bf16
+    int32_t pages, page_size, kv_heads, head_dim;
+};
+struct KvRows {
+    uint16_t* p;  // (read only by a write into the cache)
+    int64_t token, head;
+};
+hipError_t launch_kv_write(const KvCache& c, const KvRows& k, const KvRows& v, const int32_t* slots, int32_t M,
+                           hipStream_t stream);
+hipError_t launch_kv_read(const KvCache& c, const KvRows& k, const KvRows& v, const int32_t* slots, int32_t M,
+                          hipStream_t stream);
+
+// Attention of packed prompts (fq_attn_prefill.hip).
+struct PrefillArgs {
+    const uint16_t* q;
+    int64_t q_token, q_head;
+    const uint16_t* k;
+    int64_t k_token, k_head;
+    const uint16_t* v;
+    int64_t v_token, v_head;
+    int32_t M, M_k;
+    const int32_t *cu_q, *cu_k;
+    int32_t seqs, q_heads, kv_heads, head_dim;
+    float scale;
+    int32_t causal;
+    uint16_t* o;
+    int64_t o_token, o_head;
+};
+// Query rows of the smallest block, which bounds a launch's workgroups.
+constexpr int kPrefillRows = 128;
+hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t stream);
+
+// Attention of one token per sequence over the paged cache (fq_attn_decode.hip).
+struct DecodeArgs {
+    const uint16_t* q;
+    int64_t q_token, q_head;
+    int32_t seqs, q_heads;
+    float scale;
+    KvCache cache;
+    const int32_t* page_table;
+    int32_t max_pages;
+    const int32_t* lens;
+    uint16_t* o;
+    int64_t o_token, o_head;
+    float* part;  // [seqs][q_heads][splits][head_dim] sums, behind [seqs][q_heads][splits][2] maxima and weights
+    int32_t splits;
+};
+hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t stream);
+
 hipError_t launch_geglu(const uint16_t* gu, int32_t M, int32_t F, int64_t ld_in, uint16_t* h, int64_t ld_out,
                         hipStream_t stream);
 

@@ -1,0 +1,227 @@
+// Norm of the query and key heads of every token and their rotation in one pass (gfx950, wave64).
+//
+//   n = x * (1/sqrt(mean(x^2) + eps)) * gamma,  (a, b) -> (a c - b s, b c + a s)
+//
+// over the head_dim values of a head; heads behind the queries and keys are
+// copied.  Bound by reading and writing the heads once.  As in fq_rope a thread
+// owns one item of one token, two 16-byte pieces: with halves the pieces of 8 `a`
+// elements and of their 8 `b` elements, so that every pair is inside a thread,
+// otherwise two neighbouring pieces.  head_dim / 16 items make a head; they sit
+// in 1 to 16 consecutive lanes (a power of two), which add their sums of squares
+// with lane moves.  A thread computes its item's angles once and applies them to
+// its share of the heads, UN heads' loads ahead of their stores.
+#include <hip/hip_runtime.h>
+
+#include "fq_angle.h"
+#include "fq_device.h"
+#include "fq_internal.h"
+#include "fq_row_norm.h"
+#include "fq_token.h"
+
+namespace fq {
+namespace {
+
+// Sum over L consecutive lanes (a power of two up to 16, aligned).
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+    if constexpr (L > 1) v += __int_as_float(dpp_i<0xB1>(__float_as_int(v)));   // quad_perm [1,0,3,2]
+    if constexpr (L > 2) v += __int_as_float(dpp_i<0x4E>(__float_as_int(v)));   // quad_perm [2,3,0,1]
+    if constexpr (L > 4) v += __int_as_float(dpp_i<0x141>(__float_as_int(v)));  // row_half_mirror
+    if constexpr (L > 8) v += __int_as_float(dpp_i<0x140>(__float_as_int(v)));  // row_mirror
+    return v;
+}
+
+__device__ __forceinline__ float sumsq16(const float (&p)[8], const float (&q)[8]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = __builtin_fmaf(p[j], p[j], s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = __builtin_fmaf(q[j], q[j], s);
+    return s;
+}
+
+__device__ __forceinline__ void load_gain(const float* g, int e, float (&o)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = g ? g[e + j] : 1.0f;
+}
+
+// blockIdx.y: heads [y * share, (y + 1) * share); UN of them at a time.
+// Pieces are whole: rot_dim a multiple of 16 with halves, of 8 interleaved.
+template <bool INTER, int L, int UN>
+__global__ __launch_bounds__(256) void qk_norm_kernel(QkNormArgs a, int share) {
+    const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t m = idx / L;
+    if (m >= uint32_t(a.M)) return;
+    const int items = a.head_dim / 16, rot_items = a.rot_dim / 16;
+    const bool active = int(idx % L) < items;
+    const int item = active ? int(idx % L) : items - 1;  // (the lanes past the last item repeat it and store nothing)
+    // elements of the two pieces
+    const bool halves = !INTER && item < rot_items;
+    const int ea = halves ? 8 * item : 16 * item, eb = halves ? ea + a.rot_dim / 2 : ea + 8;
+    const bool rot_a = INTER ? ea < a.rot_dim : halves, rot_b = INTER ? eb < a.rot_dim : halves;
+    float c[8], s[8];  // of the 8 pairs; interleaved: of the 4 pairs of each piece
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        c[j] = 1.0f, s[j] = 0.0f;
+        if (INTER ? (j < 4 ? rot_a : rot_b) : rot_a) {
+            const int32_t pos = a.positions ? a.positions[m] : a.pos0 + int32_t(m);
+            const int pair = INTER ? 8 * item + j : 8 * item + j;
+            cos_sin_turns(angle(a.freq[pair], pos), &c[j], &s[j]);
+            c[j] *= a.attn_scale;
+            s[j] *= a.attn_scale;
+        }
+    }
+    const int h0 = blockIdx.y * share, h1 = h0 + share < a.heads ? h0 + share : a.heads;
+    const int normed = a.q_heads + a.k_heads;
+    const uint16_t* const xp = a.x + m * a.x_token;
+    uint16_t* const yp = a.y + m * a.y_token;
+    const bool in_place = a.x == a.y;
+    float ga[8], gb[8];
+    bool have_k = h0 >= a.q_heads;
+    load_gain(have_k ? a.k_gamma : a.q_gamma, ea, ga);
+    load_gain(have_k ? a.k_gamma : a.q_gamma, eb, gb);
+    for (int h = h0; h < h1; h += UN) {
+        uint4 u[UN], v[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            const int hk = h + k < h1 ? h + k : h1 - 1;  // (past the share: loaded again, not stored)
+            u[k] = *reinterpret_cast<const uint4*>(xp + hk * a.x_head + ea);
+            v[k] = *reinterpret_cast<const uint4*>(xp + hk * a.x_head + eb);
+        }
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            if (h + k >= h1) break;
+            if (h + k < normed) {
+                if (!have_k && h + k >= a.q_heads) {
+                    have_k = true;
+                    load_gain(a.k_gamma, ea, ga);
+                    load_gain(a.k_gamma, eb, gb);
+                }
+                float p[8], q[8], r[8], t[8];
+                unpack8(u[k], p);
+                unpack8(v[k], q);
+                const float ss = lanes_sum<L>(active ? sumsq16(p, q) : 0.0f);
+                const float inv = 1.0f / sqrtf(ss / float(a.head_dim) + a.eps);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    p[j] = p[j] * inv * ga[j];
+                    q[j] = q[j] * inv * gb[j];
+                }
+                if constexpr (INTER) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        r[2 * j] = __builtin_fmaf(p[2 * j], c[j], -(p[2 * j + 1] * s[j]));
+                        r[2 * j + 1] = __builtin_fmaf(p[2 * j + 1], c[j], p[2 * j] * s[j]);
+                        t[2 * j] = __builtin_fmaf(q[2 * j], c[4 + j], -(q[2 * j + 1] * s[4 + j]));
+                        t[2 * j + 1] = __builtin_fmaf(q[2 * j + 1], c[4 + j], q[2 * j] * s[4 + j]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        r[j] = __builtin_fmaf(p[j], c[j], -(q[j] * s[j]));
+                        t[j] = __builtin_fmaf(q[j], c[j], p[j] * s[j]);
+                    }
+                }
+                u[k] = pack8(r);
+                v[k] = pack8(t);
+            } else if (in_place) {
+                continue;
+            }
+            if (active) {
+                *reinterpret_cast<uint4*>(yp + (h + k) * a.y_head + ea) = u[k];
+                *reinterpret_cast<uint4*>(yp + (h + k) * a.y_head + eb) = v[k];
+            }
+        }
+    }
+}
+
+// Any even rot_dim: a wave per head of a token, lane l on elements l, l + 64, ...
+// Every element and its partner are loaded before the first is stored.
+__global__ __launch_bounds__(64) void qk_norm_wave_kernel(QkNormArgs a) {
+    const int m = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
+    const uint16_t* const xp = a.x + m * a.x_token + h * a.x_head;
+    uint16_t* const yp = a.y + m * a.y_token + h * a.y_head;
+    const bool normed = h < a.q_heads + a.k_heads;
+    if (!normed && a.x == a.y) return;
+    const float* const g = h < a.q_heads ? a.q_gamma : a.k_gamma;
+    const int rh = a.rot_dim / 2;
+    float x[4], z[4];
+    int partner[4];
+    float ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int e = lane + 64 * k;
+        partner[k] = e >= a.rot_dim ? e : a.interleaved ? e ^ 1 : e < rh ? e + rh : e - rh;
+        x[k] = e < a.head_dim ? bf16_lo(xp[e]) : 0.0f;
+        z[k] = e < a.head_dim ? bf16_lo(xp[partner[k]]) : 0.0f;
+        ss = __builtin_fmaf(x[k], x[k], ss);
+    }
+    if (!normed) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int e = lane + 64 * k;
+            if (e < a.head_dim) yp[e] = uint16_t(__float_as_uint(x[k]) >> 16);
+        }
+        return;
+    }
+    ss = lanes_sum<16>(ss);
+    ss += __shfl_xor(ss, 16);
+    ss += __shfl_xor(ss, 32);
+    const float inv = 1.0f / sqrtf(ss / float(a.head_dim) + a.eps);
+    const int32_t pos = a.positions ? a.positions[m] : a.pos0 + m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int e = lane + 64 * k;
+        if (e >= a.head_dim) continue;
+        float v = x[k] * inv * (g ? g[e] : 1.0f);
+        if (e < a.rot_dim) {
+            const float w = z[k] * inv * (g ? g[partner[k]] : 1.0f);
+            const bool first = e < partner[k];
+            float c, s;
+            cos_sin_turns(angle(a.freq[a.interleaved ? e / 2 : first ? e : e - rh], pos), &c, &s);
+            c *= a.attn_scale;
+            s *= a.attn_scale;
+            v = __builtin_fmaf(v, c, first ? -(w * s) : w * s);
+        }
+        yp[e] = uint16_t(pack_bf16x2(v, 0.0f));
+    }
+}
+
+// Heads per thread: as in fq_rope, all of them where the tokens alone fill the
+// chip (the angles are then computed once), fewer below kFill threads.
+constexpr int64_t kFill = 256 * 1024;
+
+template <bool INTER, int L>
+hipError_t launch_items(const QkNormArgs& a, hipStream_t st) {
+    const int64_t threads = int64_t(a.M) * L;
+    int64_t parts = kFill / threads;
+    parts = parts < 1 ? 1 : parts > a.heads ? a.heads : parts;
+    const int share = int((a.heads + parts - 1) / parts);
+    const dim3 grid(uint32_t((threads + 255) / 256), uint32_t((a.heads + share - 1) / share));
+    if (share == 1)
+        hipLaunchKernelGGL((qk_norm_kernel<INTER, L, 1>), grid, dim3(256), 0, st, a, share);
+    else
+        hipLaunchKernelGGL((qk_norm_kernel<INTER, L, 2>), grid, dim3(256), 0, st, a, share);
+    return hipGetLastError();
+}
+
+template <bool INTER>
+hipError_t launch_lanes(const QkNormArgs& a, hipStream_t st) {
+    const int items = a.head_dim / 16;
+    if (items <= 1) return launch_items<INTER, 1>(a, st);
+    if (items <= 2) return launch_items<INTER, 2>(a, st);
+    if (items <= 4) return launch_items<INTER, 4>(a, st);
+    if (items <= 8) return launch_items<INTER, 8>(a, st);
+    return launch_items<INTER, 16>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm(const QkNormArgs& a, hipStream_t stream) {
+    if (a.interleaved && a.rot_dim % 8 == 0) return launch_lanes<true>(a, stream);
+    if (!a.interleaved && a.rot_dim % 16 == 0) return launch_lanes<false>(a, stream);
+    hipLaunchKernelGGL(qk_norm_wave_kernel, dim3(uint32_t(a.M), uint32_t(a.heads)), dim3(64), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace fq

@@ -20,6 +20,13 @@ __device__ __forceinline__ void copy16_to_lds(const uint8_t* base, uint32_t voff
     asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds_dst) : "memory");
 }
 
+// The same with five wait states: enough for a scalar base that a vector
+// instruction has just written (v_readfirstlane, or v_readlane of a spilled
+// register), which the compiler does not see being read by a memory instruction here.
+__device__ __forceinline__ void copy16_base(const uint8_t* base, uint32_t voff, uint32_t lds_dst) {
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds_dst) : "memory");
+}
+
 // LDS byte address of a pointer into __shared__ memory (wave uniform).
 __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
     typedef __attribute__((address_space(3))) const uint8_t lds_byte;
