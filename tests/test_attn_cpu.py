@@ -131,7 +131,7 @@ def test_decode_workspace_never_shrinks():
             last = 0
             for n in (1, 16, 127, 128, 129, 1000, 4096, 100000, 1 << 20, 1 << 30):
                 now = size(seqs, H, kv, D, n)
-                assert now >= last and now % 256 == 0 and now >= seqs * H * (D + 2) * 4
+                assert now >= last and now % 256 == 0 and now >= seqs * (H * (D + 2) * 4 + 8)
                 assert size(seqs + 1, H, kv, D, n) >= now
                 last = now
     assert size(0, 8, 2, 64, 10) == 0 and size(1, 8, 3, 64, 10) == 0 and size(1, 8, 2, 20, 10) == 0 and size(1, 8, 2, 64, 0) == 0
@@ -164,56 +164,73 @@ int main() {
             wrong += paged_entry(int(t) + 64 < most ? int(t) + 64 : int(t), int(t) + 1, magic) != t / ps;
         }
     }
-    // every token of a sequence in one part, one wave, one tile; every row inside the cache
+    // batches: every token of every sequence in one part, one wave, one tile; every row inside the cache
     const int lens[] = {-5, 0, 1, 15, 16, 17, 31, 33, 127, 128, 129, 500, 1023, 2000, 3001, 4097};
     const int sizes[] = {16, 48, 64, 112, 256};
     for (int ps : sizes)
-        for (int want : lens)
-            for (int64_t pairs : {1, 3, 100, 1024, 5000}) {
-                const int max_pages = 4097 / ps + 1, pages = 7, kv_heads = 3;
-                const int len = paged_len(want, max_pages, ps);
-                if (len < 0 || len > max_pages * ps || (want > 0 && want <= max_pages * ps && len != want)) ++wrong;
-                const int splits = decode_splits(pairs, max_pages * ps);
-                if (splits < 1 || splits > kDecodeWgs) ++wrong;
-                const DecodeParts parts = decode_parts(len, splits);
-                if (parts.count > splits || (len > 0) != (parts.count > 0)) ++wrong;
-                std::vector<int> table(max_pages), seen(len, 0);
-                for (int& p : table) p = rand() % (pages + 4) - 2;  // some outside the cache
+        for (int seqs : {1, 2, 16, 64, 150})
+            for (int heads : {1, 8, 40, 700}) {
+                const int max_pages = 4097 / ps + 1, pages = 7, kv_heads = heads > 1 ? heads / 2 : 1;
+                const int tiles = decode_head_tiles(heads, kv_heads), target = decode_target(kv_heads, tiles);
+                std::vector<int> len(seqs);
+                uint64_t sum = 0;
+                for (int s = 0; s < seqs; ++s) {
+                    const int want = lens[rand() % 16];
+                    len[s] = paged_len(want, max_pages, ps);
+                    if (len[s] != (want < 0 ? 0 : want > max_pages * ps ? max_pages * ps : want)) ++wrong;
+                    sum += decode_units(len[s]);
+                }
+                const int per = decode_part_len(sum, target);
+                if (per < kDecodeStep || per % kDecodeStep) ++wrong;
+                int64_t parts = 0;
                 const uint64_t magic = paged_magic(ps);
-                for (int split = 0; split < parts.count; ++split) {
-                    const int begin = split * parts.len, end = begin + parts.len < len ? begin + parts.len : len;
-                    for (int wave = 0; wave < kDecodeWaves; ++wave)
-                        for (int t = begin + kDecodeTile * wave; t < end; t += kDecodeTile * kDecodeWaves)
-                            for (int i = 0; i < 2; ++i, ++units) {
-                                const int ti = t + kDecodeUnit * i, entry = paged_entry(ti, len, magic);
-                                if (entry < 0 || entry >= max_pages) { ++wrong; continue; }
-                                const PagedUnit u = paged_unit(table[entry], entry, ti, len, pages, ps);
-                                // 16 rows are read, whatever is valid
-                                const int64_t rows = int64_t(pages) * kv_heads * ps;
-                                for (int h = 0; h < kv_heads; ++h) {
-                                    const int64_t row = paged_row(u.page, u.first, h, kv_heads, ps);
-                                    if (row < 0 || row + kDecodeUnit > rows || u.first + kDecodeUnit > ps || u.first % 4) ++wrong;
+                for (int s = 0; s < seqs; ++s) {
+                    const int count = decode_count(len[s], per);
+                    parts += count;
+                    std::vector<int> table(max_pages), seen(len[s], 0);
+                    for (int& p : table) p = rand() % (pages + 4) - 2;  // some outside the cache
+                    for (int part = 0; part < count; ++part) {
+                        const int begin = part * per, end = begin + per < len[s] ? begin + per : len[s];
+                        for (int wave = 0; wave < kDecodeWaves; ++wave)
+                            for (int t = begin + kDecodeTile * wave; t < end; t += kDecodeTile * kDecodeWaves)
+                                for (int i = 0; i < 2; ++i, ++units) {
+                                    const int ti = t + kDecodeUnit * i, entry = paged_entry(ti, len[s], magic);
+                                    if (entry < 0 || entry >= max_pages) { ++wrong; continue; }
+                                    const PagedUnit u = paged_unit(table[entry], entry, ti, len[s], pages, ps);
+                                    // 16 rows are read, whatever is valid
+                                    const int64_t rows = int64_t(pages) * kv_heads * ps;
+                                    for (int h = 0; h < kv_heads; ++h) {
+                                        const int64_t row = paged_row(u.page, u.first, h, kv_heads, ps);
+                                        if (row < 0 || row + kDecodeUnit > rows || u.first + kDecodeUnit > ps || u.first % 4) ++wrong;
+                                    }
+                                    for (int j = 0; j < kDecodeUnit; ++j) {
+                                        const int tok = ti + j, p = tok < len[s] ? table[tok / ps] : -1;
+                                        const bool there = tok < len[s] && p >= 0 && p < pages;
+                                        if (there != (j < u.valid)) ++wrong;
+                                        if (there && (u.page != p || u.first + j != tok % ps)) ++wrong;
+                                        if (tok < len[s]) ++seen[tok];
+                                    }
                                 }
-                                for (int j = 0; j < kDecodeUnit; ++j) {
-                                    const int tok = ti + j, p = tok < len ? table[tok / ps] : -1;
-                                    const bool there = tok < len && p >= 0 && p < pages;
-                                    if (there != (j < u.valid)) ++wrong;
-                                    if (there && (u.page != p || u.first + j != tok % ps)) ++wrong;
-                                    if (tok < len) ++seen[tok];
-                                }
-                            }
+                    }
+                    for (int n : seen) wrong += n != 1;
                 }
-                for (int n : seen) wrong += n != 1;
+                if (parts > decode_parts(seqs, heads, kv_heads, max_pages * ps)) ++wrong;
             }
-    // parts fit the workspace
-    for (int seqs : {1, 2, 7, 64, 1000})
-        for (int kv : {1, 2, 8})
-            for (int group : {1, 7, 16, 17, 40})
-                for (int max_len : {16, 128, 129, 4096, 1 << 20, 1 << 30}) {
-                    const int64_t pairs = int64_t(seqs) * kv * ((group + kDecodeHeads - 1) / kDecodeHeads);
-                    const int splits = decode_splits(pairs, max_len);
-                    if (decode_part_rows(seqs, kv * group, kv, max_len) < size_t(seqs) * kv * group * splits) ++wrong;
-                }
+    // no batch has more parts than its launch, and they fit the workspace
+    for (int k = 0; k < 20000; ++k) {
+        const int seqs = 1 + rand() % 200, kv = 1 + rand() % 40, q = kv * (1 + rand() % 40), top = 1 << (rand() % 31);
+        const int target = decode_target(kv, decode_head_tiles(q, kv));
+        std::vector<int> len(seqs);
+        uint64_t sum = 0;
+        for (int& n : len) sum += decode_units(n = rand() % 3 ? rand() % top : k % 2 ? top : 0);
+        const int per = decode_part_len(sum, target);
+        int64_t parts = 0;
+        for (int n : len) parts += decode_count(n, per);
+        const int64_t most = decode_parts(seqs, q, kv, top);
+        if (parts > most || per < kDecodeStep) ++wrong;
+        const DecodeWorkspace ws = decode_workspace(seqs, q, kv, 64, top);
+        if (ws.stats < size_t(seqs) * 8 || ws.sums < ws.stats + size_t(most) * q * 8 || ws.bytes < ws.sums + size_t(most) * q * 256) ++wrong;
+    }
     printf("%ld %ld\n", units, wrong);
     return 0;
 }

@@ -209,7 +209,7 @@ size_t fq_attn_decode_workspace_bytes(int32_t seqs, int32_t q_heads, int32_t kv_
     if (seqs < 1 || q_heads < 1 || q_heads > kMaxHeads || kv_heads < 1 || kv_heads > kMaxKvHeads || q_heads % kv_heads ||
         head_dim < 16 || head_dim > kMaxHeadDim || head_dim % 16 || max_len < 1 || max_len > fq::kDecodeMaxLen)
         return 0;
-    return round_up(fq::decode_part_rows(seqs, q_heads, kv_heads, max_len) * size_t(head_dim + 2) * sizeof(float), 256);
+    return fq::decode_workspace(seqs, q_heads, kv_heads, head_dim, max_len).bytes;
 }
 
 fq_status fq_attn_decode(const void* q_bf16, int64_t q_token, int64_t q_head, int32_t seqs, int32_t q_heads,
@@ -230,24 +230,26 @@ fq_status fq_attn_decode(const void* q_bf16, int64_t q_token, int64_t q_head, in
     FQ_TRY(check_head_rows(fn, "o_bf16", o_bf16, "o_token", o_token, "o_head", o_head, q_heads, seqs, head_dim, true));
     FQ_TRY(check_int32s(fn, "page_table", page_table));
     FQ_TRY(check_int32s(fn, "lens", lens));
-    const int32_t group = q_heads / kv_heads;
-    const int64_t pairs = int64_t(seqs) * kv_heads * ((group + fq::kDecodeHeads - 1) / fq::kDecodeHeads);
-    const int32_t splits = fq::decode_splits(pairs, max_pages * page_size);
-    if (pairs * splits >= kMaxThreads / 256 || int64_t(seqs) * q_heads >= kMaxThreads / 256)
+    const int32_t max_len = max_pages * page_size;
+    const int64_t parts = fq::decode_parts(seqs, q_heads, kv_heads, max_len);
+    if (parts * kv_heads * fq::decode_head_tiles(q_heads, kv_heads) >= kMaxThreads / 256 ||
+        int64_t(seqs) * q_heads >= kMaxThreads / 256)
         return fail(FQ_ERR_SHAPE, fmt("%s: seqs=%d x q_heads=%d are too many for one launch", fn, seqs, q_heads));
     if (!workspace) return fail(FQ_ERR_ARG, fmt("%s: workspace is NULL", fn));
     if (!aligned(workspace, 256)) return fail(FQ_ERR_ALIGN, fmt("%s: workspace is not 256-byte aligned", fn));
-    const size_t need = fq_attn_decode_workspace_bytes(seqs, q_heads, kv_heads, head_dim, max_pages * page_size);
-    if (workspace_bytes < need)
+    const fq::DecodeWorkspace ws = fq::decode_workspace(seqs, q_heads, kv_heads, head_dim, max_len);
+    if (workspace_bytes < ws.bytes)
         return fail(FQ_ERR_ARG, fmt("%s: workspace_bytes=%zu < %zu needed for seqs=%d q_heads=%d kv_heads=%d head_dim=%d "
-                                    "max_pages=%d page_size=%d", fn, workspace_bytes, need, seqs, q_heads, kv_heads,
+                                    "max_pages=%d page_size=%d", fn, workspace_bytes, ws.bytes, seqs, q_heads, kv_heads,
                                     head_dim, max_pages, page_size));
     const fq::DeviceInfo* dev = nullptr;
     FQ_TRY(prepare(fn, &dev));
+    uint8_t* const base = static_cast<uint8_t*>(workspace);
     const fq::DecodeArgs a{static_cast<const uint16_t*>(q_bf16), q_token, q_head, seqs, q_heads, scale,
                            cache_of(k_cache, v_cache, k_scale, v_scale, pages, page_size, kv_heads, head_dim), page_table,
                            max_pages, lens, static_cast<uint16_t*>(o_bf16), o_token, o_head,
-                           static_cast<float*>(workspace), splits};
+                           static_cast<int2*>(workspace), reinterpret_cast<float2*>(base + ws.stats),
+                           reinterpret_cast<float*>(base + ws.sums), int32_t(parts)};
     return device_status(fn, fq::launch_attn_decode(a, static_cast<hipStream_t>(stream)));
 }
 

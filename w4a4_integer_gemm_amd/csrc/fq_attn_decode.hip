@@ -3,10 +3,12 @@
 //   o[s][h] = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - max),  s_j = scale log2(e) <q[s][h], k_j>
 //
 // Bound by reading the visible keys and values once.  A workgroup takes up to 16
-// query heads of one key head, so that they share the reading, and one part of the
+// query heads of one key head, so that they share the reading, and one part of a
 // sequence; its four waves take tiles of 32 tokens in turn, each with its own
-// running maximum, sum and output, and join at the end.  Parts of a sequence
-// meet in the workspace and are joined by a second launch.
+// running maximum, sum and output, and join at the end.  All parts of a batch have
+// one length, found from its lengths by every workgroup, so that sequences of any lengths keep
+// the chip equally busy.  Parts of a sequence meet in the workspace and are joined by a
+// second launch.
 //
 // Both products are matrix instructions over 16 heads:
 //   S^T[key][head] = K Q^T     lane l: key l % 16 of a unit of 16 tokens, 8 of 32 d
@@ -76,11 +78,55 @@ __device__ __forceinline__ void transpose8(const uint2 (&r)[8], v8bf (&out)[8]) 
     for (int t = 0; t < 8; ++t) out[t] = as_bf(make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]));
 }
 
+// Inclusive sums over the lanes before.
+__device__ __forceinline__ uint32_t lanes_scan(uint32_t v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15, 31
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+    return v;
+}
+
+// Part w of the batch: its sequence (-1: there are fewer parts), the number inside it and the
+// parts it has, the sequence's length and a part's.  Every wave finds it.
+struct Part {
+    int seq, index, count, len, part_len;
+};
+__device__ __forceinline__ Part find_part(const DecodeArgs& a, int w, int target) {
+    const int lane = threadIdx.x & 63, most = a.max_pages, size = a.cache.page_size;
+    if (a.seqs == 1) {
+        const int len = paged_len(scalar_load(a.lens, 0), most, size);
+        const int per = decode_part_len(decode_units(len), target), count = decode_count(len, per);
+        return Part{w < count ? 0 : -1, w, count, len, per};
+    }
+    auto length = [&](int s) { return s < a.seqs ? paged_len(a.lens[s], most, size) : 0; };
+    const int len0 = length(lane);
+    uint64_t units = 0;
+    for (int s0 = 0; s0 < a.seqs; s0 += 64)
+        units += uint32_t(__builtin_amdgcn_readlane(int(lanes_scan(decode_units(s0 ? length(s0 + lane) : len0))), 63));
+    const int per = decode_part_len(units, target);
+    uint32_t before = 0;
+    for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+        const int len = s0 ? length(s0 + lane) : len0;
+        const uint32_t n = s0 + lane < a.seqs ? decode_count(len, per) : 0, upto = before + lanes_scan(n);
+        const uint64_t past = __ballot(upto > uint32_t(w));
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            return Part{s0 + at, w - __builtin_amdgcn_readlane(int(upto - n), at), __builtin_amdgcn_readlane(int(n), at),
+                        __builtin_amdgcn_readlane(len, at), per};
+        }
+        before = uint32_t(__builtin_amdgcn_readlane(int(upto), 63));
+    }
+    return Part{-1, 0, 0, 0, per};
+}
+
 // DP: head_dim rounded up to a size with code of its own.  A lane's pieces past
 // head_dim read the row's first piece: the query's zeros meet them in the first product, and
 // the outputs of the second are not stored.
 template <int DP, bool FP8>
-__global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs a, uint64_t magic, int tiles_of_heads) {
+__global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs a, uint64_t magic, int target, int head_tiles) {
     constexpr int ES = FP8 ? 1 : 2;                       // bytes of a value
     constexpr int KL = FP8 ? (DP + 63) / 64 : DP / 32;    // loads of 16 bytes of a lane's key
     constexpr int KM = FP8 ? 2 * KL : KL;                 // products of a unit
@@ -93,21 +139,20 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs a, uint64_t
     const KvCache& kc = a.cache;
     const int D = kc.head_dim, lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // split, tile of heads, key head, sequence
+    // tile of heads, key head, part
     int id = blockIdx.x;
-    const int split = id % a.splits;
-    id /= a.splits;
-    const int ht = id % tiles_of_heads;
-    id /= tiles_of_heads;
-    const int kvh = id % kc.kv_heads, seq = id / kc.kv_heads;
+    const int ht = id % head_tiles;
+    id /= head_tiles;
+    const int kvh = id % kc.kv_heads, w = id / kc.kv_heads;
     const int group = a.q_heads / kc.kv_heads;
     const int heads = group - ht * kDecodeHeads < kDecodeHeads ? group - ht * kDecodeHeads : kDecodeHeads;
     const int head0 = kvh * group + ht * kDecodeHeads;
 
-    const int len = paged_len(scalar_load(a.lens, seq), a.max_pages, kc.page_size);
-    const DecodeParts parts = decode_parts(len, a.splits);
-    if (split >= (parts.count ? parts.count : 1)) return;
-    const int begin = split * parts.len, end = begin + parts.len < len ? begin + parts.len : len;
+    const Part part = find_part(a, w, target);
+    if (part.seq < 0) return;
+    const int seq = part.seq, len = part.len;
+    if (part.index == 0 && kvh == 0 && ht == 0 && threadIdx.x == 0) a.plan[seq] = make_int2(w, part.count);
+    const int begin = part.index * part.part_len, end = min(begin + part.part_len, len);
     const int32_t* const table = a.page_table + int64_t(seq) * a.max_pages;
 
     // the query's operand
@@ -291,7 +336,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs a, uint64_t
     }
     __syncthreads();
     const int quads = D / 4;
-    const bool whole = parts.count <= 1;
+    const bool whole = part.count == 1;
     for (int i = threadIdx.x; i < heads * quads; i += 64 * kDecodeWaves) {
         const int h = i / quads, d = 4 * (i - h * quads);
         float top = ml[0][0][h], sum = 0.0f;
@@ -309,80 +354,82 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs a, uint64_t
             *reinterpret_cast<uint2*>(a.o + seq * a.o_token + (head0 + h) * a.o_head + d) =
                 make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
         } else {
-            const int64_t row = (int64_t(seq) * a.q_heads + head0 + h) * a.splits + split;
-            float* const sums = a.part + 2 * int64_t(a.seqs) * a.q_heads * a.splits;
-            *reinterpret_cast<float4*>(sums + row * D + d) = v;
-            if (d == 0) *reinterpret_cast<float2*>(a.part + 2 * row) = make_float2(top, sum);
+            const int64_t row = int64_t(w) * a.q_heads + head0 + h;
+            *reinterpret_cast<float4*>(a.sums + row * D + d) = v;
+            if (d == 0) a.stats[row] = make_float2(top, sum);
         }
     }
 }
 
-// The parts of one query head: weights 2^(max - top), then the weighted sums.
+// The parts of one query head.  A thread takes four d of every (256 / quads)-th part, eight
+// parts' loads at once, with a running maximum of its own; the threads meet in LDS.
 __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
-    __shared__ float weight[kDecodeWgs];
-    __shared__ float red[8];
     __shared__ __attribute__((aligned(16))) float4 sums[256];
+    __shared__ float2 stats[64];
     const int D = a.cache.head_dim, seq = blockIdx.x / a.q_heads, head = blockIdx.x - seq * a.q_heads;
-    const int len = paged_len(a.lens[seq], a.max_pages, a.cache.page_size);
-    const int count = decode_parts(len, a.splits).count;
+    const int t = threadIdx.x, quads = D / 4, lines = 256 / quads, line = t / quads, d = 4 * (t - line * quads);
+    const int2 plan = a.plan[seq];
+    const int count = plan.y;
     if (count <= 1) return;
-    const int64_t row = (int64_t(seq) * a.q_heads + head) * a.splits;
-    const float2* const parts = reinterpret_cast<const float2*>(a.part) + row;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    float top = -INFINITY;
-    for (int i = t; i < count; i += 256) top = fmaxf(top, parts[i].x);
-    top = max_over_rows(top);
-#pragma unroll
-    for (int s = 8; s; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-    if (lane == 0) red[wave] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    float sum = 0.0f;
-    for (int i = t; i < count; i += 256) {
-        const float2 p = parts[i];
-        const float w = top == -INFINITY ? 0.0f : exp2_fast(p.x - top);
-        weight[i] = w;
-        sum += w * p.y;
-    }
-    sum = sum_over_rows(sum);
-#pragma unroll
-    for (int s = 8; s; s >>= 1) sum += __shfl_xor(sum, s);
-    if (lane == 0) red[4 + wave] = sum;
-    __syncthreads();
-    sum = red[4] + red[5] + red[6] + red[7];
-    // thread t: four d, every (256 / quads)-th part
-    const int quads = D / 4, lines = 256 / quads, line = t / quads, d = 4 * (t - line * quads);
+    const int64_t row0 = int64_t(plan.x) * a.q_heads + head;
+    constexpr int UN = 8;
+    float m = -INFINITY, l = 0.0f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (line < lines) {
-        const float* const p = a.part + 2 * int64_t(a.seqs) * a.q_heads * a.splits + row * D + d;
-        for (int i = line; i < count; i += lines) {
-            const float4 x = *reinterpret_cast<const float4*>(p + int64_t(i) * D);
-            const float w = weight[i];
-            v.x += w * x.x, v.y += w * x.y, v.z += w * x.z, v.w += w * x.w;
+        for (int i = line; i < count; i += UN * lines) {
+            float4 x[UN];
+            float2 st[UN];
+#pragma unroll
+            for (int k = 0; k < UN; ++k) {
+                const int part = min(i + k * lines, count - 1);  // (past the last: loaded again, of no weight)
+                const int64_t row = row0 + int64_t(part) * a.q_heads;
+                x[k] = *reinterpret_cast<const float4*>(a.sums + row * D + d);
+                st[k] = a.stats[row];
+                if (i + k * lines >= count) st[k] = make_float2(-INFINITY, 0.0f);
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < UN; ++k) top = fmaxf(top, st[k].x);
+            const float base = top == -INFINITY ? 0.0f : top, f = exp2_fast(m - base);
+            v.x *= f, v.y *= f, v.z *= f, v.w *= f, l *= f;
+#pragma unroll
+            for (int k = 0; k < UN; ++k) {
+                const float w = exp2_fast(st[k].x - base);
+                v.x += w * x[k].x, v.y += w * x[k].y, v.z += w * x[k].z, v.w += w * x[k].w;
+                l += w * st[k].y;
+            }
+            m = top;
         }
         sums[t] = v;
+        if (d == 0) stats[line] = make_float2(m, l);
     }
     __syncthreads();
-    if (t < quads) {
-        for (int i = 1; i < lines; ++i) {
-            const float4 x = sums[i * quads + t];
-            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-        }
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        *reinterpret_cast<uint2*>(a.o + seq * a.o_token + head * a.o_head + d) =
-            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+    if (t >= quads) return;
+    float top = -INFINITY;
+    for (int i = 0; i < lines; ++i) top = fmaxf(top, stats[i].x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.0f;
+    for (int i = 0; i < lines; ++i) {
+        const float w = exp2_fast(stats[i].x - base);
+        const float4 x = sums[i * quads + t];
+        v.x += w * x.x, v.y += w * x.y, v.z += w * x.z, v.w += w * x.w;
+        l += w * stats[i].y;
     }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    *reinterpret_cast<uint2*>(a.o + seq * a.o_token + head * a.o_head + d) =
+        make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
 }
 
 template <int DP>
 void launch_bits(const DecodeArgs& a, hipStream_t st) {
-    const int group = a.q_heads / a.cache.kv_heads, tiles = (group + kDecodeHeads - 1) / kDecodeHeads;
-    const dim3 grid(uint32_t(int64_t(a.seqs) * a.cache.kv_heads * tiles * a.splits));
+    const int tiles = decode_head_tiles(a.q_heads, a.cache.kv_heads), target = decode_target(a.cache.kv_heads, tiles);
+    const dim3 grid(uint32_t(int64_t(a.parts) * a.cache.kv_heads * tiles));
     const uint64_t magic = paged_magic(a.cache.page_size);
     if (a.cache.k_scale)
-        hipLaunchKernelGGL((attn_decode_kernel<DP, true>), grid, dim3(64 * kDecodeWaves), 0, st, a, magic, tiles);
+        hipLaunchKernelGGL((attn_decode_kernel<DP, true>), grid, dim3(64 * kDecodeWaves), 0, st, a, magic, target, tiles);
     else
-        hipLaunchKernelGGL((attn_decode_kernel<DP, false>), grid, dim3(64 * kDecodeWaves), 0, st, a, magic, tiles);
+        hipLaunchKernelGGL((attn_decode_kernel<DP, false>), grid, dim3(64 * kDecodeWaves), 0, st, a, magic, target, tiles);
 }
 
 }  // namespace
@@ -400,7 +447,7 @@ hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t stream) {
     else
         launch_bits<256>(a, stream);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
+    if (e != hipSuccess || a.parts == a.seqs) return e;  // (no sequence can have more than one part)
     hipLaunchKernelGGL(attn_join_kernel, dim3(uint32_t(a.seqs * a.q_heads)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }

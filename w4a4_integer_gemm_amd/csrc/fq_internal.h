@@ -275,8 +275,10 @@ struct DecodeArgs {
     const int32_t* lens;
     uint16_t* o;
     int64_t o_token, o_head;
-    float* part;  // [seqs][q_heads][splits][head_dim] sums, behind [seqs][q_heads][splits][2] maxima and weights
-    int32_t splits;
+    int2* plan;    // [seqs] first part and parts of each
+    float2* stats; // [parts][q_heads] maximum and sum of weights
+    float* sums;   // [parts][q_heads][head_dim]
+    int32_t parts; // (at most)
 };
 hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t stream);
 

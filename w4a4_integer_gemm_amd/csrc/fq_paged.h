@@ -29,23 +29,34 @@ FQ_PAGED_FN int32_t paged_len(int32_t len, int32_t max_pages, int32_t page_size)
     return len < 0 ? 0 : len > most ? most : len;
 }
 
-// Parts that a sequence of up to max_len tokens is split into, at most: as many as
-// give kDecodeWgs workgroups, and no part shorter than a tile for each wave.
-FQ_PAGED_FN int32_t decode_splits(int64_t pairs, int32_t max_len) {
-    const int32_t step = kDecodeTile * kDecodeWaves;
-    const int64_t want = (kDecodeWgs + pairs - 1) / pairs, most = (int64_t(max_len) + step - 1) / step;
-    return int32_t(want < most ? want : most);
+// A call's sequences are cut into parts of one length, which the kernel finds from the
+// lengths: as many parts as give kDecodeWgs workgroups, and no part shorter than a tile
+// for each wave.  Parts are numbered through the sequences in turn; one of no tokens has a part too.
+constexpr int32_t kDecodeStep = kDecodeTile * kDecodeWaves;
+// Query heads share a key head's reads in workgroups of up to kDecodeHeads.
+FQ_PAGED_FN int32_t decode_head_tiles(int32_t q_heads, int32_t kv_heads) {
+    return (q_heads / kv_heads + kDecodeHeads - 1) / kDecodeHeads;
 }
-
-// The tokens of each part of a sequence (whole tiles for each wave), and the parts it has.
-struct DecodeParts {
-    int32_t len, count;
-};
-FQ_PAGED_FN DecodeParts decode_parts(int32_t len, int32_t splits) {
-    const int32_t step = kDecodeTile * kDecodeWaves;
-    const int32_t steps = (len + step - 1) / step;
-    const int32_t per = (steps + splits - 1) / splits;
-    return DecodeParts{per * step, per ? (steps + per - 1) / per : 0};
+// Parts of the batch, aside from one that every sequence has.
+FQ_PAGED_FN int32_t decode_target(int32_t kv_heads, int32_t head_tiles) {
+    const int32_t n = kv_heads * head_tiles;
+    return (kDecodeWgs + n - 1) / n;
+}
+// What a sequence adds to the batch's length, in 64 tokens.
+FQ_PAGED_FN uint32_t decode_units(int32_t len) { return (uint32_t(len) + 63) / 64; }
+// Tokens of a part, from the batch's sum of those: sum / target of them are at most target parts.
+FQ_PAGED_FN int32_t decode_part_len(uint64_t units, int32_t target) {
+    const uint32_t t = uint32_t(target);
+    const uint64_t per = units >> 32 ? (units + t - 1) / t : uint64_t((uint32_t(units) + t - 1) / t);
+    const uint64_t steps = (per * 64 + kDecodeStep - 1) / kDecodeStep;
+    return steps > uint64_t(kDecodeMaxLen / kDecodeStep) ? kDecodeMaxLen : steps ? int32_t(steps) * kDecodeStep : kDecodeStep;
+}
+FQ_PAGED_FN int32_t decode_count(int32_t len, int32_t part_len) { return len <= part_len ? 1 : (len + part_len - 1) / part_len; }
+// Most parts that a call has, whatever the lengths.
+FQ_PAGED_FN int64_t decode_parts(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t max_len) {
+    const int64_t by_len = int64_t(seqs) * ((int64_t(max_len) + kDecodeStep - 1) / kDecodeStep);
+    const int64_t by_target = int64_t(seqs) + decode_target(kv_heads, decode_head_tiles(q_heads, kv_heads));
+    return by_len < by_target ? by_len : by_target;
 }
 
 // Pages by a multiplication: units of a page d = page_size / 16 <= 2^11, m = 2^37 / d + 1.
@@ -73,14 +84,16 @@ FQ_PAGED_FN int64_t paged_row(int32_t page, int32_t place, int32_t head, int32_t
     return (int64_t(page) * kv_heads + head) * page_size + place;
 }
 
-// Workspace of a decode call in rows of (head_dim + 2) floats: at least one for every
-// sequence, query head and part, and never fewer for more sequences or tokens.
-FQ_PAGED_FN size_t decode_part_rows(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t max_len) {
-    const int32_t step = kDecodeTile * kDecodeWaves;
-    const int64_t group = q_heads / kv_heads, per_seq = kv_heads * ((group + kDecodeHeads - 1) / kDecodeHeads);
-    const int64_t by_len = int64_t(seqs) * ((int64_t(max_len) + step - 1) / step);
-    const int64_t by_wgs = seqs + (kDecodeWgs + per_seq - 1) / per_seq;
-    return size_t(by_len < by_wgs ? by_len : by_wgs) * size_t(q_heads);
+// Workspace of a decode call, never smaller for more sequences or tokens: the first part and the
+// parts of every sequence, then for every part and query head the maximum, the sum of weights and the output.
+struct DecodeWorkspace {
+    size_t stats, sums, bytes;  // offsets of the two, and the size
+};
+FQ_PAGED_FN DecodeWorkspace decode_workspace(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                             int32_t max_len) {
+    const size_t rows = size_t(decode_parts(seqs, q_heads, kv_heads, max_len)) * size_t(q_heads);
+    const size_t stats = (size_t(seqs) * 8 + 255) / 256 * 256, sums = stats + (rows * 8 + 255) / 256 * 256;
+    return DecodeWorkspace{stats, sums, (sums + rows * size_t(head_dim) * 4 + 255) / 256 * 256};
 }
 
 }  // namespace fq
