@@ -10,6 +10,14 @@ from fqtest import bf16_to_f64, dev, host
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(params=["auto", "rows", "64", "128"], autouse=True)
+def kernel(request, hook):
+    """Every test on each of the kernels, and on the one that its sizes get."""
+    hook(f"attn_prefill={request.param}")
+    yield request.param
+
+
 MARK = 0x1234
 
 

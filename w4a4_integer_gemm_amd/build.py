@@ -18,7 +18,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["fq_api.cpp", "fq_pack.cpp", "fq_prologue.hip", "fq_gemm.hip", "fq_gemm_fp6.hip", "fq_gemv.hip", "fq_geglu.hip",
            "fq_noalloc.hip", "fq_decode1.hip", "fq_api_block.cpp", "fq_fp8_pack.cpp", "fq_rope_plan.cpp",
            "fq_block_norm.hip", "fq_fp8_gemm.hip", "fq_fp8_gemv.hip", "fq_fp8_decode.hip", "fq_rope.hip",
-           "fq_api_attn.cpp", "fq_qk_norm.hip", "fq_kv_cache.hip", "fq_attn_prefill.hip", "fq_attn_decode.hip"]
+           "fq_api_attn.cpp", "fq_qk_norm.hip", "fq_kv_cache.hip", "fq_attn_prefill.hip", "fq_attn_rows.hip",
+           "fq_attn_decode.hip"]
 # the benchmark's ceiling probes: a library of their own, outside the layer's ABI
 CEILING_SOURCES = ["fq_ceiling.hip"]
 

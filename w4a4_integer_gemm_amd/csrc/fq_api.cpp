@@ -27,10 +27,10 @@ void clear_error() { g_error.clear(); }
 namespace {
 
 // Applies a test-hook spec "key=value,key=value" (keys gemm_tile, gemm_mfma,
-// fp8_tile, gemv, decode1; "" or "default" resets every hook).  Returns false, with the reason in
+// fp8_tile, gemv, decode1, attn_prefill; "" or "default" resets every hook).  Returns false, with the reason in
 // *why, on an unknown key or value; nothing changes then.
 bool apply_hooks(Hooks& h, const char* spec, std::string* why) {
-    int tile = -1, fp8 = -1, mfma = 16, split = 0, d1off = 0;
+    int prefill = -1, tile = -1, fp8 = -1, mfma = 16, split = 0, d1off = 0;
     std::string s = spec ? spec : "";
     if (s == "default") s.clear();
     size_t pos = 0;
@@ -72,8 +72,14 @@ bool apply_hooks(Hooks& h, const char* spec, std::string* why) {
                 return false;
             }
             d1off = val == "off";
+        } else if (key == "attn_prefill") {
+            prefill = val == "auto" ? -1 : val == "rows" ? 0 : val == "64" ? 1 : val == "128" ? 2 : -2;
+            if (prefill == -2) {
+                *why = "attn_prefill must be rows, 64, 128 or auto, not '" + val + "'";
+                return false;
+            }
         } else {
-            *why = "unknown hook '" + key + "' (gemm_tile, gemm_mfma, fp8_tile, gemv, decode1)";
+            *why = "unknown hook '" + key + "' (gemm_tile, gemm_mfma, fp8_tile, gemv, decode1, attn_prefill)";
             return false;
         }
     }
@@ -82,6 +88,7 @@ bool apply_hooks(Hooks& h, const char* spec, std::string* why) {
     h.gemm_mfma.store(mfma, std::memory_order_relaxed);
     h.gemv_split.store(split, std::memory_order_relaxed);
     h.decode1_off.store(d1off, std::memory_order_relaxed);
+    h.attn_prefill.store(prefill, std::memory_order_relaxed);
     return true;
 }
 

@@ -202,7 +202,7 @@ fq_status fq_attn_prefill(const void* q_bf16, int64_t q_token, int64_t q_head, c
                             k_token, k_head, static_cast<const uint16_t*>(v_bf16), v_token, v_head, M, M_k, cu_q,
                             cu_k ? cu_k : cu_q, seqs, q_heads, kv_heads, head_dim, scale, causal,
                             static_cast<uint16_t*>(o_bf16), o_token, o_head};
-    return device_status(fn, fq::launch_attn_prefill(a, static_cast<hipStream_t>(stream)));
+    return device_status(fn, fq::launch_attn_prefill(a, *dev, static_cast<hipStream_t>(stream)));
 }
 
 size_t fq_attn_decode_workspace_bytes(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_len) {

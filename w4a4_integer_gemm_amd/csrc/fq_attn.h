@@ -48,4 +48,20 @@ __device__ __forceinline__ float sum_over_rows(float x) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A uniform load that the vector loads in flight need not be waited for.
+typedef const int32_t __attribute__((address_space(4)))* const_i32;
+__device__ __forceinline__ int32_t scalar_load(const int32_t* p, int64_t i) {
+    return reinterpret_cast<const_i32>(reinterpret_cast<uintptr_t>(p))[i];
+}
+
+// The sequence that block b of a packed launch belongs to: sequence s has the blocks
+// first(s), which grows by at least one with s, and the ones behind it.  -1: none.
+template <class First>
+__device__ __forceinline__ int find_sequence(int seqs, int64_t b, First first) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int s0 = 0; s0 < seqs; s0 += 64) n += __popcll(__ballot(s0 + lane < seqs && first(s0 + lane) <= b));
+    return __builtin_amdgcn_readfirstlane(n - 1);
+}
+
 }  // namespace fq

@@ -1,0 +1,258 @@
+// Attention of 16 columns (query heads, or rows, that share a key head) by the waves of a
+// workgroup, straight from global memory (gfx950, wave64).
+//
+// The waves take tiles of 32 keys in turn, each with its own running maximum, sum
+// and output, and join at the end.  Both products are matrix instructions over the columns:
+//   S^T[key][column] = K Q^T     lane l: key l % 16 of a unit of 16 keys, 8 of 32 d
+//   O^T[d][column]   = V^T P^T   lane l: one d, 8 of the tile's 32 keys
+// A lane holds its column's scores of keys 4 (l / 16) + 0 .. 3 of both units, and those
+// are the 8 keys that it has to present to the second product: the weights never
+// leave their lane.  The other operand needs 8 keys of one d in a lane; lane l loads
+// 8 consecutive d of each of these 8 keys and pairs them up in registers, the d's of
+// its piece going to eight products.  e4m3 codes are exact in bf16; the key's scale
+// multiplies the score, the value's the weight before it is rounded to bf16.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "fq_attn.h"
+#include "fq_device.h"
+#include "fq_paged.h"
+
+namespace fq {
+
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+// Two of a dword's four codes as bf16.
+template <bool HI>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+}
+
+// 8 keys of one d (eight times, for 8 consecutive d) from rows of 8 keys.
+__device__ __forceinline__ void transpose8(const uint4 (&r)[8], v8bf (&out)[8]) {
+    uint32_t w[8][4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t a[4] = {r[2 * p].x, r[2 * p].y, r[2 * p].z, r[2 * p].w};
+        const uint32_t b[4] = {r[2 * p + 1].x, r[2 * p + 1].y, r[2 * p + 1].z, r[2 * p + 1].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            w[2 * c][p] = __builtin_amdgcn_perm(b[c], a[c], 0x05040100u);
+            w[2 * c + 1][p] = __builtin_amdgcn_perm(b[c], a[c], 0x07060302u);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) out[t] = as_bf(make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]));
+}
+__device__ __forceinline__ void transpose8(const uint2 (&r)[8], v8bf (&out)[8]) {
+    uint32_t w[8][4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t a[2] = {r[2 * p].x, r[2 * p].y}, b[2] = {r[2 * p + 1].x, r[2 * p + 1].y};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t lo = __builtin_amdgcn_perm(b[c], a[c], 0x05010400u);
+            const uint32_t hi = __builtin_amdgcn_perm(b[c], a[c], 0x07030602u);
+            w[4 * c][p] = codes_bf16<false>(lo);
+            w[4 * c + 1][p] = codes_bf16<true>(lo);
+            w[4 * c + 2][p] = codes_bf16<false>(hi);
+            w[4 * c + 3][p] = codes_bf16<true>(hi);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) out[t] = as_bf(make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]));
+}
+
+// DP: head_dim rounded up to a size with code of its own.  A lane's pieces past
+// head_dim read the row's first piece: the query's zeros meet them in the first product, and
+// the outputs of the second are not stored.
+template <int DP, bool FP8>
+struct Columns {
+    static constexpr int ES = FP8 ? 1 : 2;                     // bytes of a value
+    static constexpr int KL = FP8 ? (DP + 63) / 64 : DP / 32;  // loads of 16 bytes of a lane's key
+    static constexpr int KM = FP8 ? 2 * KL : KL;               // products of a unit
+    static constexpr int HV = (DP + 127) / 128;                // pieces of 8 d of a lane's value
+    static constexpr int LD = DP + 4;                          // (floats; a column's row in LDS starts on another bank)
+    using vpiece = std::conditional_t<FP8, uint2, uint4>;
+
+    // 16 rows of keys and of values, from the first; the scales of theirs that the lane needs.
+    struct Unit {
+        const uint8_t *k, *v;
+        const float *ks, *vs;
+        int last;  // row that the ones behind it are read as (15: all are there)
+    };
+
+    v8bf q[KM];
+    uint4 kf[2][KL];
+    vpiece vf[HV][8];
+    float4 ks[2], vs[2];
+    v4f acc[HV][8];
+    float m = -INFINITY, l = 0.0f;
+
+    // The column's query (nullptr: zeros).
+    __device__ __forceinline__ void load_query(const uint16_t* p, int D) {
+        const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            const int d = FP8 ? 64 * (j / 2) + 16 * g + 8 * (j % 2) : 32 * j + 8 * g;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (p && d < D) v = *reinterpret_cast<const uint4*>(p + d);
+            q[j] = as_bf(v);
+        }
+#pragma unroll
+        for (int i = 0; i < HV; ++i)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) acc[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // kstride, vstride: bytes from row to row.
+    __device__ __forceinline__ void load_k(const Unit (&u)[2], int D, uint32_t kstride) {
+        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t row = uint32_t(u[i].last < 15 ? min(col, u[i].last) : col) * kstride;
+#pragma unroll
+            for (int j = 0; j < KL; ++j) {
+                const int at = 16 * (4 * j + g);
+                kf[i][j] = *reinterpret_cast<const uint4*>(u[i].k + (row + (at < D * ES ? at : 0)));
+            }
+            if constexpr (FP8) {
+                ks[i] = *reinterpret_cast<const float4*>(u[i].ks + 4 * g);
+                vs[i] = *reinterpret_cast<const float4*>(u[i].vs + 4 * g);
+            }
+        }
+    }
+    __device__ __forceinline__ void load_v(const Unit (&u)[2], int D, uint32_t vstride) {
+        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t row = uint32_t(u[i].last < 15 ? min(4 * g + j, u[i].last) : 4 * g + j) * vstride;
+#pragma unroll
+                for (int hv = 0; hv < HV; ++hv) {
+                    const int d = 128 * hv + 8 * col;
+                    vf[hv][4 * i + j] = *reinterpret_cast<const vpiece*>(u[i].v + (row + (d < D ? d * ES : 0)));
+                }
+            }
+    }
+
+    // The scores of the loaded keys, times c (and the key's scale), and the values' scales.
+    __device__ __forceinline__ void scores(float c, float (&x)[8], float (&w)[8]) {
+        v4f s[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s[i] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < KL; ++j) {
+                if constexpr (FP8) {
+                    const uint4 k = kf[i][j];
+                    s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k.x), codes_bf16<true>(k.x),
+                                                         codes_bf16<false>(k.y), codes_bf16<true>(k.y))), q[2 * j], s[i]);
+                    s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k.z), codes_bf16<true>(k.z),
+                                                         codes_bf16<false>(k.w), codes_bf16<true>(k.w))), q[2 * j + 1], s[i]);
+                } else {
+                    s[i] = mfma_bf16_16(as_bf(kf[i][j]), q[j], s[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 &kq = ks[i / 4], &vq = vs[i / 4];
+            x[i] = s[i / 4][i % 4] * (FP8 ? (i % 4 == 0 ? kq.x : i % 4 == 1 ? kq.y : i % 4 == 2 ? kq.z : kq.w) * c : c);
+            w[i] = FP8 ? (i % 4 == 0 ? vq.x : i % 4 == 1 ? vq.y : i % 4 == 2 ? vq.z : vq.w) : 1.0f;
+        }
+    }
+    // Key i of the lane (0 .. 7) is not seen by any column, and its place may hold anything.
+    __device__ __forceinline__ void drop(int i, float (&x)[8], float (&w)[8]) {
+        x[i] = -INFINITY;
+        w[i] = 0.0f;
+#pragma unroll
+        for (int hv = 0; hv < HV; ++hv) vf[hv][i] = vpiece{};
+    }
+    // The weights of the scores x, and the loaded values with them.
+    __device__ __forceinline__ void add(float (&x)[8], const float (&w)[8]) {
+        float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        top = fmaxf(m, max_over_rows(top));
+        if (__any(top > m)) {
+            const float f = top == -INFINITY ? 1.0f : exp2_fast(m - top);
+            l *= f;
+#pragma unroll
+            for (int hv = 0; hv < HV; ++hv)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[hv][k] *= f;
+            m = top;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = exp2_fast(x[i] - base);
+            l += x[i];
+            if constexpr (FP8) x[i] *= w[i];
+        }
+        const v8bf p = as_bf(make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                        pack_bf16x2(x[6], x[7])));
+#pragma unroll
+        for (int hv = 0; hv < HV; ++hv) {
+            v8bf vt[8];
+            transpose8(vf[hv], vt);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[hv][k] = mfma_bf16_16(vt[k], p, acc[hv][k]);
+        }
+    }
+
+    // The waves' parts, each scaled to the common maximum, meet in LDS.
+    template <int WAVES>
+    struct Meeting {
+        float part[WAVES][kDecodeHeads][LD];
+        float stat[2][WAVES][kDecodeHeads];  // maxima, sums
+    };
+    template <int WAVES>
+    __device__ __forceinline__ void meet(Meeting<WAVES>& lds, int wave) {
+        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+        l = sum_over_rows(l);
+        if (g == 0) {
+            lds.stat[0][wave][col] = m;
+            lds.stat[1][wave][col] = l;
+        }
+        __syncthreads();
+        float top = lds.stat[0][0][col];
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) top = fmaxf(top, lds.stat[0][i][col]);
+        const float f = top == -INFINITY ? 0.0f : exp2_fast(m - top);
+        // register r of product k: d = 128 hv + 32 g + 8 r + k
+#pragma unroll
+        for (int hv = 0; hv < HV; ++hv)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d = 128 * hv + 32 * g + 8 * r;
+                if (d >= DP) continue;
+                float* const out = &lds.part[wave][col][d];
+                *reinterpret_cast<float4*>(out) =
+                    make_float4(acc[hv][0][r] * f, acc[hv][1][r] * f, acc[hv][2][r] * f, acc[hv][3][r] * f);
+                *reinterpret_cast<float4*>(out + 4) =
+                    make_float4(acc[hv][4][r] * f, acc[hv][5][r] * f, acc[hv][6][r] * f, acc[hv][7][r] * f);
+            }
+        __syncthreads();
+    }
+    // Four d of a column from there: the sums over the waves, their maximum and the weights' sum.
+    template <int WAVES>
+    static __device__ __forceinline__ float4 joined(const Meeting<WAVES>& lds, int column, int d, float& top, float& sum) {
+        top = lds.stat[0][0][column];
+        sum = 0.0f;
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) top = fmaxf(top, lds.stat[0][w][column]);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(&lds.part[w][column][d]);
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            sum += lds.stat[1][w][column] * (top == -INFINITY ? 0.0f : exp2_fast(lds.stat[0][w][column] - top));
+        }
+        return v;
+    }
+};
+
+}  // namespace fq

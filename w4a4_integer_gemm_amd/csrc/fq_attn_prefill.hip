@@ -18,7 +18,8 @@
 // last key are read as that key and masked, whatever lies there.
 #include <hip/hip_runtime.h>
 
-#include <climits>
+#include <atomic>
+#include <type_traits>
 
 #include "fq_attn.h"
 #include "fq_device.h"
@@ -42,70 +43,120 @@ __device__ __forceinline__ v4s lds_read_tr(uint32_t addr) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(uintptr_t(addr)));
 }
 
-template <int DP_, int WAVES_>
+// WQ x WK waves: WQ of them share a tile and have 32 query rows each; WK such groups take
+// the tiles in turn and join at the end.
+template <int DP_, int WQ_, int WK_, int BK_>
 struct Shape {
-    static constexpr int DP = DP_, WAVES = WAVES_;
-    static constexpr int BQ = 32 * WAVES;            // query rows of a workgroup
-    static constexpr int BK = DP <= 128 ? 64 : 32;   // keys of a tile
+    static constexpr int DP = DP_, WQ = WQ_, WK = WK_, THREADS = 64 * WQ * WK;
+    static constexpr int BQ = 32 * WQ;  // query rows of a workgroup
+    static constexpr int BK = BK_;      // keys of a tile
     static constexpr int CH = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;  // 16-byte pieces of a row in LDS
     static constexpr int ROW = 16 * CH;              // its bytes
-    static constexpr int TILE = BK * ROW;
-    static constexpr int COPIES = TILE / 1024 / WAVES;  // of a wave, for the keys (the values) of a tile
+    static constexpr int TILE = BK * ROW;            // of keys, or of values
+    static constexpr int RING = 2 * 2 * TILE;        // of a group: two stages
+    static constexpr int COPIES = TILE / 1024 / WQ;  // of a wave, for the keys (the values) of a tile
     static constexpr int KT = BK / 32, DT = DP / 32, DS = DP / 16;
+    static constexpr int SLAB = 1024 * 4 * DT + 512;  // a wave's output, maxima and sums
+    static constexpr int JOIN = (WK - 1) * WQ * SLAB, LDS = WK * RING > JOIN ? WK * RING : JOIN;
+    static_assert(COPIES * WQ * 1024 == TILE && LDS <= 160 * 1024, "LDS");
 };
 
 // Slot of piece c of row r.
 template <int CH>
-__device__ __forceinline__ int key_slot(int r, int c) { return c ^ (r & 7); }
+__device__ __forceinline__ int key_slot(int r, int c) { return c ^ (r & (CH == 8 ? 7 : 15)); }
 template <int CH>
 __device__ __forceinline__ int value_slot(int r, int c) { return c ^ (CH == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2); }
 
-// The sequence that block b of the launch belongs to and its first row: blocks of
-// sequence s are cu[s] / BQ + s and the ones behind it, of which those of sequence s + 1
-// leave at least as many as s has.
-struct Block {
-    int seq, row;  // the row inside the sequence
-};
-template <int BQ>
-__device__ __forceinline__ Block find_block(const int32_t* cu, int seqs, int M, int b) {
-    const int lane = threadIdx.x & 63;
-    auto first = [&](int s) { return max(0, min(cu[s], M)) / BQ + s; };
-    int n = 0;
-    for (int s0 = 0; s0 < seqs; s0 += 64) {
-        const int s = s0 + lane;
-        n += __popcll(__ballot(s < seqs && first(s) <= b));
-    }
-    const int seq = __builtin_amdgcn_readfirstlane(max(n - 1, 0));
-    return Block{seq, __builtin_amdgcn_readfirstlane((b - first(seq)) * BQ)};
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+// l plus the two packed weights: the sum is that of the weights as they are multiplied.
+__device__ __forceinline__ float add_weights(uint32_t w, float l) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, w), __builtin_bit_cast(v2bf, 0x3F803F80u), l, false);
 }
 
 template <class SH>
-__global__ __launch_bounds__(64 * SH::WAVES) void attn_prefill_kernel(PrefillArgs a, int blocks) {
-    constexpr int BQ = SH::BQ, BK = SH::BK, CH = SH::CH, ROW = SH::ROW, KT = SH::KT, DT = SH::DT, DS = SH::DS;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * 2 * SH::TILE];
+__global__ __launch_bounds__(SH::THREADS) void attn_prefill_kernel(PrefillArgs a, int blocks) {
+    constexpr int BQ = SH::BQ, BK = SH::BK, CH = SH::CH, ROW = SH::ROW, KT = SH::KT, DT = SH::DT, DS = SH::DS, WK = SH::WK;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[SH::LDS];
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wq = wave % SH::WQ, wk = wave / SH::WQ;
     // heads in turn, the blocks that see most keys first
     const int head = blockIdx.x % a.q_heads, b = blocks - 1 - int(blockIdx.x / a.q_heads);
-    const Block at = find_block<BQ>(a.cu_q, a.seqs, a.M, b);
+    // (those of sequence s are cu[s] / BQ + s and on, which leaves at least as many as it has)
+    auto first = [&](int s) { return max(0, min(a.cu_q[s], a.M)) / BQ + s; };
+    const int seq = find_sequence(a.seqs, b, first);
+    if (seq < 0) return;
+    const int at_row = __builtin_amdgcn_readfirstlane((b - first(seq)) * BQ);
     auto range = [](const int32_t* cu, int s, int M, int& begin, int& count) {
         begin = __builtin_amdgcn_readfirstlane(max(0, min(cu[s], M)));
         count = __builtin_amdgcn_readfirstlane(max(0, min(cu[s + 1], M) - begin));
     };
     int q0, Lq, k0, Lk;
-    range(a.cu_q, at.seq, a.M, q0, Lq);
-    if (at.row < 0 || at.row >= Lq) return;
-    range(a.cu_k, at.seq, a.M_k, k0, Lk);
+    range(a.cu_q, seq, a.M, q0, Lq);
+    if (at_row < 0 || at_row >= Lq) return;
+    range(a.cu_k, seq, a.M_k, k0, Lk);
     const int D = a.head_dim, kvh = head / (a.q_heads / a.kv_heads);
     const int shift = Lk - Lq;  // row i sees the keys up to i + shift
-    const int rows = min(BQ, Lq - at.row);
-    const int seen = a.causal ? min(Lk, at.row + rows + shift) : Lk;  // by any of the block's rows
+    const int rows = min(BQ, Lq - at_row);
+    const int seen = a.causal ? min(Lk, at_row + rows + shift) : Lk;  // by any of the block's rows
     const int tiles = seen > 0 ? (seen + BK - 1) / BK : 0;
-    const int row = at.row + 32 * wave + col;  // this lane's
+    const int row0 = at_row + 32 * wq, row = row0 + col;  // the wave's first, this lane's
     const int limit = a.causal ? min(row + shift, Lk - 1) : Lk - 1;  // its last key
-    // keys that every row of the wave sees, and that any sees
-    const int wave_all = a.causal ? min(at.row + 32 * wave + shift, Lk - 1) : Lk - 1;
-    const int wave_any = at.row + 32 * wave >= Lq ? -1 : a.causal ? min(min(at.row + 32 * wave + 31, Lq - 1) + shift, Lk - 1) : Lk - 1;
+    // the last key that every row of the wave sees, and that any sees
+    const int wave_all = a.causal ? min(row0 + shift, Lk - 1) : Lk - 1;
+    const int wave_any = row0 >= Lq ? -1 : a.causal ? min(min(row0 + 31, Lq - 1) + shift, Lk - 1) : Lk - 1;
+
+    // copies: of the rows of a whole tile, or of its first ones
+    const uint32_t lds0 = lds_address(lds) + wk * SH::RING;
+    const uint8_t* const kbase = reinterpret_cast<const uint8_t*>(a.k + k0 * a.k_token + kvh * a.k_head);
+    const uint8_t* const vbase = reinterpret_cast<const uint8_t*>(a.v + k0 * a.v_token + kvh * a.v_head);
+    const uint32_t kstride = uint32_t(2 * a.k_token), vstride = uint32_t(2 * a.v_token);
+    constexpr int PER = 64 / CH;  // rows of a copy
+    auto offset = [&](int i, int most, bool value) {
+        const int r = (wq * SH::COPIES + i) * PER + lane / CH, slot = lane % CH;
+        const int piece = value ? value_slot<CH>(r, slot) : key_slot<CH>(r, slot);
+        // (pieces past head_dim: any that exists; rows behind the sequence: its last)
+        return uint32_t(min(r, most)) * (value ? vstride : kstride) + (piece * 8 < D ? 16 * piece : 0);
+    };
+    uint32_t koff[SH::COPIES], voff[SH::COPIES];
+#pragma unroll
+    for (int i = 0; i < SH::COPIES; ++i) {
+        koff[i] = offset(i, BK, false);
+        voff[i] = offset(i, BK, true);
+    }
+    const uint32_t cdst = lds0 + wq * SH::COPIES * 1024;
+    // Copies of the group's tile t, rows (t * WK + wk) * BK and on; behind the last tile they
+    // read it again, so that no branch lies between the products.
+    struct Source {
+        const uint8_t *k, *v;
+        uint32_t kdst, vdst;
+    };
+    auto source = [&](int tk, int tv) {
+        const int jk = min(tk * WK + wk, tiles - 1) * BK, jv = min(tv * WK + wk, tiles - 1) * BK;
+        if (jk + BK > Lk) {
+#pragma unroll
+            for (int i = 0; i < SH::COPIES; ++i) koff[i] = offset(i, Lk - jk - 1, false);
+        }
+        if (jv + BK > Lk) {
+#pragma unroll
+            for (int i = 0; i < SH::COPIES; ++i) voff[i] = offset(i, Lk - jv - 1, true);
+        }
+        return Source{kbase + 2 * (jk * a.k_token), vbase + 2 * (jv * a.v_token), cdst + (tk & 1) * 2 * SH::TILE,
+                      cdst + (tv & 1) * 2 * SH::TILE + SH::TILE};
+    };
+    auto copy_k = [&](const Source& from, int i) { copy16_base(from.k, koff[i], from.kdst + 1024 * i); };
+    auto copy_v = [&](const Source& from, int i) { copy16_base(from.v, voff[i], from.vdst + 1024 * i); };
+    const int rounds = (tiles + WK - 1) / WK;  // tiles of the first group,
+    const int wave_tiles = wave_any < wk * BK ? 0 : (wave_any / BK - wk) / WK + 1;  // and those that the wave's rows see
+    if (tiles > 0) {
+        const Source first = source(0, 0);
+#pragma unroll
+        for (int i = 0; i < SH::COPIES; ++i) copy_k(first, i);
+#pragma unroll
+        for (int i = 0; i < SH::COPIES; ++i) copy_v(first, i);
+        const Source second = source(1, 1);
+#pragma unroll
+        for (int i = 0; i < SH::COPIES; ++i) copy_k(second, i);
+    }
 
     // the query's operand
     v8bf q[DS];
@@ -122,39 +173,13 @@ __global__ __launch_bounds__(64 * SH::WAVES) void attn_prefill_kernel(PrefillArg
     }
     const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);  // (0 times a masked score would be no number)
 
-    // copies
-    const uint32_t lds0 = lds_address(lds);
-    const uint8_t* const kbase = reinterpret_cast<const uint8_t*>(a.k + k0 * a.k_token + kvh * a.k_head);
-    const uint8_t* const vbase = reinterpret_cast<const uint8_t*>(a.v + k0 * a.v_token + kvh * a.v_head);
-    constexpr int PER = 64 / CH;  // rows of a copy
-    int crow[SH::COPIES];
-    uint32_t kpiece[SH::COPIES], vpiece[SH::COPIES];
-#pragma unroll
-    for (int i = 0; i < SH::COPIES; ++i) {
-        const int r = (wave * SH::COPIES + i) * PER + lane / CH, slot = lane % CH;
-        const int kc = key_slot<CH>(r, slot), vc = value_slot<CH>(r, slot);
-        crow[i] = r;
-        kpiece[i] = kc * 8 < D ? 16 * kc : 0;  // (pieces past head_dim: any that exists)
-        vpiece[i] = vc * 8 < D ? 16 * vc : 0;
-    }
-    auto copy = [&](int t) {
-        const uint32_t dst = lds0 + (t & 1) * 2 * SH::TILE + wave * SH::COPIES * 1024;
-        const int j0 = t * BK, last = min(BK, Lk - j0) - 1;
-        const uint8_t* const kp = kbase + 2 * (j0 * a.k_token);
-        const uint8_t* const vp = vbase + 2 * (j0 * a.v_token);
-#pragma unroll
-        for (int i = 0; i < SH::COPIES; ++i) {
-            const uint32_t r = uint32_t(min(crow[i], last));
-            copy16_base(kp, r * uint32_t(2 * a.k_token) + kpiece[i], dst + 1024 * i);
-            copy16_base(vp, r * uint32_t(2 * a.v_token) + vpiece[i], dst + SH::TILE + 1024 * i);
-        }
-    };
-
     // addresses of the operands' reads in a stage
-    uint32_t ka[4], va[4];
+    constexpr int KA = CH == 8 ? 4 : 8;
+    uint32_t ka[KA], va[4];
+#pragma unroll
+    for (int i = 0; i < KA; ++i) ka[i] = lds0 + col * ROW + 16 * key_slot<CH>(col, 2 * i + half);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        ka[i] = lds0 + col * ROW + 16 * key_slot<CH>(col, 2 * i + half);
         const int r = 4 * half + (lane & 15) / 4, sub = (lane >> 4) & 1;
         va[i] = lds0 + SH::TILE + r * ROW + 16 * value_slot<CH>(r, (CH == 8 ? 4 * (i & 1) : 4 * i) + 2 * sub + ((lane & 3) >> 1)) +
                 8 * (lane & 1);
@@ -167,110 +192,248 @@ __global__ __launch_bounds__(64 * SH::WAVES) void attn_prefill_kernel(PrefillArg
         for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
     float m = -INFINITY, l = 0.0f;
 
-    if (tiles > 0) copy(0);
-    for (int t = 0; t < tiles; ++t) {
-        wait_vmcnt<0>();
-        barrier_lds();
-        if (t + 1 < tiles) copy(t + 1);
-        const int j0 = t * BK;
-        if (j0 > wave_any) continue;
-        const uint32_t stage = (t & 1) * 2 * SH::TILE;
-        v16f s[KT];
+    // One product of the scores, or of the output, at a time, its operand read AHEAD
+    // products before.
+    constexpr int NS = DS * KT, NO = 2 * DT * KT, AHEAD = 4;
+    auto key_frag = [&](int stage, int n) {
+        const int i = n / KT, kt = n % KT;
+        return lds_read16(ka[i % KA] + (stage + kt * 32 * ROW + (i / KA) * 32 * KA));
+    };
+    auto value_frag = [&](int stage, int n) {
+        const int dt = n % DT, ku = n / DT;
+        const uint32_t x = va[dt & 3] + (stage + 16 * ku * ROW + (dt >> 2) * 256);
+        const v4s lo = lds_read_tr(x), hi = lds_read_tr(x + 8 * ROW);
+        return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    // Scores of the tile in a stage; `between(n)` is put behind product n.
+    auto scores = [&](int stage, v16f (&s)[KT], auto between) {
+        v8bf f[AHEAD];
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) f[n] = key_frag(stage, n);
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[kt][r] = 0.0f;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < DS; ++i)
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-                s[kt] = mfma_bf16_32(lds_read16(ka[i & 3] + stage + kt * 32 * ROW + (i >> 2) * 128), q[i], s[kt]);
-        if (j0 + BK - 1 > wave_all) {
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (j0 + 32 * kt + 8 * (r / 4) + 4 * half + r % 4 > limit) s[kt][r] = -INFINITY;
+        for (int n = 0; n < NS; ++n) {
+            s[n % KT] = mfma_bf16_32(f[n % AHEAD], q[n / KT], s[n % KT]);
+            if (n + AHEAD < NS) f[n % AHEAD] = key_frag(stage, n + AHEAD);
+            between(n);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        float top = s[0][0];
+    };
+    auto mask = [&](int t, v16f (&s)[KT]) {
+        const int j0 = (t * WK + wk) * BK;
+        if (j0 + BK - 1 <= wave_all) return;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kt][r]);
+            for (int r = 0; r < 16; ++r)
+                if (j0 + 32 * kt + 8 * (r / 4) + 4 * half + r % 4 > limit) s[kt][r] = -INFINITY;
+    };
+    // A maximum that grew by less than 2^8 stays where it was: the weights reach 256 at most.
+    auto raise = [&](float top) {
         top = fmaxf(m, max_over_halves(top));
-        // A maximum that grew by less than 2^8 stays where it was: the weights reach 256 at most.
-        if (__any((top - m) * c > 8.0f)) {
-            const float f = top == -INFINITY ? 1.0f : exp2_fast((m - top) * c);
+        if (!__any((top - m) * c > 8.0f)) return;
+        const float f = top == -INFINITY ? 1.0f : exp2_fast((m - top) * c);
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[i][r] *= f;
+        m = top;
+    };
+
+    // Software pipeline: the scores of the next tile are computed between the weights of
+    // this one, and their maximum between the products of this one's weights.
+    v16f s0[KT], s1[KT];
+    wait_vmcnt<0>();
+    barrier_lds();
+    if (wave_tiles > 0) {
+        scores(0, s0, [](int) {});
+        mask(0, s0);
+        float top = -INFINITY;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s0[kt][r]);
+        raise(top);
+    }
+    // Tile t, in stage STAGE, from its scores s; those of tile t + 1 go to next.
+    auto tile = [&](int t, auto stage_tag, v16f (&s)[KT], v16f (&next)[KT]) {
+        constexpr int HERE = decltype(stage_tag)::value * 2 * SH::TILE, THERE = 2 * SH::TILE - HERE;
+        wait_vmcnt<0>();
+        barrier_lds();
+        const Source from = source(t + 2, t + 1);
+        auto copy = [&](int n) {
+            if (n < SH::COPIES)
+                copy_k(from, n);
+            else
+                copy_v(from, n - SH::COPIES);
+        };
+        if (t >= wave_tiles) {
+#pragma unroll
+            for (int n = 0; n < 2 * SH::COPIES; ++n) copy(n);
+            return;
+        }
+        const float base = m == -INFINITY ? 0.0f : m * c;
+        uint32_t w[KT][8];
+        // Pairs of weights, spread over the products: scaled one product ahead, raised, and packed one behind,
+        // so that no instruction waits for the one before it.
+        constexpr int PAIRS = 8 * KT;
+        auto pairs = [&](int n, auto what) {
+            if (n < 0 || n >= NS) return;
+#pragma unroll
+            for (int e = PAIRS * n / NS; e < PAIRS * (n + 1) / NS; ++e) what(e / 8, e % 8);
+        };
+        auto scaled = [&](int kt, int i) {
+#pragma unroll
+            for (int r = 2 * i; r < 2 * i + 2; ++r) s[kt][r] = __builtin_fmaf(s[kt][r], c, -base);
+        };
+        auto raised = [&](int kt, int i) {
+#pragma unroll
+            for (int r = 2 * i; r < 2 * i + 2; ++r) s[kt][r] = exp2_fast(s[kt][r]);
+        };
+        auto packed = [&](int kt, int i) {
+            w[kt][i] = pack_bf16x2(s[kt][2 * i], s[kt][2 * i + 1]);
+            l = add_weights(w[kt][i], l);
+            asm volatile("" : "+v"(w[kt][i]), "+v"(l));  // (here, not behind the branch below)
+        };
+        pairs(0, scaled);
+        // (behind the last tile: scores of whatever the stage holds, not used)
+        scores(THERE, next, [&](int n) {
+#pragma unroll
+            for (int i = 2 * SH::COPIES * n / NS; i < 2 * SH::COPIES * (n + 1) / NS; ++i) copy(i);
+            pairs(n + 1, scaled);
+            pairs(n, raised);
+            pairs(n - 1, packed);
+        });
+        pairs(NS - 1, packed);
+        v8bf f[AHEAD];
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) f[n] = value_frag(HERE, n);
+        if (t + 1 < wave_tiles) mask(t + 1, next);
+        float top = -INFINITY;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < NO; ++n) {
+            const int dt = n % DT, ku = n / DT, kt = ku / 2, u = ku % 2;
+            const v8bf p = as_bf(make_uint4(w[kt][4 * u], w[kt][4 * u + 1], w[kt][4 * u + 2], w[kt][4 * u + 3]));
+            o[dt] = mfma_bf16_32(f[n % AHEAD], p, o[dt]);
+            if (n + AHEAD < NO) f[n % AHEAD] = value_frag(HERE, n + AHEAD);
+            constexpr int EACH = (16 * KT + NO - 1) / NO;
+#pragma unroll
+            for (int e = EACH * n; e < EACH * (n + 1) && e < 16 * KT; ++e) top = fmaxf(top, next[e / 16][e % 16]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (t + 1 < wave_tiles) raise(top);
+    };
+    for (int t = 0; t < rounds; t += 2) {
+        tile(t, std::integral_constant<int, 0>{}, s0, s1);
+        if (t + 1 < rounds) tile(t + 1, std::integral_constant<int, 1>{}, s1, s0);
+    }
+    wait_vmcnt<0>();  // (the copies behind the last tile)
+    l = sum_over_halves(l);
+
+    barrier_lds();  // (every wave's copies have landed, and its reads are done)
+    if constexpr (WK > 1) {
+        // the groups' parts, scaled to the common maximum, are added in the groups' order
+        uint8_t* const slab = lds + ((wk - 1) * SH::WQ + wq) * SH::SLAB;  // (not of group 0)
+        if (wk > 0) {
+#pragma unroll
+            for (int i = 0; i < 4 * DT; ++i)
+                reinterpret_cast<float4*>(slab)[64 * i + lane] = make_float4(o[i / 4][4 * (i % 4)], o[i / 4][4 * (i % 4) + 1],
+                                                                             o[i / 4][4 * (i % 4) + 2], o[i / 4][4 * (i % 4) + 3]);
+            reinterpret_cast<float2*>(slab + 4096 * DT)[lane] = make_float2(m, l);
+        }
+        barrier_lds();
+        if (wk == 0) {
+            float2 st[WK - 1];
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < WK - 1; ++k) {
+                st[k] = reinterpret_cast<const float2*>(lds + (k * SH::WQ + wq) * SH::SLAB + 4096 * DT)[lane];
+                top = fmaxf(top, st[k].x);
+            }
+            const float base = top == -INFINITY ? 0.0f : top, f = exp2_fast((m - base) * c);
             l *= f;
 #pragma unroll
             for (int i = 0; i < DT; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[i][r] *= f;
-            m = top;
-        }
-        const float base = m == -INFINITY ? 0.0f : m * c;
-        v8bf p[KT][2];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
+            for (int k = 0; k < WK - 1; ++k) {
+                const float fk = exp2_fast((st[k].x - base) * c);
+                l += st[k].y * fk;
+                const float4* const other = reinterpret_cast<const float4*>(lds + (k * SH::WQ + wq) * SH::SLAB);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                s[kt][r] = exp2_fast(__builtin_fmaf(s[kt][r], c, -base));
-                l += s[kt][r];
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                p[kt][u] = as_bf(make_uint4(pack_bf16x2(s[kt][8 * u], s[kt][8 * u + 1]), pack_bf16x2(s[kt][8 * u + 2], s[kt][8 * u + 3]),
-                                            pack_bf16x2(s[kt][8 * u + 4], s[kt][8 * u + 5]),
-                                            pack_bf16x2(s[kt][8 * u + 6], s[kt][8 * u + 7])));
-        }
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    const uint32_t ad = va[dt & 3] + stage + (32 * kt + 16 * u) * ROW + (dt >> 2) * 256;
-                    const v4s lo = lds_read_tr(ad), hi = lds_read_tr(ad + 8 * ROW);
-                    const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                    o[dt] = mfma_bf16_32(v, p[kt][u], o[dt]);
+                for (int i = 0; i < 4 * DT; ++i) {
+                    const float4 x = other[64 * i + lane];
+                    o[i / 4][4 * (i % 4)] += x.x * fk, o[i / 4][4 * (i % 4) + 1] += x.y * fk;
+                    o[i / 4][4 * (i % 4) + 2] += x.z * fk, o[i / 4][4 * (i % 4) + 3] += x.w * fk;
+                    if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (few of them in registers at a time)
                 }
+            }
+        }
+        barrier_lds();
+        if (wk > 0) return;
     }
 
-    if (row >= Lq) return;
-    l = sum_over_halves(l);
+    // A lane holds one row's output in pieces of 4 d; through LDS it leaves in whole rows
+    // (each wave in a part of its own, so that only its own writes are waited for).
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;  // (a row that sees no key: zeros)
-    uint16_t* const op = a.o + (q0 + row) * a.o_token + head * a.o_head;
+    uint8_t* const mine = lds + wq * 32 * ROW;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int d = 32 * dt + 8 * n + 4 * half;
-            if (d < D)
-                *reinterpret_cast<uint2*>(op + d) = make_uint2(pack_bf16x2(o[dt][4 * n] * inv, o[dt][4 * n + 1] * inv),
-                                                               pack_bf16x2(o[dt][4 * n + 2] * inv, o[dt][4 * n + 3] * inv));
-        }
+        for (int n = 0; n < 4; ++n)
+            *reinterpret_cast<uint2*>(mine + col * ROW + 16 * key_slot<CH>(col, 4 * dt + n) + 8 * half) =
+                make_uint2(pack_bf16x2(o[dt][4 * n] * inv, o[dt][4 * n + 1] * inv),
+                           pack_bf16x2(o[dt][4 * n + 2] * inv, o[dt][4 * n + 3] * inv));
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32 / PER; ++i) {
+        const int r = i * PER + lane / CH, piece = lane % CH;
+        const uint4 x = *reinterpret_cast<const uint4*>(mine + r * ROW + 16 * key_slot<CH>(r, piece));
+        if (row0 + r < Lq && 8 * piece < D)
+            *reinterpret_cast<uint4*>(a.o + (q0 + row0 + r) * a.o_token + head * a.o_head + 8 * piece) = x;
+    }
 }
 
 template <class SH>
 void launch_shape(const PrefillArgs& a, hipStream_t st) {
     const int blocks = a.M / SH::BQ + a.seqs;
-    hipLaunchKernelGGL((attn_prefill_kernel<SH>), dim3(uint32_t(blocks) * uint32_t(a.q_heads)), dim3(64 * SH::WAVES), 0, st, a,
+    hipLaunchKernelGGL((attn_prefill_kernel<SH>), dim3(uint32_t(blocks) * uint32_t(a.q_heads)), dim3(SH::THREADS), 0, st, a,
                        blocks);
+}
+
+template <int DP>
+void launch_rows(const PrefillArgs& a, bool few, hipStream_t st) {
+    if (few)
+        launch_shape<Shape<DP, 2, 2, DP <= 64 ? 64 : 32>>(a, st);
+    else
+        launch_shape<Shape<DP, 4, 1, DP <= 128 ? 64 : 32>>(a, st);
 }
 
 }  // namespace
 
-hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t stream) {
+hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t stream) {
+    const int forced = hooks().attn_prefill.load(std::memory_order_relaxed);
+    const int64_t columns = attn_rows_groups(a), blocks = (int64_t(a.M) / kPrefillRows + a.seqs) * a.q_heads;
+    if (forced < 0 ? columns <= dev.cus : forced == 0) return launch_attn_rows(a, stream);
+    const bool few = forced < 0 ? 2 * blocks < 3 * int64_t(dev.cus) : forced == 1;
     if (a.head_dim <= 64)
-        launch_shape<Shape<64, 4>>(a, stream);
+        launch_rows<64>(a, few, stream);
     else if (a.head_dim <= 96)
-        launch_shape<Shape<96, 4>>(a, stream);
+        launch_rows<96>(a, few, stream);
     else if (a.head_dim <= 128)
-        launch_shape<Shape<128, 4>>(a, stream);
+        launch_rows<128>(a, few, stream);
     else if (a.head_dim <= 192)
-        launch_shape<Shape<192, 4>>(a, stream);
+        launch_rows<192>(a, few, stream);
     else
-        launch_shape<Shape<256, 4>>(a, stream);
+        launch_rows<256>(a, few, stream);
     return hipGetLastError();
 }
 

@@ -1,0 +1,131 @@
+// Attention of prompts of few rows (gfx950, wave64).
+//
+// The operator of fq_attn_prefill.hip where its blocks of rows would leave most of the chip
+// idle.  A workgroup takes 16 columns of one key head, consecutive rows' query heads of
+// its group, and its waves take tiles of 32 keys in turn and join at the end: a row's keys are
+// shared out over the waves instead of passing one wave (fq_attn_columns.h).
+#include <hip/hip_runtime.h>
+
+#include "fq_attn.h"
+#include "fq_attn_columns.h"
+#include "fq_device.h"
+#include "fq_internal.h"
+
+namespace fq {
+namespace {
+
+constexpr int kColumns = kDecodeHeads;
+
+template <int DP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, int64_t blocks) {
+    using Cols = Columns<DP, false>;
+    using Unit = typename Cols::Unit;
+    __shared__ __attribute__((aligned(16))) typename Cols::template Meeting<WAVES> lds;
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kvh = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
+    const int64_t b = blocks - 1 - int64_t(blockIdx.x / a.kv_heads);  // (the blocks that see most keys first)
+    auto first = [&](int s) { return int64_t(max(0, min(a.cu_q[s], a.M))) * group / kColumns + s; };
+    const int seq = find_sequence(a.seqs, b, first);
+    if (seq < 0) return;
+    auto range = [](const int32_t* cu, int s, int M, int& begin, int& count) {
+        begin = __builtin_amdgcn_readfirstlane(max(0, min(cu[s], M)));
+        count = __builtin_amdgcn_readfirstlane(max(0, min(cu[s + 1], M) - begin));
+    };
+    int q0, Lq, k0, Lk;
+    range(a.cu_q, seq, a.M, q0, Lq);
+    range(a.cu_k, seq, a.M_k, k0, Lk);
+    const int64_t column0 = (b - first(seq)) * kColumns;
+    if (column0 < 0 || column0 >= int64_t(Lq) * group) return;
+    const int D = a.head_dim, shift = Lk - Lq;  // row i sees the keys up to i + shift
+    auto row_of = [&](int c) { return int((column0 + c) / group); };
+    const int row = row_of(col), row_first = row_of(0), row_last = min(row_of(kColumns - 1), Lq - 1);
+    const int head = kvh * group + int((column0 + col) % group);
+    const int limit = row >= Lq ? -1 : a.causal ? min(row + shift, Lk - 1) : Lk - 1;  // the column's last key
+    const int all = row_of(kColumns - 1) >= Lq ? -1 : a.causal ? min(row_first + shift, Lk - 1) : Lk - 1;  // every column's
+    const int end = a.causal ? min(row_last + shift + 1, Lk) : Lk;
+
+    Cols x;
+    x.load_query(row < Lq ? a.q + (q0 + row) * a.q_token + head * a.q_head : nullptr, D);
+    const float c = a.scale * kLog2e;
+    const uint8_t* const kbase = reinterpret_cast<const uint8_t*>(a.k + k0 * a.k_token + kvh * a.k_head);
+    const uint8_t* const vbase = reinterpret_cast<const uint8_t*>(a.v + k0 * a.v_token + kvh * a.v_head);
+    const uint32_t kstride = uint32_t(2 * a.k_token), vstride = uint32_t(2 * a.v_token);
+    Unit u[2];
+    auto find = [&](int t) {  // (rows behind the sequence's last are read as that one)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = min(t + kDecodeUnit * i, Lk - 1);
+            u[i] = Unit{kbase + 2 * (j * a.k_token), vbase + 2 * (j * a.v_token), nullptr, nullptr,
+                        t + kDecodeUnit * i < Lk ? min(15, Lk - 1 - j) : 0};
+        }
+    };
+    int t = kDecodeTile * wave;
+    if (t < end) {
+        find(t);
+        x.load_k(u, D, kstride);
+        x.load_v(u, D, vstride);
+    }
+    for (; t < end; t += kDecodeTile * WAVES) {
+        const bool more = t + kDecodeTile * WAVES < end;
+        float s[8], scale[8];
+        x.scores(c, s, scale);
+        if (t + kDecodeTile - 1 > all) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (t + kDecodeUnit * (i / 4) + 4 * g + i % 4 > limit) s[i] = -INFINITY;
+        }
+        if (more) {
+            find(t + kDecodeTile * WAVES);
+            x.load_k(u, D, kstride);
+        }
+        x.add(s, scale);
+        if (more) x.load_v(u, D, vstride);
+    }
+    x.meet(lds, wave);
+
+    const int quads = D / 4;
+    for (int i = threadIdx.x; i < kColumns * quads; i += 64 * WAVES) {
+        const int column = i / quads, d = 4 * (i - column * quads), r = row_of(column);
+        if (r >= Lq) continue;
+        float top, sum;
+        const float4 v = Cols::joined(lds, column, d, top, sum);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // (a row that sees no key: zeros)
+        *reinterpret_cast<uint2*>(a.o + (q0 + r) * a.o_token + (kvh * group + int((column0 + column) % group)) * a.o_head + d) =
+            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+    }
+}
+
+}  // namespace
+
+// Workgroups of a call.
+int64_t attn_rows_groups(const PrefillArgs& a) {
+    return (int64_t(a.M) * (a.q_heads / a.kv_heads) / kColumns + a.seqs) * a.kv_heads;
+}
+
+namespace {
+
+template <int DP>
+void launch_waves(const PrefillArgs& a, hipStream_t st) {
+    constexpr int WAVES = DP <= 128 ? 8 : 4;  // (a wave of the larger ones takes more than half of a SIMD's registers)
+    const int64_t groups = attn_rows_groups(a);
+    hipLaunchKernelGGL((attn_rows_kernel<DP, WAVES>), dim3(uint32_t(groups)), dim3(64 * WAVES), 0, st, a, groups / a.kv_heads);
+}
+
+}  // namespace
+
+hipError_t launch_attn_rows(const PrefillArgs& a, hipStream_t stream) {
+    if (a.head_dim <= 64)
+        launch_waves<64>(a, stream);
+    else if (a.head_dim <= 96)
+        launch_waves<96>(a, stream);
+    else if (a.head_dim <= 128)
+        launch_waves<128>(a, stream);
+    else if (a.head_dim <= 192)
+        launch_waves<192>(a, stream);
+    else
+        launch_waves<256>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace fq
