@@ -421,8 +421,14 @@ void launch_rows(const PrefillArgs& a, bool few, hipStream_t st) {
 
 hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t stream) {
     const int forced = hooks().attn_prefill.load(std::memory_order_relaxed);
-    const int64_t columns = attn_rows_groups(a), blocks = (int64_t(a.M) / kPrefillRows + a.seqs) * a.q_heads;
-    if (forced < 0 ? columns <= dev.cus : forced == 0) return launch_attn_rows(a, stream);
+    // Few rows: as long as its workgroups are about one to a CU (graph-replayed, us, rows / blocks of 64 / of 128:
+    // 28 heads on 4 of 128, 128 rows 6.4 / 7.9 / 8.2, 256 rows 11.6 / 9.4 / 10.1; 8 heads on 1 of 256, 512 rows 15.8 /
+    // 18.1 / 23.4, 1024 rows 32.1 / 27.1 / 38.6).  Blocks of 64 rows with the keys shared by two groups of waves:
+    // where blocks of 128 would be fewer than three to two CUs (28 on 4 of 128, 1024 rows 21.4 / 23.7, 2048 rows
+    // 46.3 / 46.2, 4096 rows 149 / 129; 16 heads of 64, 2048 rows 21.7 / 29.5, 8192 rows 177 / 175; 8 on 1 of 256,
+    // 4096 rows 92 / 128, 8192 rows 324 / 289).
+    const int64_t groups = attn_rows_groups(a), blocks = (int64_t(a.M) / kPrefillRows + a.seqs) * a.q_heads;
+    if (forced < 0 ? 8 * groups <= 9 * int64_t(dev.cus) : forced == 0) return launch_attn_rows(a, stream);
     const bool few = forced < 0 ? 2 * blocks < 3 * int64_t(dev.cus) : forced == 1;
     if (a.head_dim <= 64)
         launch_rows<64>(a, few, stream);
