@@ -30,39 +30,32 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
 }
 
-// 8 keys of one d (eight times, for 8 consecutive d) from rows of 8 keys.
-__device__ __forceinline__ void transpose8(const uint4 (&r)[8], v8bf (&out)[8]) {
-    uint32_t w[8][4];
+// 8 keys of one d, for the d's of dword c of a lane's piece (bf16: two; codes: four), from rows of 8 keys.
+__device__ __forceinline__ void transpose_dword(const uint4 (&r)[8], int c, v8bf (&out)[2]) {
+    uint32_t lo[4], hi[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        const uint32_t a[4] = {r[2 * p].x, r[2 * p].y, r[2 * p].z, r[2 * p].w};
-        const uint32_t b[4] = {r[2 * p + 1].x, r[2 * p + 1].y, r[2 * p + 1].z, r[2 * p + 1].w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            w[2 * c][p] = __builtin_amdgcn_perm(b[c], a[c], 0x05040100u);
-            w[2 * c + 1][p] = __builtin_amdgcn_perm(b[c], a[c], 0x07060302u);
-        }
+        const uint4 &x = r[2 * p], &y = r[2 * p + 1];
+        const uint32_t a = c == 0 ? x.x : c == 1 ? x.y : c == 2 ? x.z : x.w, b = c == 0 ? y.x : c == 1 ? y.y : c == 2 ? y.z : y.w;
+        lo[p] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+        hi[p] = __builtin_amdgcn_perm(b, a, 0x07060302u);
     }
-#pragma unroll
-    for (int t = 0; t < 8; ++t) out[t] = as_bf(make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]));
+    out[0] = as_bf(make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    out[1] = as_bf(make_uint4(hi[0], hi[1], hi[2], hi[3]));
 }
-__device__ __forceinline__ void transpose8(const uint2 (&r)[8], v8bf (&out)[8]) {
-    uint32_t w[8][4];
+__device__ __forceinline__ void transpose_dword(const uint2 (&r)[8], int c, v8bf (&out)[4]) {
+    uint32_t w[4][4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        const uint32_t a[2] = {r[2 * p].x, r[2 * p].y}, b[2] = {r[2 * p + 1].x, r[2 * p + 1].y};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const uint32_t lo = __builtin_amdgcn_perm(b[c], a[c], 0x05010400u);
-            const uint32_t hi = __builtin_amdgcn_perm(b[c], a[c], 0x07030602u);
-            w[4 * c][p] = codes_bf16<false>(lo);
-            w[4 * c + 1][p] = codes_bf16<true>(lo);
-            w[4 * c + 2][p] = codes_bf16<false>(hi);
-            w[4 * c + 3][p] = codes_bf16<true>(hi);
-        }
+        const uint32_t a = c ? r[2 * p].y : r[2 * p].x, b = c ? r[2 * p + 1].y : r[2 * p + 1].x;
+        const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x05010400u), hi = __builtin_amdgcn_perm(b, a, 0x07030602u);
+        w[0][p] = codes_bf16<false>(lo);
+        w[1][p] = codes_bf16<true>(lo);
+        w[2][p] = codes_bf16<false>(hi);
+        w[3][p] = codes_bf16<true>(hi);
     }
 #pragma unroll
-    for (int t = 0; t < 8; ++t) out[t] = as_bf(make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]));
+    for (int t = 0; t < 4; ++t) out[t] = as_bf(make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]));
 }
 
 // DP: head_dim rounded up to a size with code of its own.  A lane's pieces past
@@ -71,10 +64,13 @@ __device__ __forceinline__ void transpose8(const uint2 (&r)[8], v8bf (&out)[8]) 
 template <int DP, bool FP8>
 struct Columns {
     static constexpr int ES = FP8 ? 1 : 2;                     // bytes of a value
+    static constexpr int LEAST = DP == 64 ? 16 : DP == 96 ? 80 : DP == 128 ? 112 : DP == 192 ? 144 : 208;  // head_dim
     static constexpr int KL = FP8 ? (DP + 63) / 64 : DP / 32;  // loads of 16 bytes of a lane's key
     static constexpr int KM = FP8 ? 2 * KL : KL;               // products of a unit
     static constexpr int HV = (DP + 127) / 128;                // pieces of 8 d of a lane's value
     static constexpr int LD = DP + 4;                          // (floats; a column's row in LDS starts on another bank)
+    // The query in LDS where its registers would cost a wave's place on the SIMD.
+    static constexpr bool QL = !FP8 && DP > 128;
     using vpiece = std::conditional_t<FP8, uint2, uint4>;
 
     // 16 rows of keys and of values, from the first; the scales of theirs that the lane needs.
@@ -84,27 +80,48 @@ struct Columns {
         int last;  // row that the ones behind it are read as (15: all are there)
     };
 
-    v8bf q[KM];
+    v8bf q[QL ? 1 : KM];
     uint4 kf[2][KL];
     vpiece vf[HV][8];
     float4 ks[2], vs[2];
     v4f acc[HV][8];
     float m = -INFINITY, l = 0.0f;
 
-    // The column's query (nullptr: zeros).
-    __device__ __forceinline__ void load_query(const uint16_t* p, int D) {
-        const int g = (threadIdx.x & 63) >> 4;
+    // What the waves share: their parts' outputs, maxima and sums, and the query.
+    template <int WAVES>
+    struct Shared {
+        float part[WAVES][kDecodeHeads][LD];
+        float stat[2][WAVES][kDecodeHeads];
+        uint4 query[QL ? KM : 1][64];
+    };
+
+    // The column's query (nullptr: zeros).  With QL a barrier has to follow.
+    template <int WAVES>
+    __device__ __forceinline__ void load_query(const uint16_t* p, int D, Shared<WAVES>& lds) {
+        const int lane = threadIdx.x & 63, g = lane >> 4;
+        if (!QL || threadIdx.x < 64) {
 #pragma unroll
-        for (int j = 0; j < KM; ++j) {
-            const int d = FP8 ? 64 * (j / 2) + 16 * g + 8 * (j % 2) : 32 * j + 8 * g;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (p && d < D) v = *reinterpret_cast<const uint4*>(p + d);
-            q[j] = as_bf(v);
+            for (int j = 0; j < KM; ++j) {
+                const int d = FP8 ? 64 * (j / 2) + 16 * g + 8 * (j % 2) : 32 * j + 8 * g;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (p && d < D) v = *reinterpret_cast<const uint4*>(p + d);
+                if constexpr (QL)
+                    lds.query[j][lane] = v;
+                else
+                    q[j] = as_bf(v);
+            }
         }
 #pragma unroll
         for (int i = 0; i < HV; ++i)
 #pragma unroll
             for (int t = 0; t < 8; ++t) acc[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    template <int WAVES>
+    __device__ __forceinline__ v8bf query(const Shared<WAVES>& lds, int j) const {
+        if constexpr (QL)
+            return as_bf(lds.query[j][threadIdx.x & 63]);
+        else
+            return q[j];
     }
 
     // kstride, vstride: bytes from row to row.
@@ -115,8 +132,8 @@ struct Columns {
             const uint32_t row = uint32_t(u[i].last < 15 ? min(col, u[i].last) : col) * kstride;
 #pragma unroll
             for (int j = 0; j < KL; ++j) {
-                const int at = 16 * (4 * j + g);
-                kf[i][j] = *reinterpret_cast<const uint4*>(u[i].k + (row + (at < D * ES ? at : 0)));
+                const bool ok = 16 * (4 * j + 3) < LEAST * ES || 16 * (4 * j + g) < D * ES;
+                kf[i][j] = *reinterpret_cast<const uint4*>(ok ? u[i].k + (row + 16 * g) + 64 * j : u[i].k + row);
             }
             if constexpr (FP8) {
                 ks[i] = *reinterpret_cast<const float4*>(u[i].ks + 4 * g);
@@ -133,14 +150,17 @@ struct Columns {
                 const uint32_t row = uint32_t(u[i].last < 15 ? min(4 * g + j, u[i].last) : 4 * g + j) * vstride;
 #pragma unroll
                 for (int hv = 0; hv < HV; ++hv) {
-                    const int d = 128 * hv + 8 * col;
-                    vf[hv][4 * i + j] = *reinterpret_cast<const vpiece*>(u[i].v + (row + (d < D ? d * ES : 0)));
+                    const bool ok = 128 * hv + 120 < LEAST || 128 * hv + 8 * col < D;
+                    vf[hv][4 * i + j] =
+                        *reinterpret_cast<const vpiece*>(ok ? u[i].v + (row + 8 * ES * col) + 128 * ES * hv : u[i].v + row);
                 }
             }
     }
 
     // The scores of the loaded keys, times c (and the key's scale), and the values' scales.
-    __device__ __forceinline__ void scores(float c, float (&x)[8], float (&w)[8]) {
+    template <int WAVES>
+    __device__ __forceinline__ void scores(const Shared<WAVES>& lds, float c, float (&x)[8], float (&w)[8]) {
+        if constexpr (QL) asm volatile("" ::: "memory");  // (read again for every tile)
         v4f s[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -150,11 +170,11 @@ struct Columns {
                 if constexpr (FP8) {
                     const uint4 k = kf[i][j];
                     s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k.x), codes_bf16<true>(k.x),
-                                                         codes_bf16<false>(k.y), codes_bf16<true>(k.y))), q[2 * j], s[i]);
+                                                         codes_bf16<false>(k.y), codes_bf16<true>(k.y))), query(lds, 2 * j), s[i]);
                     s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k.z), codes_bf16<true>(k.z),
-                                                         codes_bf16<false>(k.w), codes_bf16<true>(k.w))), q[2 * j + 1], s[i]);
+                                                         codes_bf16<false>(k.w), codes_bf16<true>(k.w))), query(lds, 2 * j + 1), s[i]);
                 } else {
-                    s[i] = mfma_bf16_16(as_bf(kf[i][j]), q[j], s[i]);
+                    s[i] = mfma_bf16_16(as_bf(kf[i][j]), query(lds, j), s[i]);
                 }
             }
         }
@@ -196,21 +216,20 @@ struct Columns {
                                         pack_bf16x2(x[6], x[7])));
 #pragma unroll
         for (int hv = 0; hv < HV; ++hv) {
-            v8bf vt[8];
-            transpose8(vf[hv], vt);
+            constexpr int EACH = FP8 ? 4 : 2;  // d's of a dword
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[hv][k] = mfma_bf16_16(vt[k], p, acc[hv][k]);
+            for (int w = 0; w < 8 / EACH; ++w) {
+                v8bf vt[EACH];
+                transpose_dword(vf[hv], w, vt);
+#pragma unroll
+                for (int k = 0; k < EACH; ++k) acc[hv][EACH * w + k] = mfma_bf16_16(vt[k], p, acc[hv][EACH * w + k]);
+            }
         }
     }
 
     // The waves' parts, each scaled to the common maximum, meet in LDS.
     template <int WAVES>
-    struct Meeting {
-        float part[WAVES][kDecodeHeads][LD];
-        float stat[2][WAVES][kDecodeHeads];  // maxima, sums
-    };
-    template <int WAVES>
-    __device__ __forceinline__ void meet(Meeting<WAVES>& lds, int wave) {
+    __device__ __forceinline__ void meet(Shared<WAVES>& lds, int wave) {
         const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
         l = sum_over_rows(l);
         if (g == 0) {
@@ -239,7 +258,7 @@ struct Columns {
     }
     // Four d of a column from there: the sums over the waves, their maximum and the weights' sum.
     template <int WAVES>
-    static __device__ __forceinline__ float4 joined(const Meeting<WAVES>& lds, int column, int d, float& top, float& sum) {
+    static __device__ __forceinline__ float4 joined(const Shared<WAVES>& lds, int column, int d, float& top, float& sum) {
         top = lds.stat[0][0][column];
         sum = 0.0f;
 #pragma unroll

@@ -67,10 +67,10 @@ __device__ __forceinline__ Part find_part(const DecodeArgs& a, int w, int target
 }
 
 template <int DP, bool FP8>
-__global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs a, uint64_t magic, int target, int head_tiles) {
+__global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a, uint64_t magic, int target, int head_tiles) {
     using Cols = Columns<DP, FP8>;
     using Unit = typename Cols::Unit;
-    __shared__ __attribute__((aligned(16))) typename Cols::template Meeting<kDecodeWaves> lds;
+    __shared__ __attribute__((aligned(16))) typename Cols::template Shared<kDecodeWaves> lds;
 
     const KvCache& kc = a.cache;
     const int D = kc.head_dim, lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs a, uint64_t
     const uint32_t row_bytes = uint32_t(D * Cols::ES);
 
     Cols x;
-    x.load_query(col < heads ? a.q + seq * a.q_token + (head0 + col) * a.q_head : nullptr, D);
+    x.load_query(col < heads ? a.q + seq * a.q_token + (head0 + col) * a.q_head : nullptr, D, lds);
     const float c = a.scale * kLog2e;
 
     Unit u[2];
@@ -110,25 +110,36 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs a, uint64_t
         }
     };
     int t = begin + kDecodeTile * wave;
-    if (t < end) {
-        find(t);
-        x.load_k(u, D, row_bytes);
-        x.load_v(u, D, row_bytes);
-    }
-    for (; t < end; t += kDecodeStep) {
+    // (Two copies of the loop's body: with the next tile's loads behind a branch, the waits for this one's
+    // values would have to count on either and so wait for the next keys.)
+    auto tile = [&](auto more) {
         const int seen[2] = {valid[0], valid[1]};
-        const bool more = t + kDecodeStep < end;
-        if (more) find(t + kDecodeStep);
+        if constexpr (decltype(more)::value) find(t + kDecodeStep);
         float s[8], scale[8];
-        x.scores(c, s, scale);
+        x.scores(lds, c, s, scale);
         if (seen[0] != kDecodeUnit || seen[1] != kDecodeUnit) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (4 * g + i % 4 >= seen[i / 4]) x.drop(i, s, scale);
         }
-        if (more) x.load_k(u, D, row_bytes);
+        // (the next keys are on their way before the values are waited for, and older than the next values)
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(more)::value) x.load_k(u, D, row_bytes);
+        __builtin_amdgcn_sched_barrier(0);
         x.add(s, scale);
-        if (more) x.load_v(u, D, row_bytes);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(more)::value) x.load_v(u, D, row_bytes);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (Cols::QL) __syncthreads();
+    if (t < end) {
+        find(t);
+        x.load_k(u, D, row_bytes);
+        __builtin_amdgcn_sched_barrier(0);
+        x.load_v(u, D, row_bytes);
+        __builtin_amdgcn_sched_barrier(0);
+        for (; t + kDecodeStep < end; t += kDecodeStep) tile(std::true_type{});
+        tile(std::false_type{});
     }
     x.meet(lds, wave);
 

@@ -20,7 +20,7 @@ template <int DP, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, int64_t blocks) {
     using Cols = Columns<DP, false>;
     using Unit = typename Cols::Unit;
-    __shared__ __attribute__((aligned(16))) typename Cols::template Meeting<WAVES> lds;
+    __shared__ __attribute__((aligned(16))) typename Cols::template Shared<WAVES> lds;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, in
     const int end = a.causal ? min(row_last + shift + 1, Lk) : Lk;
 
     Cols x;
-    x.load_query(row < Lq ? a.q + (q0 + row) * a.q_token + head * a.q_head : nullptr, D);
+    x.load_query(row < Lq ? a.q + (q0 + row) * a.q_token + head * a.q_head : nullptr, D, lds);
     const float c = a.scale * kLog2e;
     const uint8_t* const kbase = reinterpret_cast<const uint8_t*>(a.k + k0 * a.k_token + kvh * a.k_head);
     const uint8_t* const vbase = reinterpret_cast<const uint8_t*>(a.v + k0 * a.v_token + kvh * a.v_head);
@@ -61,26 +61,34 @@ __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, in
         }
     };
     int t = kDecodeTile * wave;
-    if (t < end) {
-        find(t);
-        x.load_k(u, D, kstride);
-        x.load_v(u, D, vstride);
-    }
-    for (; t < end; t += kDecodeTile * WAVES) {
-        const bool more = t + kDecodeTile * WAVES < end;
+    auto tile = [&](auto more) {  // (two copies of it: see fq_attn_decode.hip)
         float s[8], scale[8];
-        x.scores(c, s, scale);
+        x.scores(lds, c, s, scale);
         if (t + kDecodeTile - 1 > all) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (t + kDecodeUnit * (i / 4) + 4 * g + i % 4 > limit) s[i] = -INFINITY;
         }
-        if (more) {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(more)::value) {
             find(t + kDecodeTile * WAVES);
             x.load_k(u, D, kstride);
         }
+        __builtin_amdgcn_sched_barrier(0);
         x.add(s, scale);
-        if (more) x.load_v(u, D, vstride);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(more)::value) x.load_v(u, D, vstride);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (Cols::QL) __syncthreads();
+    if (t < end) {
+        find(t);
+        x.load_k(u, D, kstride);
+        __builtin_amdgcn_sched_barrier(0);
+        x.load_v(u, D, vstride);
+        __builtin_amdgcn_sched_barrier(0);
+        for (; t + kDecodeTile * WAVES < end; t += kDecodeTile * WAVES) tile(std::true_type{});
+        tile(std::false_type{});
     }
     x.meet(lds, wave);
 
@@ -107,7 +115,7 @@ namespace {
 
 template <int DP>
 void launch_waves(const PrefillArgs& a, hipStream_t st) {
-    constexpr int WAVES = DP <= 128 ? 8 : 4;  // (a wave of the larger ones takes more than half of a SIMD's registers)
+    constexpr int WAVES = 8;  // (a wave of the larger ones takes more than half of a SIMD's registers)
     const int64_t groups = attn_rows_groups(a);
     hipLaunchKernelGGL((attn_rows_kernel<DP, WAVES>), dim3(uint32_t(groups)), dim3(64 * WAVES), 0, st, a, groups / a.kv_heads);
 }
