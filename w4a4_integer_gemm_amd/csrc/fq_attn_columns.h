@@ -58,15 +58,20 @@ __device__ __forceinline__ void transpose_dword(const uint2 (&r)[8], int c, v8bf
     for (int t = 0; t < 4; ++t) out[t] = as_bf(make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]));
 }
 
-// DP: head_dim rounded up to a size with code of its own.  A lane's pieces past
-// head_dim read the row's first piece: the query's zeros meet them in the first product, and
+// DP: head_dim rounded up to a size with code of its own.  Pieces past head_dim
+// are read as the row's first piece: the query's zeros meet them in the first product, and
 // the outputs of the second are not stored.
-template <int DP, bool FP8>
+// WHOLE: every unit has its 16 rows (a page's units do).
+template <int DP, bool FP8, bool WHOLE>
 struct Columns {
     static constexpr int ES = FP8 ? 1 : 2;                     // bytes of a value
     static constexpr int LEAST = DP == 64 ? 16 : DP == 96 ? 80 : DP == 128 ? 112 : DP == 192 ? 144 : 208;  // head_dim
-    static constexpr int KL = FP8 ? (DP + 63) / 64 : DP / 32;  // loads of 16 bytes of a lane's key
+    static constexpr int KL = FP8 ? (DP + 63) / 64 : DP / 32;  // 16-byte pieces of a lane's key
     static constexpr int KM = FP8 ? 2 * KL : KL;               // products of a unit
+    // Keys pass through LDS: they are loaded a few whole rows at a time, since 16 rows in
+    // 16 neighbouring lanes, as the product wants them, cost the address unit four times as much.
+    static constexpr int PIECES = DP * ES <= 64 ? 4 : DP * ES <= 128 ? 8 : DP * ES <= 256 ? 16 : 32;  // of a row in LDS
+    static constexpr int ROWS = 64 / PIECES, LOADS = kDecodeUnit / ROWS;  // rows of a load, loads of a unit
     static constexpr int HV = (DP + 127) / 128;                // pieces of 8 d of a lane's value
     static constexpr int LD = DP + 4;                          // (floats; a column's row in LDS starts on another bank)
     // The query in LDS where its registers would cost a wave's place on the SIMD.
@@ -77,11 +82,11 @@ struct Columns {
     struct Unit {
         const uint8_t *k, *v;
         const float *ks, *vs;
-        int last;  // row that the ones behind it are read as (15: all are there)
+        int last;  // row that the ones behind it are read as, with WHOLE 15
     };
 
     v8bf q[QL ? 1 : KM];
-    uint4 kf[2][KL];
+    u32x4 kf[2 * LOADS];
     vpiece vf[HV][8];
     float4 ks[2], vs[2];
     v4f acc[HV][8];
@@ -90,10 +95,16 @@ struct Columns {
     // What the waves share: their parts' outputs, maxima and sums, and the query.
     template <int WAVES>
     struct Shared {
-        float part[WAVES][kDecodeHeads][LD];
+        union {
+            float part[WAVES][kDecodeHeads][LD];
+            u32x4 keys[WAVES][kDecodeTile * (PIECES + 1)];  // (a wave's own)
+        };
         float stat[2][WAVES][kDecodeHeads];
         uint4 query[QL ? KM : 1][64];
     };
+    // Place of piece c of key r: a row is one piece longer than an even number of them, so that 16
+    // rows' pieces of one number lie in different banks.
+    static __device__ __forceinline__ int key_place(int r, int c) { return r * (PIECES + 1) + c; }
 
     // The column's query (nullptr: zeros).  With QL a barrier has to follow.
     template <int WAVES>
@@ -117,23 +128,28 @@ struct Columns {
             for (int t = 0; t < 8; ++t) acc[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
     }
     template <int WAVES>
-    __device__ __forceinline__ v8bf query(const Shared<WAVES>& lds, int j) const {
+    __device__ __forceinline__ v8bf query(const Shared<WAVES>& lds, int j, int lane) const {
         if constexpr (QL)
-            return as_bf(lds.query[j][threadIdx.x & 63]);
+            return as_bf(lds.query[j][lane]);
         else
             return q[j];
     }
 
-    // kstride, vstride: bytes from row to row.
+    // kstride, vstride: bytes from row to row.  (Both sides of a branch issue the same loads, so
+    // that the waits behind it know how many are in flight.)
     __device__ __forceinline__ void load_k(const Unit (&u)[2], int D, uint32_t kstride) {
-        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+        const int lane = threadIdx.x & 63, g = lane >> 4, row = lane / PIECES, at = 16 * (lane % PIECES);
+        const uint32_t piece = at < D * ES ? at : 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t row = uint32_t(u[i].last < 15 ? min(col, u[i].last) : col) * kstride;
+            if (WHOLE || u[i].last == 15) {
 #pragma unroll
-            for (int j = 0; j < KL; ++j) {
-                const bool ok = 16 * (4 * j + 3) < LEAST * ES || 16 * (4 * j + g) < D * ES;
-                kf[i][j] = *reinterpret_cast<const uint4*>(ok ? u[i].k + (row + 16 * g) + 64 * j : u[i].k + row);
+                for (int j = 0; j < LOADS; ++j)
+                    kf[LOADS * i + j] = *reinterpret_cast<const u32x4*>(u[i].k + uint64_t(ROWS * j) * kstride + (row * kstride + piece));
+            } else {
+#pragma unroll
+                for (int j = 0; j < LOADS; ++j)
+                    kf[LOADS * i + j] = *reinterpret_cast<const u32x4*>(u[i].k + (uint32_t(min(ROWS * j + row, u[i].last)) * kstride + piece));
             }
             if constexpr (FP8) {
                 ks[i] = *reinterpret_cast<const float4*>(u[i].ks + 4 * g);
@@ -142,39 +158,46 @@ struct Columns {
         }
     }
     __device__ __forceinline__ void load_v(const Unit (&u)[2], int D, uint32_t vstride) {
-        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+        const int col = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t row = uint32_t(u[i].last < 15 ? min(4 * g + j, u[i].last) : 4 * g + j) * vstride;
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int hv = 0; hv < HV; ++hv) {
-                    const bool ok = 128 * hv + 120 < LEAST || 128 * hv + 8 * col < D;
-                    vf[hv][4 * i + j] =
-                        *reinterpret_cast<const vpiece*>(ok ? u[i].v + (row + 8 * ES * col) + 128 * ES * hv : u[i].v + row);
+                    const bool there = 128 * hv + 120 < LEAST || 128 * hv + 8 * col < D;
+                    const uint32_t piece = there ? 8 * ES * col : 0;
+                    const uint8_t* const p = u[i].v + (there ? 128 * ES * hv : 0);
+                    if (WHOLE || u[i].last == 15)
+                        vf[hv][4 * i + j] = *reinterpret_cast<const vpiece*>(p + uint64_t(j) * vstride + (4 * g * vstride + piece));
+                    else
+                        vf[hv][4 * i + j] = *reinterpret_cast<const vpiece*>(p + (uint32_t(min(4 * g + j, u[i].last)) * vstride + piece));
                 }
-            }
     }
 
     // The scores of the loaded keys, times c (and the key's scale), and the values' scales.
     template <int WAVES>
-    __device__ __forceinline__ void scores(const Shared<WAVES>& lds, float c, float (&x)[8], float (&w)[8]) {
-        if constexpr (QL) asm volatile("" ::: "memory");  // (read again for every tile)
+    __device__ __forceinline__ void scores(Shared<WAVES>& lds, int wave, float c, float (&x)[8], float (&w)[8]) {
+        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+        u32x4* const keys = lds.keys[wave];
+#pragma unroll
+        for (int n = 0; n < 2 * LOADS; ++n) keys[key_place(ROWS * n + lane / PIECES, lane % PIECES)] = kf[n];
+        int at = lane;
+        if constexpr (QL) asm volatile("" : "+v"(at));  // (so that the query is read again for every tile)
         v4f s[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             s[i] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < KL; ++j) {
+                const u32x4 k = keys[key_place(kDecodeUnit * i + col, 4 * j + g)];
                 if constexpr (FP8) {
-                    const uint4 k = kf[i][j];
-                    s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k.x), codes_bf16<true>(k.x),
-                                                         codes_bf16<false>(k.y), codes_bf16<true>(k.y))), query(lds, 2 * j), s[i]);
-                    s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k.z), codes_bf16<true>(k.z),
-                                                         codes_bf16<false>(k.w), codes_bf16<true>(k.w))), query(lds, 2 * j + 1), s[i]);
+                    s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k[0]), codes_bf16<true>(k[0]),
+                                                         codes_bf16<false>(k[1]), codes_bf16<true>(k[1]))), query(lds, 2 * j, at), s[i]);
+                    s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k[2]), codes_bf16<true>(k[2]),
+                                                         codes_bf16<false>(k[3]), codes_bf16<true>(k[3]))), query(lds, 2 * j + 1, at), s[i]);
                 } else {
-                    s[i] = mfma_bf16_16(as_bf(kf[i][j]), query(lds, j), s[i]);
+                    s[i] = mfma_bf16_16(__builtin_bit_cast(v8bf, k), query(lds, j, at), s[i]);
                 }
             }
         }
@@ -231,7 +254,7 @@ struct Columns {
     template <int WAVES>
     __device__ __forceinline__ void meet(Shared<WAVES>& lds, int wave) {
         const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-        l = sum_over_rows(l);
+        l = sum_over_rows(l);  // (the barrier below is behind every wave's last reading of its keys)
         if (g == 0) {
             lds.stat[0][wave][col] = m;
             lds.stat[1][wave][col] = l;

@@ -68,7 +68,7 @@ __device__ __forceinline__ Part find_part(const DecodeArgs& a, int w, int target
 
 template <int DP, bool FP8>
 __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a, uint64_t magic, int target, int head_tiles) {
-    using Cols = Columns<DP, FP8>;
+    using Cols = Columns<DP, FP8, true>;
     using Unit = typename Cols::Unit;
     __shared__ __attribute__((aligned(16))) typename Cols::template Shared<kDecodeWaves> lds;
 
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a, uint6
         const int seen[2] = {valid[0], valid[1]};
         if constexpr (decltype(more)::value) find(t + kDecodeStep);
         float s[8], scale[8];
-        x.scores(lds, c, s, scale);
+        x.scores(lds, wave, c, s, scale);
         if (seen[0] != kDecodeUnit || seen[1] != kDecodeUnit) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

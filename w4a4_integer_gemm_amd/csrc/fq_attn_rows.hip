@@ -18,7 +18,7 @@ constexpr int kColumns = kDecodeHeads;
 
 template <int DP, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, int64_t blocks) {
-    using Cols = Columns<DP, false>;
+    using Cols = Columns<DP, false, false>;
     using Unit = typename Cols::Unit;
     __shared__ __attribute__((aligned(16))) typename Cols::template Shared<WAVES> lds;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, in
     int t = kDecodeTile * wave;
     auto tile = [&](auto more) {  // (two copies of it: see fq_attn_decode.hip)
         float s[8], scale[8];
-        x.scores(lds, c, s, scale);
+        x.scores(lds, wave, c, s, scale);
         if (t + kDecodeTile - 1 > all) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
