@@ -58,10 +58,19 @@ __device__ __forceinline__ int32_t scalar_load(const int32_t* p, int64_t i) {
 // first(s), which grows by at least one with s, and the ones behind it.  -1: none.
 template <class First>
 __device__ __forceinline__ int find_sequence(int seqs, int64_t b, First first) {
+    if (seqs == 1) return 0;
     const int lane = threadIdx.x & 63;
     int n = 0;
     for (int s0 = 0; s0 < seqs; s0 += 64) n += __popcll(__ballot(s0 + lane < seqs && first(s0 + lane) <= b));
     return __builtin_amdgcn_readfirstlane(n - 1);
+}
+// Rows of sequence s, cut off at [0, M].
+struct Rows {
+    int begin, count;
+};
+__device__ __forceinline__ Rows sequence_rows(const int32_t* cu, int s, int M) {
+    const int begin = max(0, min(scalar_load(cu, s), M));
+    return Rows{begin, max(0, min(scalar_load(cu, s + 1), M) - begin)};
 }
 
 }  // namespace fq

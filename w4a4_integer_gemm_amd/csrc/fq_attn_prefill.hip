@@ -85,15 +85,10 @@ __global__ __launch_bounds__(SH::THREADS) void attn_prefill_kernel(PrefillArgs a
     auto first = [&](int s) { return max(0, min(a.cu_q[s], a.M)) / BQ + s; };
     const int seq = find_sequence(a.seqs, b, first);
     if (seq < 0) return;
-    const int at_row = __builtin_amdgcn_readfirstlane((b - first(seq)) * BQ);
-    auto range = [](const int32_t* cu, int s, int M, int& begin, int& count) {
-        begin = __builtin_amdgcn_readfirstlane(max(0, min(cu[s], M)));
-        count = __builtin_amdgcn_readfirstlane(max(0, min(cu[s + 1], M) - begin));
-    };
-    int q0, Lq, k0, Lk;
-    range(a.cu_q, seq, a.M, q0, Lq);
+    const Rows qr = sequence_rows(a.cu_q, seq, a.M), kr = sequence_rows(a.cu_k, seq, a.M_k);
+    const int q0 = qr.begin, Lq = qr.count, k0 = kr.begin, Lk = kr.count;
+    const int at_row = (b - (q0 / BQ + seq)) * BQ;
     if (at_row < 0 || at_row >= Lq) return;
-    range(a.cu_k, seq, a.M_k, k0, Lk);
     const int D = a.head_dim, kvh = head / (a.q_heads / a.kv_heads);
     const int shift = Lk - Lq;  // row i sees the keys up to i + shift
     const int rows = min(BQ, Lq - at_row);

@@ -28,14 +28,9 @@ __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, in
     auto first = [&](int s) { return int64_t(max(0, min(a.cu_q[s], a.M))) * group / kColumns + s; };
     const int seq = find_sequence(a.seqs, b, first);
     if (seq < 0) return;
-    auto range = [](const int32_t* cu, int s, int M, int& begin, int& count) {
-        begin = __builtin_amdgcn_readfirstlane(max(0, min(cu[s], M)));
-        count = __builtin_amdgcn_readfirstlane(max(0, min(cu[s + 1], M) - begin));
-    };
-    int q0, Lq, k0, Lk;
-    range(a.cu_q, seq, a.M, q0, Lq);
-    range(a.cu_k, seq, a.M_k, k0, Lk);
-    const int64_t column0 = (b - first(seq)) * kColumns;
+    const Rows qr = sequence_rows(a.cu_q, seq, a.M), kr = sequence_rows(a.cu_k, seq, a.M_k);
+    const int q0 = qr.begin, Lq = qr.count, k0 = kr.begin, Lk = kr.count;
+    const int64_t column0 = (b - (int64_t(q0) * group / kColumns + seq)) * kColumns;
     if (column0 < 0 || column0 >= int64_t(Lq) * group) return;
     const int D = a.head_dim, shift = Lk - Lq;  // row i sees the keys up to i + shift
     auto row_of = [&](int c) { return int((column0 + c) / group); };

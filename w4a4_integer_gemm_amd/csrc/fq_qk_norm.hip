@@ -21,13 +21,14 @@
 namespace fq {
 namespace {
 
-// Sum over L consecutive lanes (a power of two up to 16, aligned).
+// Sum over L consecutive lanes (a power of two up to 32, aligned).
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
     if constexpr (L > 1) v += __int_as_float(dpp_i<0xB1>(__float_as_int(v)));   // quad_perm [1,0,3,2]
     if constexpr (L > 2) v += __int_as_float(dpp_i<0x4E>(__float_as_int(v)));   // quad_perm [2,3,0,1]
     if constexpr (L > 4) v += __int_as_float(dpp_i<0x141>(__float_as_int(v)));  // row_half_mirror
     if constexpr (L > 8) v += __int_as_float(dpp_i<0x140>(__float_as_int(v)));  // row_mirror
+    if constexpr (L > 16) v += __shfl_xor(v, 16);
     return v;
 }
 
@@ -135,55 +136,64 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(QkNormArgs a, int share) {
     }
 }
 
-// Any even rot_dim: a wave per head of a token, lane l on elements l, l + 64, ...
-// Every element and its partner are loaded before the first is stored.
-__global__ __launch_bounds__(64) void qk_norm_wave_kernel(QkNormArgs a) {
-    const int m = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
-    const uint16_t* const xp = a.x + m * a.x_token + h * a.x_head;
-    uint16_t* const yp = a.y + m * a.y_token + h * a.y_head;
-    const bool normed = h < a.q_heads + a.k_heads;
-    if (!normed && a.x == a.y) return;
-    const float* const g = h < a.q_heads ? a.q_gamma : a.k_gamma;
-    const int rh = a.rot_dim / 2;
-    float x[4], z[4];
-    int partner[4];
-    float ss = 0.0f;
+// Any even rot_dim: an element's partner may be in any lane, so a head's normed values pass
+// through LDS.  A thread owns 8 consecutive elements of one token, L lanes a head.
+template <int L>
+__global__ __launch_bounds__(256) void qk_norm_any_kernel(QkNormArgs a, int share) {
+    // (the lanes of a head are in one wave, whose LDS accesses stay in order)
+    __shared__ __attribute__((aligned(16))) float rows[256 / L][8 * L + 4];
+    const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t m = idx / L;
+    if (m >= uint32_t(a.M)) return;
+    const bool active = int(idx % L) < a.head_dim / 8;
+    const int e = active ? 8 * int(idx % L) : 0, rh = a.rot_dim / 2;  // (the lanes past the head repeat its first piece)
+    float* const row = rows[threadIdx.x / L];
+    int partner[8];
+    float c[8], s[8];  // y = n c + partner s
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int e = lane + 64 * k;
-        partner[k] = e >= a.rot_dim ? e : a.interleaved ? e ^ 1 : e < rh ? e + rh : e - rh;
-        x[k] = e < a.head_dim ? bf16_lo(xp[e]) : 0.0f;
-        z[k] = e < a.head_dim ? bf16_lo(xp[partner[k]]) : 0.0f;
-        ss = __builtin_fmaf(x[k], x[k], ss);
+    for (int j = 0; j < 8; ++j) {
+        const int x = e + j;
+        partner[j] = x, c[j] = 1.0f, s[j] = 0.0f;
+        if (x >= a.rot_dim) continue;
+        partner[j] = a.interleaved ? x ^ 1 : x < rh ? x + rh : x - rh;
+        const int32_t pos = a.positions ? a.positions[m] : a.pos0 + int32_t(m);
+        cos_sin_turns(angle(a.freq[a.interleaved ? x / 2 : x < rh ? x : x - rh], pos), &c[j], &s[j]);
+        c[j] *= a.attn_scale;
+        s[j] *= x < partner[j] ? -a.attn_scale : a.attn_scale;
     }
-    if (!normed) {
+    const int h0 = blockIdx.y * share, h1 = h0 + share < a.heads ? h0 + share : a.heads;
+    const uint16_t* const xp = a.x + m * a.x_token + e;
+    uint4 next[2];  // the two heads behind the current one
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int e = lane + 64 * k;
-            if (e < a.head_dim) yp[e] = uint16_t(__float_as_uint(x[k]) >> 16);
-        }
-        return;
-    }
-    ss = lanes_sum<16>(ss);
-    ss += __shfl_xor(ss, 16);
-    ss += __shfl_xor(ss, 32);
-    const float inv = 1.0f / sqrtf(ss / float(a.head_dim) + a.eps);
-    const int32_t pos = a.positions ? a.positions[m] : a.pos0 + m;
+    for (int k = 0; k < 2; ++k) next[k] = *reinterpret_cast<const uint4*>(xp + min(h0 + k, h1 - 1) * a.x_head);
+    for (int h = h0; h < h1; ++h) {
+        uint4 u = next[0];
+        next[0] = next[1];
+        next[1] = *reinterpret_cast<const uint4*>(xp + min(h + 2, h1 - 1) * a.x_head);
+        if (h < a.q_heads + a.k_heads) {
+            const float* const g = h < a.q_heads ? a.q_gamma : a.k_gamma;
+            float p[8];
+            unpack8(u, p);
+            float ss = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int e = lane + 64 * k;
-        if (e >= a.head_dim) continue;
-        float v = x[k] * inv * (g ? g[e] : 1.0f);
-        if (e < a.rot_dim) {
-            const float w = z[k] * inv * (g ? g[partner[k]] : 1.0f);
-            const bool first = e < partner[k];
-            float c, s;
-            cos_sin_turns(angle(a.freq[a.interleaved ? e / 2 : first ? e : e - rh], pos), &c, &s);
-            c *= a.attn_scale;
-            s *= a.attn_scale;
-            v = __builtin_fmaf(v, c, first ? -(w * s) : w * s);
+            for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(p[j], p[j], ss);
+            ss = lanes_sum<L>(active ? ss : 0.0f);
+            const float inv = 1.0f / sqrtf(ss / float(a.head_dim) + a.eps);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = p[j] * inv * (g ? g[e + j] : 1.0f);
+            if (active) {
+                *reinterpret_cast<float4*>(row + e) = make_float4(p[0], p[1], p[2], p[3]);
+                *reinterpret_cast<float4*>(row + e + 4) = make_float4(p[4], p[5], p[6], p[7]);
+            }
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = __builtin_fmaf(p[j], c[j], row[partner[j]] * s[j]);
+            asm volatile("" ::: "memory");
+            u = pack8(p);
+        } else if (a.x == a.y) {
+            continue;
         }
-        yp[e] = uint16_t(pack_bf16x2(v, 0.0f));
+        if (active) *reinterpret_cast<uint4*>(a.y + m * a.y_token + h * a.y_head + e) = u;
     }
 }
 
@@ -215,13 +225,27 @@ hipError_t launch_lanes(const QkNormArgs& a, hipStream_t st) {
     return launch_items<INTER, 16>(a, st);
 }
 
+template <int L>
+hipError_t launch_any(const QkNormArgs& a, hipStream_t st) {
+    const int64_t threads = int64_t(a.M) * L;
+    int64_t parts = kFill / threads;
+    parts = parts < 1 ? 1 : parts > a.heads ? a.heads : parts;
+    const int share = int((a.heads + parts - 1) / parts);
+    hipLaunchKernelGGL((qk_norm_any_kernel<L>), dim3(uint32_t((threads + 255) / 256), uint32_t((a.heads + share - 1) / share)),
+                       dim3(256), 0, st, a, share);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_qk_norm(const QkNormArgs& a, hipStream_t stream) {
     if (a.interleaved && a.rot_dim % 8 == 0) return launch_lanes<true>(a, stream);
     if (!a.interleaved && a.rot_dim % 16 == 0) return launch_lanes<false>(a, stream);
-    hipLaunchKernelGGL(qk_norm_wave_kernel, dim3(uint32_t(a.M), uint32_t(a.heads)), dim3(64), 0, stream, a);
-    return hipGetLastError();
+    if (a.head_dim <= 16) return launch_any<2>(a, stream);
+    if (a.head_dim <= 32) return launch_any<4>(a, stream);
+    if (a.head_dim <= 64) return launch_any<8>(a, stream);
+    if (a.head_dim <= 128) return launch_any<16>(a, stream);
+    return launch_any<32>(a, stream);
 }
 
 }  // namespace fq
