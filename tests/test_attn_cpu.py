@@ -246,3 +246,14 @@ def test_paged_reads_stay_inside_the_cache_and_cover_every_token_once(tmp_path):
     subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", f"-I{CSRC}", str(src), "-o", str(exe)], check=True)
     units, wrong = (int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split())
     assert units > 10000 and wrong == 0
+
+
+def test_hook_takes_the_prompt_kernels_and_nothing_else():
+    L = fq.lib()
+    try:
+        for good in ("attn_prefill=rows", "attn_prefill=64", "attn_prefill=128", "attn_prefill=auto", ""):
+            assert L.fq_test_hook(good.encode()) == 0, good
+        for bad in ("attn_prefill=32", "attn_prefill=", "attn_prefil=64"):
+            assert L.fq_test_hook(bad.encode()) == 1, bad
+    finally:
+        L.fq_test_hook(b"")

@@ -2,7 +2,7 @@
 run under it (AddressSanitizer + UndefinedBehaviorSanitizer).
 
 The host code -- argument validation, error messages, the weight packer and
-dequantiser, the FP8 and rotary host parts (HOST_SOURCES) -- and the oracle (fqo.c) are compiled
+dequantiser, the FP8, rotary and attention host parts (HOST_SOURCES) -- and the oracle (fqo.c) are compiled
 with g++/gcc and -fsanitize=address,undefined; the HIP kernel objects are
 taken unchanged from the ordinary build (run build.py first), since device
 code is not sanitized.  The result, libfq_san.so and oracle/liboracle_san.so,
@@ -33,7 +33,7 @@ from w4a4_integer_gemm_amd.build import SOURCES as _LIB_SOURCES  # noqa: E402
 
 DEVICE_OBJECTS = [os.path.splitext(s)[0] + ".o" for s in _LIB_SOURCES if s.endswith(".hip")]
 TESTS = ["tests/test_abi_cpu.py", "tests/test_oracle_pins.py", "tests/test_fold_consistency.py",
-         "tests/test_block_cpu.py", "tests/test_fp8_refusals_cpu.py"]
+         "tests/test_block_cpu.py", "tests/test_fp8_refusals_cpu.py", "tests/test_attn_cpu.py"]
 
 
 def run(cmd):

@@ -10,7 +10,8 @@
 // leave their lane.  The other operand needs 8 keys of one d in a lane; lane l loads
 // 8 consecutive d of each of these 8 keys and pairs them up in registers, the d's of
 // its piece going to eight products.  e4m3 codes are exact in bf16; the key's scale
-// multiplies the score, the value's the weight before it is rounded to bf16.
+// multiplies the score, the value's the weight before it is rounded to bf16.  (Both products are the matrix
+// instruction's bf16 ones with float32 sums; the weights are rounded for it, at most 2^-8 of each.)
 #pragma once
 
 #include <hip/hip_runtime.h>

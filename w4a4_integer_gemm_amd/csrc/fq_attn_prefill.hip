@@ -12,10 +12,21 @@
 // keys that it presents to the second product, and the transposing LDS read gives
 // the other operand the same keys.
 //
-// Tiles go from global memory straight into LDS, the next one while the products of
-// the current one run; 16-byte pieces are swizzled, so that neither the first
-// operand's rows nor the transposing reads meet in a bank.  Rows behind a sequence's
-// last key are read as that key and masked, whatever lies there.
+// Tiles go from global memory straight into LDS, two stages of them, each copy issued
+// between two products; 16-byte pieces are swizzled, so that neither the first operand's rows
+// nor the transposing reads meet in a bank.  Rows behind a sequence's last key are read as that
+// key and masked, whatever lies there.
+//
+// A wave's loop is a software pipeline, so that the matrix unit has work while the vector unit makes
+// weights: the products of the next tile's scores are issued with this tile's scalings, powers and
+// packings between them, and those of the output with the next tile's maximum.  Operands are
+// read four products ahead.  Rounded: the weights, to bf16 (the sum takes them as rounded), and the output.
+//
+// 16384 rows, 28 heads on 4 of 128, causal: 1.70 ms, 1.13 PFLOP/s, where a bf16 product of 8192^3 by the library
+// runs at 1.2; the products keep the matrix unit busy for 64 % of the cycles, at the 1.65 to 1.8 GHz that the
+// power limit leaves it (the same loop of products alone: 1.74 PFLOP/s at 1.67 GHz).  4580 rows of eight
+// sequences: 59.7 us, 44 % busy: the last blocks, and a block's first loads and its epilogue (about 5 us).  1024 rows:
+// 19.2 us, 24 % busy: two blocks to a CU, whose 16 tiles follow one another.
 #include <hip/hip_runtime.h>
 
 #include <atomic>
@@ -417,11 +428,13 @@ void launch_rows(const PrefillArgs& a, bool few, hipStream_t st) {
 hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t stream) {
     const int forced = hooks().attn_prefill.load(std::memory_order_relaxed);
     // Few rows: as long as its workgroups are about one to a CU (graph-replayed, us, rows / blocks of 64 / of 128:
-    // 28 heads on 4 of 128, 128 rows 6.4 / 7.9 / 8.2, 256 rows 11.6 / 9.4 / 10.1; 8 heads on 1 of 256, 512 rows 15.8 /
-    // 18.1 / 23.4, 1024 rows 32.1 / 27.1 / 38.6).  Blocks of 64 rows with the keys shared by two groups of waves:
-    // where blocks of 128 would be fewer than three to two CUs (28 on 4 of 128, 1024 rows 21.4 / 23.7, 2048 rows
-    // 46.3 / 46.2, 4096 rows 149 / 129; 16 heads of 64, 2048 rows 21.7 / 29.5, 8192 rows 177 / 175; 8 on 1 of 256,
-    // 4096 rows 92 / 128, 8192 rows 324 / 289).
+    // 28 heads on 4 of 128, 128 rows 5.9 / 7.8 / 8.0, 256 rows 10.2 / 9.2 / 10.1; 16 heads of 64, 256 rows 5.8 /
+    // 6.7 / 7.6, 384 rows 8.5 / 7.5 / 9.0; 8 heads on 1 of 256, 512 rows 12.4 / 17.9 / 23.1, 1024 rows 26.2 / 26.7 /
+    // 39.0; 16 heads on 2 of 256 with 8 sequences of 64 rows 16.0 / 12.1 at two to a CU).  Blocks of 64 rows with the
+    // keys shared by two groups of waves: where blocks of 128 would be fewer than three to two CUs (28 on 4 of
+    // 128, 1024 rows 20.2 / 23.2, 2048 rows 46.3 / 46.2, 4096 rows 149 / 129; 40 on 8 of 128, 1024 rows 24.2 / 25.0;
+    // 16 heads of 64, 2048 rows 21.7 / 29.5, 8192 rows 177 / 175; 8 on 1 of 256, 4096 rows 92 / 128, 8192 rows 324 /
+    // 289).
     const int64_t groups = attn_rows_groups(a), blocks = (int64_t(a.M) / kPrefillRows + a.seqs) * a.q_heads;
     if (forced < 0 ? 8 * groups <= 9 * int64_t(dev.cus) : forced == 0) return launch_attn_rows(a, stream);
     const bool few = forced < 0 ? 2 * blocks < 3 * int64_t(dev.cus) : forced == 1;

@@ -7,6 +7,13 @@
 // Consecutive rows are consecutive tokens of one head: they lie behind one
 // another in the head layout and in a page, so that a wave reads and writes whole
 // lines.  blockIdx.y: 2 * head + (0: key, 1: value).
+//
+// e4m3: s = max|h| / 448 in float32, q = e4m3(h / s) with one rounding to nearest even; read back as
+// bf16(s q), one rounding more.  A row's scale is one store of the lane that holds its first piece.
+// 4580 tokens, 4 heads of 128, e4m3: written in 4.7 us (14 MB, 3.0 TB/s); 4571 tokens, 8 heads, read in 6.9 us
+// (28 MB, 4.1 TB/s).  Both are one round of waves: slot, row and store are three latencies in
+// a chain.  A thread with two or four tokens of a head, all loaded before the first store, was slower (8.0 us
+// for the reading).
 #include <hip/hip_runtime.h>
 
 #include "fq_device.h"

@@ -9,7 +9,11 @@
 // otherwise two neighbouring pieces.  head_dim / 16 items make a head; they sit
 // in 1 to 16 consecutive lanes (a power of two), which add their sums of squares
 // with lane moves.  A thread computes its item's angles once and applies them to
-// its share of the heads, UN heads' loads ahead of their stores.
+// its share of the heads, UN heads' loads ahead of their stores.  Sum, root, gain and rotation
+// are float32, one rounding to bf16 at the end.
+//
+// 4571 tokens of 36 heads of 128: 15.5 us for 84 MB (5.4 TB/s; its vector instructions issue for half of it).
+// One token of 12 heads of 256: 4.3 us, a launch and one memory latency.
 #include <hip/hip_runtime.h>
 
 #include "fq_angle.h"
@@ -137,7 +141,9 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(QkNormArgs a, int share) {
 }
 
 // Any even rot_dim: an element's partner may be in any lane, so a head's normed values pass
-// through LDS.  A thread owns 8 consecutive elements of one token, L lanes a head.
+// through LDS.  A thread owns 8 consecutive elements of one token, L lanes a head.  20000 tokens of 18
+// heads of 80, 40 of them rotated in halves: 57.6 us for 115 MB (2.0 TB/s); with 32 in halves, which the kernel
+// above takes, 25.2.
 template <int L>
 __global__ __launch_bounds__(256) void qk_norm_any_kernel(QkNormArgs a, int share) {
     // (the lanes of a head are in one wave, whose LDS accesses stay in order)
