@@ -12,8 +12,8 @@
 // its share of the heads, UN heads' loads ahead of their stores.  Sum, root, gain and rotation
 // are float32, one rounding to bf16 at the end.
 //
-// 4571 tokens of 36 heads of 128: 15.5 us for 84 MB (5.4 TB/s; its vector instructions issue for half of it).
-// One token of 12 heads of 256: 4.3 us, a launch and one memory latency.
+// 4571 tokens of 36 heads of 128: 15.5 us for 84 MB (5.4 TB/s, the Infinity Cache helping).
+// One token of 12 heads of 256: 3.8 us, a launch, one memory latency and eight pairs' angles in turn.
 #include <hip/hip_runtime.h>
 
 #include "fq_angle.h"
@@ -66,14 +66,18 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(QkNormArgs a, int share) {
     const bool rot_a = INTER ? ea < a.rot_dim : halves, rot_b = INTER ? eb < a.rot_dim : halves;
     float c[8], s[8];  // of the 8 pairs; interleaved: of the 4 pairs of each piece
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        c[j] = 1.0f, s[j] = 0.0f;
-        if (INTER ? (j < 4 ? rot_a : rot_b) : rot_a) {
-            const int32_t pos = a.positions ? a.positions[m] : a.pos0 + int32_t(m);
-            const int pair = INTER ? 8 * item + j : 8 * item + j;
-            cos_sin_turns(angle(a.freq[pair], pos), &c[j], &s[j]);
+    for (int j = 0; j < 8; ++j) c[j] = 1.0f, s[j] = 0.0f;
+    if (rot_a) {
+        const int32_t pos = a.positions ? a.positions[m] : a.pos0 + int32_t(m);
+        uint64_t f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = a.freq[8 * item + (!INTER || rot_b || j < 4 ? j : 0)];  // (one that exists)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            cos_sin_turns(angle(f[j], pos), &c[j], &s[j]);
             c[j] *= a.attn_scale;
             s[j] *= a.attn_scale;
+            if (INTER && j >= 4 && !rot_b) c[j] = 1.0f, s[j] = 0.0f;
         }
     }
     const int h0 = blockIdx.y * share, h1 = h0 + share < a.heads ? h0 + share : a.heads;
@@ -142,7 +146,7 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(QkNormArgs a, int share) {
 
 // Any even rot_dim: an element's partner may be in any lane, so a head's normed values pass
 // through LDS.  A thread owns 8 consecutive elements of one token, L lanes a head.  20000 tokens of 18
-// heads of 80, 40 of them rotated in halves: 57.6 us for 115 MB (2.0 TB/s); with 32 in halves, which the kernel
+// heads of 80, 40 of them rotated in halves: 56.2 us for 115 MB (2.0 TB/s); with 32 in halves, which the kernel
 // above takes, 25.2.
 template <int L>
 __global__ __launch_bounds__(256) void qk_norm_any_kernel(QkNormArgs a, int share) {
@@ -155,17 +159,22 @@ __global__ __launch_bounds__(256) void qk_norm_any_kernel(QkNormArgs a, int shar
     const int e = active ? 8 * int(idx % L) : 0, rh = a.rot_dim / 2;  // (the lanes past the head repeat its first piece)
     float* const row = rows[threadIdx.x / L];
     int partner[8];
+    uint64_t f[8];
     float c[8], s[8];  // y = n c + partner s
+    const int32_t pos = a.positions ? a.positions[m] : a.pos0 + int32_t(m);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int x = e + j;
-        partner[j] = x, c[j] = 1.0f, s[j] = 0.0f;
-        if (x >= a.rot_dim) continue;
-        partner[j] = a.interleaved ? x ^ 1 : x < rh ? x + rh : x - rh;
-        const int32_t pos = a.positions ? a.positions[m] : a.pos0 + int32_t(m);
-        cos_sin_turns(angle(a.freq[a.interleaved ? x / 2 : x < rh ? x : x - rh], pos), &c[j], &s[j]);
+        const bool rotated = x < a.rot_dim;
+        partner[j] = !rotated ? x : a.interleaved ? x ^ 1 : x < rh ? x + rh : x - rh;
+        f[j] = a.freq[!rotated ? 0 : a.interleaved ? x / 2 : x < rh ? x : x - rh];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        cos_sin_turns(angle(f[j], pos), &c[j], &s[j]);
         c[j] *= a.attn_scale;
-        s[j] *= x < partner[j] ? -a.attn_scale : a.attn_scale;
+        s[j] *= e + j < partner[j] ? -a.attn_scale : a.attn_scale;
+        if (e + j >= a.rot_dim) c[j] = 1.0f, s[j] = 0.0f;
     }
     const int h0 = blockIdx.y * share, h1 = h0 + share < a.heads ? h0 + share : a.heads;
     const uint16_t* const xp = a.x + m * a.x_token + e;
