@@ -6,14 +6,14 @@
 // lanes (a power of two), which find the row's maximum with lane moves.
 // Consecutive rows are consecutive tokens of one head: they lie behind one
 // another in the head layout and in a page, so that a wave reads and writes whole
-// lines.  blockIdx.y: 2 * head + (0: key, 1: value).
+// lines.  A thread takes a piece of the key and the same of the value (blockIdx.y: the
+// head), whose loads are in flight together.
 //
 // e4m3: s = max|h| / 448 in float32, q = e4m3(h / s) with one rounding to nearest even; read back as
 // bf16(s q), one rounding more.  A row's scale is one store of the lane that holds its first piece.
-// 4580 tokens, 4 heads of 128, e4m3: written in 4.7 us (14 MB, 3.0 TB/s); 4571 tokens, 8 heads, read in 6.9 us
-// (28 MB, 4.1 TB/s).  Both are one round of waves: slot, row and store are three latencies in
-// a chain.  A thread with two or four tokens of a head, all loaded before the first store, was slower (8.0 us
-// for the reading).
+// 32768 tokens, 8 heads of 128, e4m3: written in 39.4 us, read in 34.3 (203 MB, 5.2 and 5.9 TB/s; with a
+// thread each for key and value 46.5 and 43.1).  4571 tokens read in 6.9 us, 4580 of 4 heads written in
+// 5.1: one round of waves, slot, row and store three latencies in a chain.
 #include <hip/hip_runtime.h>
 
 #include "fq_device.h"
@@ -38,33 +38,42 @@ __device__ __forceinline__ float lanes_max_nonneg(float x) {
     return __uint_as_float(v);
 }
 
+// Index of a slot's row of a head.
+__device__ __forceinline__ int64_t slot_row(const KvCache& c, int32_t slot, int head) {
+    const int32_t page = slot / c.page_size;
+    return paged_row(page, slot - page * c.page_size, head, c.kv_heads, c.page_size);
+}
+
 template <int L, bool FP8>
 __global__ __launch_bounds__(256) void kv_write_kernel(KvCache c, KvRows k, KvRows v, const int32_t* slots, int32_t M) {
     const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
     const uint32_t m = idx / L;
     if (m >= uint32_t(M)) return;
-    const int e = 8 * int(idx % L), head = blockIdx.y >> 1;
-    const bool value = blockIdx.y & 1, active = e < c.head_dim;
-    const KvRows& src = value ? v : k;
+    const int e = 8 * int(idx % L), head = blockIdx.y;
+    const bool active = e < c.head_dim;
     const int32_t slot = slots[m];
+    const int at = active ? e : 0;
+    const uint4 x = *reinterpret_cast<const uint4*>(k.p + m * k.token + head * k.head + at);
+    const uint4 y = *reinterpret_cast<const uint4*>(v.p + m * v.token + head * v.head + at);
     if (slot < 0 || slot >= c.pages * c.page_size) return;  // (all lanes of a row)
-    const uint4 x = active ? *reinterpret_cast<const uint4*>(src.p + m * src.token + head * src.head + e)
-                           : make_uint4(0, 0, 0, 0);
-    const int32_t page = slot / c.page_size;
-    const int64_t row = paged_row(page, slot - page * c.page_size, head, c.kv_heads, c.page_size);
-    uint8_t* const rows = static_cast<uint8_t*>(value ? c.v : c.k);
+    const int64_t row = slot_row(c, slot, head);
     if constexpr (!FP8) {
-        if (active) *reinterpret_cast<uint4*>(rows + 2 * (row * c.head_dim + e)) = x;
+        if (!active) return;
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(c.k) + 2 * (row * c.head_dim + e)) = x;
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(c.v) + 2 * (row * c.head_dim + e)) = y;
     } else {
-        float h[8], top = 0.0f;
-        unpack8(x, h);
-        uint32_t t = 0;
+        auto one = [&](const uint4& in, void* rows, float* scales) {
+            float h[8];
+            unpack8(in, h);
+            uint32_t t = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t = max(t, __float_as_uint(h[j]) & 0x7FFFFFFFu);
-        top = lanes_max_nonneg<L>(__uint_as_float(t));
-        const float s = fp8_scale(top);
-        if (active) *reinterpret_cast<uint2*>(rows + row * c.head_dim + e) = fp8_codes8(h, s);
-        if (e == 0) (value ? c.v_scale : c.k_scale)[row] = s;
+            for (int j = 0; j < 8; ++j) t = max(t, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+            const float s = fp8_scale(lanes_max_nonneg<L>(__uint_as_float(t)));
+            if (active) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(rows) + row * c.head_dim + e) = fp8_codes8(h, s);
+            if (e == 0) scales[row] = s;
+        };
+        one(x, c.k, c.k_scale);
+        one(y, c.v, c.v_scale);
     }
 }
 
@@ -72,39 +81,42 @@ template <int L, bool FP8>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, KvRows k, KvRows v, const int32_t* slots, int32_t M) {
     const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
     const uint32_t m = idx / L;
-    const int e = 8 * int(idx % L), head = blockIdx.y >> 1;
+    const int e = 8 * int(idx % L), head = blockIdx.y;
     if (m >= uint32_t(M) || e >= c.head_dim) return;
-    const bool value = blockIdx.y & 1;
-    const KvRows& dst = value ? v : k;
     const int32_t slot = slots[m];
-    uint4 x = make_uint4(0, 0, 0, 0);
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
     if (slot >= 0 && slot < c.pages * c.page_size) {
-        const int32_t page = slot / c.page_size;
-        const int64_t row = paged_row(page, slot - page * c.page_size, head, c.kv_heads, c.page_size);
-        const uint8_t* const rows = static_cast<const uint8_t*>(value ? c.v : c.k);
+        const int64_t row = slot_row(c, slot, head);
         if constexpr (!FP8) {
-            x = *reinterpret_cast<const uint4*>(rows + 2 * (row * c.head_dim + e));
+            x = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.k) + 2 * (row * c.head_dim + e));
+            y = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.v) + 2 * (row * c.head_dim + e));
         } else {
-            const uint2 q = *reinterpret_cast<const uint2*>(rows + row * c.head_dim + e);
-            const float s = (value ? c.v_scale : c.k_scale)[row];
-            const uint32_t w[2] = {q.x, q.y};
-            float h[8];
+            const uint2 p = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + row * c.head_dim + e);
+            const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + row * c.head_dim + e);
+            const float ps = c.k_scale[row], qs = c.v_scale[row];
+            auto one = [](const uint2& q, float s) {
+                const uint32_t w[2] = {q.x, q.y};
+                float h[8];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[j]), false);
-                const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[j]), true);
-                h[4 * j] = lo[0] * s, h[4 * j + 1] = lo[1] * s, h[4 * j + 2] = hi[0] * s, h[4 * j + 3] = hi[1] * s;
-            }
-            x = pack8(h);
+                for (int j = 0; j < 2; ++j) {
+                    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[j]), false);
+                    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[j]), true);
+                    h[4 * j] = lo[0] * s, h[4 * j + 1] = lo[1] * s, h[4 * j + 2] = hi[0] * s, h[4 * j + 3] = hi[1] * s;
+                }
+                return pack8(h);
+            };
+            x = one(p, ps);
+            y = one(q, qs);
         }
     }
-    *reinterpret_cast<uint4*>(dst.p + m * dst.token + head * dst.head + e) = x;
+    *reinterpret_cast<uint4*>(k.p + m * k.token + head * k.head + e) = x;
+    *reinterpret_cast<uint4*>(v.p + m * v.token + head * v.head + e) = y;
 }
 
 template <int L>
 hipError_t launch_lanes(bool write, const KvCache& c, const KvRows& k, const KvRows& v, const int32_t* slots, int32_t M,
                         hipStream_t st) {
-    const dim3 grid(uint32_t((int64_t(M) * L + 255) / 256), uint32_t(2 * c.kv_heads));
+    const dim3 grid(uint32_t((int64_t(M) * L + 255) / 256), uint32_t(c.kv_heads));
     if (write && c.k_scale)
         hipLaunchKernelGGL((kv_write_kernel<L, true>), grid, dim3(256), 0, st, c, k, v, slots, M);
     else if (write)
