@@ -63,7 +63,8 @@ __device__ __forceinline__ void transpose_dword(const uint2 (&r)[8], int c, v8bf
 // are read as the row's first piece: the query's zeros meet them in the first product, and
 // the outputs of the second are not stored.
 // WHOLE: every unit has its 16 rows (a page's units do).
-template <int DP, bool FP8, bool WHOLE>
+// PARTS: workgroups that share a head's values and outputs, 128 d each (every one computes all weights).
+template <int DP, bool FP8, bool WHOLE, int PARTS = 1>
 struct Columns {
     static constexpr int ES = FP8 ? 1 : 2;                     // bytes of a value
     static constexpr int LEAST = DP == 64 ? 16 : DP == 96 ? 80 : DP == 128 ? 112 : DP == 192 ? 144 : 208;  // head_dim
@@ -73,8 +74,10 @@ struct Columns {
     // 16 neighbouring lanes, as the product wants them, cost the address unit four times as much.
     static constexpr int PIECES = DP * ES <= 64 ? 4 : DP * ES <= 128 ? 8 : DP * ES <= 256 ? 16 : 32;  // of a row in LDS
     static constexpr int ROWS = 64 / PIECES, LOADS = kDecodeUnit / ROWS;  // rows of a load, loads of a unit
-    static constexpr int HV = (DP + 127) / 128;                // pieces of 8 d of a lane's value
-    static constexpr int LD = DP + 4;                          // (floats; a column's row in LDS starts on another bank)
+    static constexpr int HV = (DP + 127) / 128 / PARTS;        // pieces of 8 d of a lane's value
+    static_assert(HV >= 1 && (PARTS == 1 || HV == 1), "a part is a piece of every lane");
+    static constexpr int VD = PARTS == 1 ? DP : 128;           // d of the values that a workgroup takes
+    static constexpr int LD = VD + 4;                          // (floats; a column's row in LDS starts on another bank)
     // The query in LDS where its registers would cost a wave's place on the SIMD.
     static constexpr bool QL = !FP8 && DP > 128;
     using vpiece = std::conditional_t<FP8, uint2, uint4>;
@@ -158,6 +161,7 @@ struct Columns {
             }
         }
     }
+    // D: of the values that the workgroup takes, whose first the units' rows are.
     __device__ __forceinline__ void load_v(const Unit (&u)[2], int D, uint32_t vstride) {
         const int col = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
 #pragma unroll
@@ -166,7 +170,7 @@ struct Columns {
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int hv = 0; hv < HV; ++hv) {
-                    const bool there = 128 * hv + 120 < LEAST || 128 * hv + 8 * col < D;
+                    const bool there = (PARTS == 1 && 128 * hv + 120 < LEAST) || 128 * hv + 8 * col < D;
                     const uint32_t piece = there ? 8 * ES * col : 0;
                     const uint8_t* const p = u[i].v + (there ? 128 * ES * hv : 0);
                     if (WHOLE || u[i].last == 15)
@@ -271,7 +275,7 @@ struct Columns {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int d = 128 * hv + 32 * g + 8 * r;
-                if (d >= DP) continue;
+                if (d >= VD) continue;
                 float* const out = &lds.part[wave][col][d];
                 *reinterpret_cast<float4*>(out) =
                     make_float4(acc[hv][0][r] * f, acc[hv][1][r] * f, acc[hv][2][r] * f, acc[hv][3][r] * f);

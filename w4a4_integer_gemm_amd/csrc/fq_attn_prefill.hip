@@ -436,7 +436,7 @@ hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipS
     // 16 heads of 64, 2048 rows 21.7 / 29.5, 8192 rows 177 / 175; 8 on 1 of 256, 4096 rows 92 / 128, 8192 rows 324 /
     // 289).
     const int64_t groups = attn_rows_groups(a), blocks = (int64_t(a.M) / kPrefillRows + a.seqs) * a.q_heads;
-    if (forced < 0 ? 8 * groups <= 9 * int64_t(dev.cus) : forced == 0) return launch_attn_rows(a, stream);
+    if (forced < 0 ? 8 * groups <= 9 * int64_t(dev.cus) : forced == 0) return launch_attn_rows(a, dev, stream);
     const bool few = forced < 0 ? 2 * blocks < 3 * int64_t(dev.cus) : forced == 1;
     if (a.head_dim <= 64)
         launch_rows<64>(a, few, stream);

@@ -5,9 +5,10 @@
 // its group, and its waves take tiles of 32 keys in turn and join at the end: a row's keys are
 // shared out over the waves instead of passing one wave (fq_attn_columns.h).
 //
-// Bound by the rate at which a CU is given the keys and values (about 95 GB/s of L2 each): 50 rows of 8 heads of
-// 256 on one key head, 866 keys: 25 workgroups, each reading all 887 kB, 14.8 us.  More workgroups would need a
-// workspace for their parts, which the call does not have.
+// Bound by what a CU is given of the keys and values (about 90 GB/s: a tile is requested
+// while the one before is worked on, and more do not fit the registers).  50 rows of 8 heads of 256 on one key head,
+// 866 keys: 25 groups of columns, 12.9 us.  More workgroups along the keys would need a workspace for their
+// parts, which the call does not have; along the values (PARTS) they only read all keys each.
 #include <hip/hip_runtime.h>
 
 #include "fq_attn.h"
@@ -20,15 +21,17 @@ namespace {
 
 constexpr int kColumns = kDecodeHeads;
 
-template <int DP, int WAVES>
+template <int DP, int WAVES, int PARTS>
 __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, int64_t blocks) {
-    using Cols = Columns<DP, false, false>;
+    using Cols = Columns<DP, false, false, PARTS>;
     using Unit = typename Cols::Unit;
     __shared__ __attribute__((aligned(16))) typename Cols::template Shared<WAVES> lds;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int kvh = blockIdx.x % a.kv_heads, group = a.q_heads / a.kv_heads;
-    const int64_t b = blocks - 1 - int64_t(blockIdx.x / a.kv_heads);  // (the blocks that see most keys first)
+    const int kvh = int(blockIdx.x / PARTS) % a.kv_heads, group = a.q_heads / a.kv_heads;
+    const int64_t b = blocks - 1 - int64_t(blockIdx.x / PARTS / a.kv_heads);  // (the blocks that see most keys first)
+    const int d0 = PARTS == 1 ? 0 : 128 * int(blockIdx.x % PARTS);             // the workgroup's first value,
+    const int Dv = PARTS == 1 ? a.head_dim : min(a.head_dim - d0, 128);        // and how many it takes
     auto first = [&](int s) { return int64_t(max(0, min(a.cu_q[s], a.M))) * group / kColumns + s; };
     const int seq = find_sequence(a.seqs, b, first);
     if (seq < 0) return;
@@ -48,7 +51,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, in
     x.load_query(row < Lq ? a.q + (q0 + row) * a.q_token + head * a.q_head : nullptr, D, lds);
     const float c = a.scale * kLog2e;
     const uint8_t* const kbase = reinterpret_cast<const uint8_t*>(a.k + k0 * a.k_token + kvh * a.k_head);
-    const uint8_t* const vbase = reinterpret_cast<const uint8_t*>(a.v + k0 * a.v_token + kvh * a.v_head);
+    const uint8_t* const vbase = reinterpret_cast<const uint8_t*>(a.v + k0 * a.v_token + kvh * a.v_head + d0);
     const uint32_t kstride = uint32_t(2 * a.k_token), vstride = uint32_t(2 * a.v_token);
     Unit u[2];
     auto find = [&](int t) {  // (rows behind the sequence's last are read as that one)
@@ -76,7 +79,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, in
         __builtin_amdgcn_sched_barrier(0);
         x.add(s, scale);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (decltype(more)::value) x.load_v(u, D, vstride);
+        if constexpr (decltype(more)::value) x.load_v(u, Dv, vstride);
         __builtin_amdgcn_sched_barrier(0);
     };
     if constexpr (Cols::QL) __syncthreads();
@@ -84,21 +87,21 @@ __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, in
         find(t);
         x.load_k(u, D, kstride);
         __builtin_amdgcn_sched_barrier(0);
-        x.load_v(u, D, vstride);
+        x.load_v(u, Dv, vstride);
         __builtin_amdgcn_sched_barrier(0);
         for (; t + kDecodeTile * WAVES < end; t += kDecodeTile * WAVES) tile(std::true_type{});
         tile(std::false_type{});
     }
     x.meet(lds, wave);
 
-    const int quads = D / 4;
+    const int quads = Dv / 4;
     for (int i = threadIdx.x; i < kColumns * quads; i += 64 * WAVES) {
         const int column = i / quads, d = 4 * (i - column * quads), r = row_of(column);
         if (r >= Lq) continue;
         float top, sum;
         const float4 v = Cols::joined(lds, column, d, top, sum);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // (a row that sees no key: zeros)
-        *reinterpret_cast<uint2*>(a.o + (q0 + r) * a.o_token + (kvh * group + int((column0 + column) % group)) * a.o_head + d) =
+        *reinterpret_cast<uint2*>(a.o + (q0 + r) * a.o_token + (kvh * group + int((column0 + column) % group)) * a.o_head + d0 + d) =
             make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
     }
 }
@@ -112,26 +115,38 @@ int64_t attn_rows_groups(const PrefillArgs& a) {
 
 namespace {
 
-template <int DP>
-void launch_waves(const PrefillArgs& a, hipStream_t st) {
+template <int DP, int PARTS>
+void launch_parts(const PrefillArgs& a, hipStream_t st) {
     constexpr int WAVES = 8;  // (a wave of the larger ones takes more than half of a SIMD's registers)
     const int64_t groups = attn_rows_groups(a);
-    hipLaunchKernelGGL((attn_rows_kernel<DP, WAVES>), dim3(uint32_t(groups)), dim3(64 * WAVES), 0, st, a, groups / a.kv_heads);
+    hipLaunchKernelGGL((attn_rows_kernel<DP, WAVES, PARTS>), dim3(uint32_t(groups) * PARTS), dim3(64 * WAVES), 0, st, a,
+                       groups / a.kv_heads);
+}
+
+template <int DP>
+void launch_waves(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t st) {
+    // Two workgroups for a group of columns, each with half of the values, where both get a CU of their own (8
+    // heads on 1 of 256, graph-replayed, us, one / two: 1 row on 817 keys 14.2 / 11.8, 50 on 866 15.8 / 12.9, 50 on
+    // 3050 39.1 / 31.8, 200 rows 9.2 / 7.9).
+    if constexpr (DP > 128) {
+        if (2 * attn_rows_groups(a) <= dev.cus) return launch_parts<DP, 2>(a, st);
+    }
+    launch_parts<DP, 1>(a, st);
 }
 
 }  // namespace
 
-hipError_t launch_attn_rows(const PrefillArgs& a, hipStream_t stream) {
+hipError_t launch_attn_rows(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t stream) {
     if (a.head_dim <= 64)
-        launch_waves<64>(a, stream);
+        launch_waves<64>(a, dev, stream);
     else if (a.head_dim <= 96)
-        launch_waves<96>(a, stream);
+        launch_waves<96>(a, dev, stream);
     else if (a.head_dim <= 128)
-        launch_waves<128>(a, stream);
+        launch_waves<128>(a, dev, stream);
     else if (a.head_dim <= 192)
-        launch_waves<192>(a, stream);
+        launch_waves<192>(a, dev, stream);
     else
-        launch_waves<256>(a, stream);
+        launch_waves<256>(a, dev, stream);
     return hipGetLastError();
 }
 

@@ -265,7 +265,7 @@ constexpr int kPrefillRows = 128;
 hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t stream);
 // The same for few rows (fq_attn_rows.hip), and its workgroups.
 int64_t attn_rows_groups(const PrefillArgs& a);
-hipError_t launch_attn_rows(const PrefillArgs& a, hipStream_t stream);
+hipError_t launch_attn_rows(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t stream);
 
 // Attention of one token per sequence over the paged cache (fq_attn_decode.hip).
 struct DecodeArgs {
