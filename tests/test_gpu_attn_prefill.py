@@ -11,7 +11,7 @@ from fqtest import bf16_to_f64, dev, host
 pytestmark = pytest.mark.gpu
 
 
-@pytest.fixture(params=["auto", "rows", "64", "128"], autouse=True)
+@pytest.fixture(params=["auto", "rows", "64", "128", "small"], autouse=True)
 def kernel(request, hook):
     """Every test on each of the kernels, and on the one that its sizes get."""
     hook(f"attn_prefill={request.param}")
@@ -84,6 +84,13 @@ def test_head_sizes(D, causal):
 def test_lengths(n, causal):
     for D in (64, 128, 256):
         run([n], 0, 2, 1, D, causal, seed=n)
+
+
+@pytest.mark.parametrize("n", [300, 3])
+@pytest.mark.parametrize("D", [144, 192, 208, 256])
+def test_large_heads_with_many_groups_and_few(D, n):
+    """Few rows: a group of columns has one workgroup, or two that share the values."""
+    run([n], 40, 16, 2, D, 1)
 
 
 @pytest.mark.parametrize("H,kv", [(1, 1), (3, 3), (8, 1), (28, 4), (7, 1), (40, 8), (36, 2)])

@@ -415,10 +415,13 @@ void launch_shape(const PrefillArgs& a, hipStream_t st) {
                        blocks);
 }
 
+enum class Blocks { few, large, small };
 template <int DP>
-void launch_rows(const PrefillArgs& a, bool few, hipStream_t st) {
-    if (few)
+void launch_rows(const PrefillArgs& a, Blocks blocks, hipStream_t st) {
+    if (blocks == Blocks::few)
         launch_shape<Shape<DP, 2, 2, DP <= 64 ? 64 : 32>>(a, st);
+    else if (blocks == Blocks::small)
+        launch_shape<Shape<DP, 2, 1, 32>>(a, st);
     else
         launch_shape<Shape<DP, 4, 1, DP <= 128 ? 64 : 32>>(a, st);
 }
@@ -437,17 +440,26 @@ hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipS
     // 289).
     const int64_t groups = attn_rows_groups(a), blocks = (int64_t(a.M) / kPrefillRows + a.seqs) * a.q_heads;
     if (forced < 0 ? 8 * groups <= 9 * int64_t(dev.cus) : forced == 0) return launch_attn_rows(a, dev, stream);
-    const bool few = forced < 0 ? 2 * blocks < 3 * int64_t(dev.cus) : forced == 1;
+    // Blocks of 64 rows and two waves, four of which share a CU: where the sequences have few keys, so that a
+    // block's first loads and its output are most of its time (small / 128, 28 heads on 4 of 128: 64 sequences of 16
+    // rows 12.7 / 22.0, 64 of 64 24.7 / 29.3, 16 of 256 26.0 / 28.2, 12 of 384 33.6 / 35.5, 8 of 512 36.5 / 36.2, 16 of
+    // 64 on 1064 keys 47.0 / 42.0; 16 of 384, 8 heads on 1 of 256 34.1 / 39.8, 16 heads of 64 17.3 / 22.6, 32 on 8 of
+    // 80 37.9 / 37.1).
+    const bool few_blocks = 2 * blocks < 3 * int64_t(dev.cus), short_keys = a.M_k <= 384 * int64_t(a.seqs);
+    const Blocks shape = forced > 0     ? Blocks(forced - 1)
+                         : few_blocks   ? Blocks::few
+                         : short_keys   ? Blocks::small
+                                        : Blocks::large;
     if (a.head_dim <= 64)
-        launch_rows<64>(a, few, stream);
+        launch_rows<64>(a, shape, stream);
     else if (a.head_dim <= 96)
-        launch_rows<96>(a, few, stream);
+        launch_rows<96>(a, shape, stream);
     else if (a.head_dim <= 128)
-        launch_rows<128>(a, few, stream);
+        launch_rows<128>(a, shape, stream);
     else if (a.head_dim <= 192)
-        launch_rows<192>(a, few, stream);
+        launch_rows<192>(a, shape, stream);
     else
-        launch_rows<256>(a, few, stream);
+        launch_rows<256>(a, shape, stream);
     return hipGetLastError();
 }
 
