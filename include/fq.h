@@ -120,9 +120,10 @@ fq_status fq_device_init(void);
  *   decode1=<off|auto>    (one-token fq_linear as two launches, not the fused kernel)
  *   fp8_tile=<256x256|256x128|128x192|128x160|128x128|128x96|128x64|64x128|64x64|auto>
  *                         (every FP8 product on the GEMM with this tile)
- *   attn_prefill=<rows|64|128|small|auto>
+ *   attn_prefill=<rows|64|128|small|wide|auto>
  *                         (prompts' attention on the kernel of few rows, on blocks of 64 or
- *                         128 rows, or on those for short sequences)
+ *                         128 rows, on those for short sequences, or on those of 64 with
+ *                         more waves for long keys)
  * The environment variable FQ_TEST_HOOK, read once per process at the hooks'
  * first use, takes the same spec.  FQ_ERR_ARG on an unknown key or value (state kept).
  * Process-wide; a call while another thread launches races with it. */

@@ -251,7 +251,7 @@ def test_paged_reads_stay_inside_the_cache_and_cover_every_token_once(tmp_path):
 def test_hook_takes_the_prompt_kernels_and_nothing_else():
     L = fq.lib()
     try:
-        for good in ("attn_prefill=rows", "attn_prefill=64", "attn_prefill=128", "attn_prefill=small", "attn_prefill=auto", ""):
+        for good in ("attn_prefill=rows", "attn_prefill=64", "attn_prefill=128", "attn_prefill=small", "attn_prefill=wide", "attn_prefill=auto", ""):
             assert L.fq_test_hook(good.encode()) == 0, good
         for bad in ("attn_prefill=32", "attn_prefill=", "attn_prefil=64"):
             assert L.fq_test_hook(bad.encode()) == 1, bad

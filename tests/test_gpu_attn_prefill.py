@@ -11,7 +11,7 @@ from fqtest import bf16_to_f64, dev, host
 pytestmark = pytest.mark.gpu
 
 
-@pytest.fixture(params=["auto", "rows", "64", "128", "small"], autouse=True)
+@pytest.fixture(params=["auto", "rows", "64", "128", "small", "wide"], autouse=True)
 def kernel(request, hook):
     """Every test on each of the kernels, and on the one that its sizes get."""
     hook(f"attn_prefill={request.param}")

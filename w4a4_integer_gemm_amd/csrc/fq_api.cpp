@@ -73,9 +73,9 @@ bool apply_hooks(Hooks& h, const char* spec, std::string* why) {
             }
             d1off = val == "off";
         } else if (key == "attn_prefill") {
-            prefill = val == "auto" ? -1 : val == "rows" ? 0 : val == "64" ? 1 : val == "128" ? 2 : val == "small" ? 3 : -2;
+            prefill = val == "auto" ? -1 : val == "rows" ? 0 : val == "64" ? 1 : val == "128" ? 2 : val == "small" ? 3 : val == "wide" ? 4 : -2;
             if (prefill == -2) {
-                *why = "attn_prefill must be rows, 64, 128, small or auto, not '" + val + "'";
+                *why = "attn_prefill must be rows, 64, 128, small, wide or auto, not '" + val + "'";
                 return false;
             }
         } else {

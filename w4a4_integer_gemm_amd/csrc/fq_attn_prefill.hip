@@ -415,11 +415,13 @@ void launch_shape(const PrefillArgs& a, hipStream_t st) {
                        blocks);
 }
 
-enum class Blocks { few, large, small };
+enum class Blocks { few, large, small, wide };
 template <int DP>
 void launch_rows(const PrefillArgs& a, Blocks blocks, hipStream_t st) {
     if (blocks == Blocks::few)
         launch_shape<Shape<DP, 2, 2, DP <= 64 ? 64 : 32>>(a, st);
+    else if (blocks == Blocks::wide)
+        launch_shape<Shape<DP, 2, DP <= 128 ? 4 : 2, DP <= 64 ? 64 : 32>>(a, st);  // (larger ones do not fit LDS)
     else if (blocks == Blocks::small)
         launch_shape<Shape<DP, 2, 1, 32>>(a, st);
     else
@@ -438,18 +440,29 @@ hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipS
     // 128, 1024 rows 20.2 / 23.2, 2048 rows 46.3 / 46.2, 4096 rows 149 / 129; 40 on 8 of 128, 1024 rows 24.2 / 25.0;
     // 16 heads of 64, 2048 rows 21.7 / 29.5, 8192 rows 177 / 175; 8 on 1 of 256, 4096 rows 92 / 128, 8192 rows 324 /
     // 289).
+    // Long keys move both bounds, since a block then passes over them in as many more steps: few rows up to seven
+    // workgroups to four CUs (one head of 128, 6466 rows 37 / 77; 4 on 2 of 64, 2000 rows 16.2 / 17.4), and four
+    // groups of waves instead of two where a CU has one block of 64 rows at most, or two of the longest (four / two
+    // groups: 7 heads on 1 of 80, 1500 rows 17.1 / 19.3; 2 heads of 128, 8000 rows 71.7 / 94.5; 7 on 1 of 96, 3500 rows
+    // 34.1 / 44.0; 8 on 1 of 128, 4000 rows 50.7 / 54.9, 10000 rows 257 / 241; but 28 on 4 of 128, 512 rows 14.0 /
+    // 12.9, 1024 rows 27.7 / 21.7).
     const int64_t groups = attn_rows_groups(a), blocks = (int64_t(a.M) / kPrefillRows + a.seqs) * a.q_heads;
-    if (forced < 0 ? 8 * groups <= 9 * int64_t(dev.cus) : forced == 0) return launch_attn_rows(a, dev, stream);
+    const int64_t blocks_64 = (int64_t(a.M) / 64 + a.seqs) * a.q_heads, cus = dev.cus;
+    const bool long_keys = a.M_k >= 1024 && a.M_k >= 512 * int64_t(a.seqs), longest = a.M_k >= 2048 * int64_t(a.seqs);
+    if (forced < 0 ? 8 * groups <= 9 * cus || (long_keys && 4 * groups <= 7 * cus) : forced == 0)
+        return launch_attn_rows(a, dev, stream);
     // Blocks of 64 rows and two waves, four of which share a CU: where the sequences have few keys, so that a
     // block's first loads and its output are most of its time (small / 128, 28 heads on 4 of 128: 64 sequences of 16
     // rows 12.7 / 22.0, 64 of 64 24.7 / 29.3, 16 of 256 26.0 / 28.2, 12 of 384 33.6 / 35.5, 8 of 512 36.5 / 36.2, 16 of
     // 64 on 1064 keys 47.0 / 42.0; 16 of 384, 8 heads on 1 of 256 34.1 / 39.8, 16 heads of 64 17.3 / 22.6, 32 on 8 of
     // 80 37.9 / 37.1).
-    const bool few_blocks = 2 * blocks < 3 * int64_t(dev.cus), short_keys = a.M_k <= 384 * int64_t(a.seqs);
-    const Blocks shape = forced > 0     ? Blocks(forced - 1)
-                         : few_blocks   ? Blocks::few
-                         : short_keys   ? Blocks::small
-                                        : Blocks::large;
+    const bool short_keys = a.M_k <= 384 * int64_t(a.seqs);
+    const bool wide = long_keys && blocks_64 <= (longest ? 2 : 1) * cus;
+    const Blocks shape = forced > 0               ? Blocks(forced - 1)
+                         : wide                   ? Blocks::wide
+                         : 2 * blocks < 3 * cus   ? Blocks::few
+                         : short_keys             ? Blocks::small
+                                                  : Blocks::large;
     if (a.head_dim <= 64)
         launch_rows<64>(a, shape, stream);
     else if (a.head_dim <= 96)

@@ -61,7 +61,7 @@ struct Hooks {
     std::atomic<int> gemm_mfma{16};  // 16: v_mfma_i32_16x16x64_i8 where it applies; 32: 32x32x32 only
     std::atomic<int> gemv_split{0};  // 1: decode-sized M always takes the split-K GEMV
     std::atomic<int> fp8_tile{-1};   // -1: the rule of fq_fp8_gemm.hip picks; else one of its tile ids
-    std::atomic<int> attn_prefill{-1};  // -1: by size; 0: few rows; 1: blocks of 64 rows, 2: of 128, 3: of 64 rows of short sequences
+    std::atomic<int> attn_prefill{-1};  // -1: by size; 0: few rows; 1: blocks of 64 rows, 2: of 128, 3: of 64 rows of short sequences, 4: of 64 with more waves
     std::atomic<int> decode1_off{0}; // 1: one-token fq_linear as two launches, never the fused kernel
 };
 Hooks& hooks();
