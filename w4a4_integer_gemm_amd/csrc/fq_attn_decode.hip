@@ -12,7 +12,7 @@
 // (The products, and how a tile's operands are laid out, are in fq_attn_columns.h.)
 //
 // One sequence of 131071 tokens, 8 key heads of 128, bf16: 93 us and 5 to join its parts, 537 MB at 5.7 TB/s.  64
-// sequences of 0 to 8191 tokens, 4 key heads of 128, e4m3: 18.6 us and 5 for 93 MB, 4.9 TB/s.  One of 1024
+// sequences of 0 to 8191 tokens, 4 key heads of 128, e4m3: 18.6 to 19.1 us and 5 for 88 MB, 4.7 TB/s.  One of 1024
 // tokens: 4.9 us and 3.8, latencies in a chain (lengths, page, keys, values, the meeting of the waves, and the
 // parts again).
 #include <hip/hip_runtime.h>
