@@ -248,6 +248,59 @@ def test_paged_reads_stay_inside_the_cache_and_cover_every_token_once(tmp_path):
     assert units > 10000 and wrong == 0
 
 
+LONG = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "fq_paged.h"
+using namespace fq;
+
+int main() {
+    const uint64_t wide = uint64_t(1) << 32;
+    long wrong = 0;
+    // parts are as long as they have to be, and no longer than a whole step more, on both sides of 2^32 units
+    for (int32_t target : {1, 2, 3, 7, 37, 128, 512, 1023, 1024})
+        for (uint64_t base : {uint64_t(target), wide / 2, wide - uint64_t(target), wide, 2 * wide, uint64_t(1) << 40})
+            for (int64_t d = -1100; d <= 1100; ++d) {
+                if (int64_t(base) + d < 1) continue;
+                const uint64_t units = base + d;
+                const unsigned __int128 tokens = (unsigned __int128)units * 64;
+                unsigned __int128 least = (tokens + target - 1) / target, steps = (least + kDecodeStep - 1) / kDecodeStep;
+                if (steps * kDecodeStep > (unsigned __int128)kDecodeMaxLen) steps = kDecodeMaxLen / kDecodeStep;
+                const int64_t per = decode_part_len(units, target);
+                // (units are rounded up once: at most one step more)
+                if (per < int64_t(steps) * kDecodeStep || per > int64_t(steps + 1) * kDecodeStep || per > kDecodeMaxLen) ++wrong;
+            }
+    if (decode_part_len(0, 1024) != kDecodeStep) ++wrong;
+    // batches of the longest sequences: no more parts than the launch and its workspace have
+    for (int seqs : {1, 2, 255, 256, 257, 300, 4096})
+        for (int kv : {1, 2, 3, 8, 32767})
+            for (int tiles : {1, 2, 5})
+                for (int less : {0, 1, 63, 64, 65, 64 * 1023, 64 * 1024, 1 << 29}) {
+                    const int q = kv * (16 * (tiles - 1) + 1), target = decode_target(kv, decode_head_tiles(q, kv));
+                    const int last = kDecodeMaxLen - less;
+                    const uint64_t units = uint64_t(seqs - 1) * decode_units(kDecodeMaxLen) + decode_units(last);
+                    const int per = decode_part_len(units, target);
+                    const int64_t parts = int64_t(seqs - 1) * decode_count(kDecodeMaxLen, per) + decode_count(last, per);
+                    if (parts > decode_parts(seqs, q, kv, kDecodeMaxLen)) ++wrong;
+                }
+    printf("%ld\n", wrong);
+    return 0;
+}
+"""
+
+
+def test_parts_of_the_longest_batches(tmp_path):
+    """Sums of lengths around 2^32 units of 64 tokens: a part's length does not wrap, and no batch has more parts than
+    its launch."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no g++")
+    src, exe = tmp_path / "long.cpp", tmp_path / "long"
+    src.write_text(LONG)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", f"-I{CSRC}", str(src), "-o", str(exe)], check=True)
+    assert int(subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout) == 0
+
+
 def test_hook_takes_the_prompt_kernels_and_nothing_else():
     L = fq.lib()
     try:

@@ -50,7 +50,8 @@ FQ_PAGED_FN uint32_t decode_units(int32_t len) { return (uint32_t(len) + 63) / 6
 // Tokens of a part, from the batch's sum of those: sum / target of them are at most target parts.
 FQ_PAGED_FN int32_t decode_part_len(uint64_t units, int32_t target) {
     const uint32_t t = uint32_t(target);
-    const uint64_t per = units >> 32 ? (units + t - 1) / t : uint64_t((uint32_t(units) + t - 1) / t);
+    const uint64_t up = units + t - 1;  // (divided in 32 bits where it fits them)
+    const uint64_t per = up >> 32 ? up / t : uint64_t(uint32_t(up) / t);
     const uint64_t steps = (per * 64 + kDecodeStep - 1) / kDecodeStep;
     return steps > uint64_t(kDecodeMaxLen / kDecodeStep) ? kDecodeMaxLen : steps ? int32_t(steps) * kDecodeStep : kDecodeStep;
 }
