@@ -310,3 +310,14 @@ def test_hook_takes_the_prompt_kernels_and_nothing_else():
             assert L.fq_test_hook(bad.encode()) == 1, bad
     finally:
         L.fq_test_hook(b"")
+
+
+@pytest.mark.parametrize("kernel,fits", [("rows", False), ("64", True), ("128", True), ("small", True), ("wide", False), ("auto", True)])
+def test_a_forced_prompt_kernel_of_too_many_threads_is_refused(kernel, fits, hook):
+    """The kernels have different rows and threads to a workgroup: each forced one's launch is checked, not the rule's."""
+    import torch
+    if fits and torch.cuda.is_available():
+        pytest.skip("the pointers are none of this device's")
+    hook(f"attn_prefill={kernel}")
+    code = prefill(M=10 ** 8)
+    assert code == (5 if fits else SHAPE) and (fits or "too many for one launch" in fq.last_error()), fq.last_error()

@@ -184,7 +184,13 @@ fq_status fq_attn_prefill(const void* q_bf16, int64_t q_token, int64_t q_head, c
     FQ_TRY(check_attn_head_dim(fn, head_dim));
     if (!std::isfinite(scale)) return fail(FQ_ERR_ARG, fmt("%s: scale=%g must be finite", fn, double(scale)));
     if (causal != 0 && causal != 1) return fail(FQ_ERR_ARG, fmt("%s: causal=%d must be 0 or 1", fn, causal));
-    if ((int64_t(M) / fq::kPrefillRows + seqs) * q_heads >= kMaxThreads / 512)
+    const fq::PrefillArgs a{static_cast<const uint16_t*>(q_bf16), q_token, q_head, static_cast<const uint16_t*>(k_bf16),
+                            k_token, k_head, static_cast<const uint16_t*>(v_bf16), v_token, v_head, M, M_k, cu_q,
+                            cu_k ? cu_k : cu_q, seqs, q_heads, kv_heads, head_dim, scale, causal,
+                            static_cast<uint16_t*>(o_bf16), o_token, o_head};
+    const int forced = fq::hooks().attn_prefill.load(std::memory_order_relaxed);
+    if ((int64_t(M) / fq::kPrefillRows + seqs) * q_heads >= kMaxThreads / 512 ||
+        (forced >= 0 && fq::attn_prefill_threads(a, forced) >= kMaxThreads))
         return fail(FQ_ERR_SHAPE, fmt("%s: M=%d rows of %d sequences x q_heads=%d are too many for one launch", fn, M, seqs,
                                       q_heads));
     FQ_TRY(check_head_rows(fn, "q_bf16", q_bf16, "q_token", q_token, "q_head", q_head, q_heads, M, head_dim, false));
@@ -198,10 +204,6 @@ fq_status fq_attn_prefill(const void* q_bf16, int64_t q_token, int64_t q_head, c
     if (!aligned(cu_k, 4)) return fail(FQ_ERR_ALIGN, fmt("%s: cu_k is not 4-byte aligned", fn));
     const fq::DeviceInfo* dev = nullptr;
     FQ_TRY(prepare(fn, &dev));
-    const fq::PrefillArgs a{static_cast<const uint16_t*>(q_bf16), q_token, q_head, static_cast<const uint16_t*>(k_bf16),
-                            k_token, k_head, static_cast<const uint16_t*>(v_bf16), v_token, v_head, M, M_k, cu_q,
-                            cu_k ? cu_k : cu_q, seqs, q_heads, kv_heads, head_dim, scale, causal,
-                            static_cast<uint16_t*>(o_bf16), o_token, o_head};
     return device_status(fn, fq::launch_attn_prefill(a, *dev, static_cast<hipStream_t>(stream)));
 }
 

@@ -408,24 +408,26 @@ __global__ __launch_bounds__(SH::THREADS) void attn_prefill_kernel(PrefillArgs a
     }
 }
 
+// Blocks of query rows that a launch has for each head.
 template <class SH>
-void launch_shape(const PrefillArgs& a, hipStream_t st) {
-    const int blocks = a.M / SH::BQ + a.seqs;
-    hipLaunchKernelGGL((attn_prefill_kernel<SH>), dim3(uint32_t(blocks) * uint32_t(a.q_heads)), dim3(SH::THREADS), 0, st, a,
-                       blocks);
-}
+int shape_blocks(const PrefillArgs& a) { return a.M / SH::BQ + a.seqs; }
 
 enum class Blocks { few, large, small, wide };
-template <int DP>
-void launch_rows(const PrefillArgs& a, Blocks blocks, hipStream_t st) {
-    if (blocks == Blocks::few)
-        launch_shape<Shape<DP, 2, 2, DP <= 64 ? 64 : 32>>(a, st);
-    else if (blocks == Blocks::wide)
-        launch_shape<Shape<DP, 2, DP <= 128 ? 4 : 2, DP <= 64 ? 64 : 32>>(a, st);  // (larger ones do not fit LDS)
-    else if (blocks == Blocks::small)
-        launch_shape<Shape<DP, 2, 1, 32>>(a, st);
-    else
-        launch_shape<Shape<DP, 4, 1, DP <= 128 ? 64 : 32>>(a, st);
+// f(the shape) of a call's heads and blocks.
+template <int DP, class F>
+auto with_blocks(Blocks blocks, F f) {
+    if (blocks == Blocks::few) return f(Shape<DP, 2, 2, DP <= 64 ? 64 : 32>{});
+    if (blocks == Blocks::wide) return f(Shape<DP, 2, DP <= 128 ? 4 : 2, DP <= 64 ? 64 : 32>{});  // (larger ones do not fit LDS)
+    if (blocks == Blocks::small) return f(Shape<DP, 2, 1, 32>{});
+    return f(Shape<DP, 4, 1, DP <= 128 ? 64 : 32>{});
+}
+template <class F>
+auto with_shape(int head_dim, Blocks blocks, F f) {
+    if (head_dim <= 64) return with_blocks<64>(blocks, f);
+    if (head_dim <= 96) return with_blocks<96>(blocks, f);
+    if (head_dim <= 128) return with_blocks<128>(blocks, f);
+    if (head_dim <= 192) return with_blocks<192>(blocks, f);
+    return with_blocks<256>(blocks, f);
 }
 
 }  // namespace
@@ -463,17 +465,21 @@ hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipS
                          : 2 * blocks < 3 * cus   ? Blocks::few
                          : short_keys             ? Blocks::small
                                                   : Blocks::large;
-    if (a.head_dim <= 64)
-        launch_rows<64>(a, shape, stream);
-    else if (a.head_dim <= 96)
-        launch_rows<96>(a, shape, stream);
-    else if (a.head_dim <= 128)
-        launch_rows<128>(a, shape, stream);
-    else if (a.head_dim <= 192)
-        launch_rows<192>(a, shape, stream);
-    else
-        launch_rows<256>(a, shape, stream);
+    with_shape(a.head_dim, shape, [&](auto of) {
+        using SH = decltype(of);
+        const int blocks = shape_blocks<SH>(a);
+        hipLaunchKernelGGL((attn_prefill_kernel<SH>), dim3(uint32_t(blocks) * uint32_t(a.q_heads)), dim3(SH::THREADS), 0, stream,
+                           a, blocks);
+    });
     return hipGetLastError();
+}
+
+int64_t attn_prefill_threads(const PrefillArgs& a, int kernel) {
+    if (kernel == 0) return attn_rows_threads(a);
+    return with_shape(a.head_dim, Blocks(kernel - 1), [&](auto of) {
+        using SH = decltype(of);
+        return int64_t(shape_blocks<SH>(a)) * a.q_heads * SH::THREADS;
+    });
 }
 
 }  // namespace fq

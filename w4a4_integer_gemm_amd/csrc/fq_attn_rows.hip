@@ -20,6 +20,7 @@ namespace fq {
 namespace {
 
 constexpr int kColumns = kDecodeHeads;
+constexpr int kWaves = 8;  // (a wave of the larger ones takes more than half of a SIMD's registers)
 
 template <int DP, int WAVES, int PARTS>
 __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, int64_t blocks) {
@@ -112,14 +113,15 @@ __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, in
 int64_t attn_rows_groups(const PrefillArgs& a) {
     return (int64_t(a.M) * (a.q_heads / a.kv_heads) / kColumns + a.seqs) * a.kv_heads;
 }
+// (Two workgroups to a group are launched for few of them only.)
+int64_t attn_rows_threads(const PrefillArgs& a) { return attn_rows_groups(a) * 64 * kWaves; }
 
 namespace {
 
 template <int DP, int PARTS>
 void launch_parts(const PrefillArgs& a, hipStream_t st) {
-    constexpr int WAVES = 8;  // (a wave of the larger ones takes more than half of a SIMD's registers)
     const int64_t groups = attn_rows_groups(a);
-    hipLaunchKernelGGL((attn_rows_kernel<DP, WAVES, PARTS>), dim3(uint32_t(groups) * PARTS), dim3(64 * WAVES), 0, st, a,
+    hipLaunchKernelGGL((attn_rows_kernel<DP, kWaves, PARTS>), dim3(uint32_t(groups) * PARTS), dim3(64 * kWaves), 0, st, a,
                        groups / a.kv_heads);
 }
 

@@ -260,11 +260,17 @@ struct PrefillArgs {
     uint16_t* o;
     int64_t o_token, o_head;
 };
-// Query rows of the smallest block, which bounds a launch's workgroups.
+// Query rows of the largest block.  A call has fewer than 2^23 blocks of them (the entry point's check), hence
+// fewer than 2^24 of 64 rows: of the kernels that the rule picks whatever the size, the one of 128 rows has 256
+// threads to a block and the one of 64 for short sequences 128, fewer than 2^31 in all; the others are picked
+// where there are a few workgroups to a CU at most.  A forced kernel's launch is checked by itself.
 constexpr int kPrefillRows = 128;
 hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t stream);
-// The same for few rows (fq_attn_rows.hip), and its workgroups.
+// Threads of a launch on one of its kernels (numbered as in Hooks::attn_prefill).
+int64_t attn_prefill_threads(const PrefillArgs& a, int kernel);
+// The same for few rows (fq_attn_rows.hip), its workgroups and its threads.
 int64_t attn_rows_groups(const PrefillArgs& a);
+int64_t attn_rows_threads(const PrefillArgs& a);
 hipError_t launch_attn_rows(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t stream);
 
 // Attention of one token per sequence over the paged cache (fq_attn_decode.hip).
