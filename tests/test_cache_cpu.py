@@ -96,3 +96,55 @@ def test_a_workspace_that_grew_keeps_the_one_before(cache):
     big = cache.workspace(64, H, 400)
     assert big.numel() > small.numel() and any(w is small for w in cache._ws_before)
     assert cache.workspace(2, H, 4) is big
+
+
+def flat(n=4 * M * KV * D):
+    return torch.zeros(n, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("t,match", [
+    (heads(1).expand(M, KV, D), "strides 0 from token"), (heads(M, 1).expand(M, KV, D), "and 0 from head"),
+    (flat()[1:].as_strided((M, KV, D), (KV * D, D, 1), 1), "16 bytes"), (heads(M, KV, D + 16)[:, :, 4:D + 4], "16 bytes"),
+    (heads(M, KV, D + 4)[:, :, :D], "multiples of 8"), (flat().as_strided((M, KV, D), (KV * D + 2, D, 1)), "multiples of 8"),
+    (flat().as_strided((M, KV, D), (D // 2, M * D, 1)), "at least 64"), (flat().as_strided((M, KV, D), (KV * D, D - 8, 1)), "at least 64"),
+])
+def test_strides_and_starts_that_the_library_refuses_are_a_valueerror(cache, t, match):
+    good = heads()
+    q, table, lens = heads(M, KV), ints(M, 4), ints(M)
+    for call in (lambda: cache.write(t, good, ints(M)), lambda: cache.write(good, t, ints(M)), lambda: cache.read(ints(M), k=t),
+                 lambda: cache.read(ints(M), v=t), lambda: cache.attend(t, table, lens), lambda: cache.attend(q, table, lens, o=t)):
+        with pytest.raises(ValueError, match=match):
+            call()
+
+
+@pytest.mark.parametrize("token,head", [(D, D), (2 * D, D + D // 2), (D + 8, 2 * D)])
+def test_heads_that_overlap_are_inputs_only(cache, token, head):
+    t = flat().as_strided((M, KV, D), (token, head, 1))
+    apart = token >= head + D
+    for call in (lambda: cache.read(ints(M), k=t), lambda: cache.read(ints(M), v=t),
+                 lambda: cache.attend(heads(M, KV), ints(M, 4), ints(M), o=t)):
+        with pytest.raises(ValueError, match="GPU tensors" if apart else "overlap"):
+            call()
+    with pytest.raises(ValueError, match="GPU tensors"):
+        cache.write(t, heads(), ints(M))
+
+
+def test_the_strides_taken_are_the_librarys():
+    """Whatever passes the checks here passes the library's own, and the other way round."""
+    c = fq.KVCache(P, S, 2, 16, 16, device="cpu")
+    lib, dev = fq.lib(), 0x10000
+    for token in (0, 8, 12, 16, 24, 32, 40, 48):
+        for head in (0, 8, 16, 20, 24, 32, 48, 64):
+            t = flat(1000).as_strided((3, 2, 16), (token, head, 1))
+            for out in (False, True):
+                try:
+                    c._heads(t, "t", 3, 2, out)
+                    ours = True
+                except ValueError:
+                    ours = False
+                if out:
+                    code = lib.fq_kv_read(dev, dev, None, None, 16, P, S, 0x10002, 3, 2, 16, dev, token, head, 2 * dev, 32, 16, None)
+                else:
+                    code = lib.fq_kv_write(dev, token, head, dev, 32, 16, 0x10002, 3, 2, 16, 16, P, S, dev, dev, None, None, None)
+                # (the slots, looked at behind the strides, are misaligned: no call goes on to the device)
+                assert ours == ("slots" in fq.last_error()), (token, head, out, code, fq.last_error())

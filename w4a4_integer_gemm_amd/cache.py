@@ -15,9 +15,12 @@ class KVCache:
     page * page_size + place in the page), attend() a page table (int32 [seqs][max_pages]) and lengths (int32
     [seqs]), all on the device, so that one captured graph serves any batch.
 
-    Heads are tensors [M][heads][head_dim] of bf16 or its bits (int16, uint16) with any strides and
-    contiguous values: a row-major projection's output as .view(M, heads, head_dim), the head layout's as
-    .transpose(0, 1).  Everything is on the cache's device, which is the current one; ValueError otherwise.
+    Heads are tensors [M][heads][head_dim] of bf16 or its bits (int16, uint16) with contiguous values that begin
+    on 16 bytes, and strides from token to token and from head to head that are multiples of 8 and at least
+    head_dim: a row-major projection's output as .view(M, heads, head_dim), the head layout's as
+    .transpose(0, 1).  An output's heads do not overlap.  Everything is on the cache's device, which is the current
+    one; ValueError otherwise.  Sizes and workspaces that the library refuses are an FqError.  That an output
+    overlaps no input and no other output is the caller's to see to.
 
     attend() uses the cache's own workspace, which belongs to one call at a time: calls on two
     streams at once pass workspaces of their own.  What a call with stream= allocates belongs to that stream.  A
@@ -46,20 +49,28 @@ class KVCache:
         if self.device.index is not None and torch.cuda.current_device() != self.device.index:
             raise ValueError(f"the cache is on {self.device}, the current device is {torch.cuda.current_device()}")
 
-    def _heads(self, t, name: str, rows: int, heads: Optional[int]):
-        """(heads, token stride, head stride) of [rows][heads][head_dim]."""
-        shape, stride = t.shape, t.stride()
+    def _heads(self, t, name: str, rows: int, heads: Optional[int], out: bool = False):
+        """(heads, token stride, head stride) of [rows][heads][head_dim]; out: they must not overlap."""
+        shape, stride, D = t.shape, t.stride(), self.head_dim
         if t.dtype not in self._bf16:
             raise ValueError(f"{name} has dtype {t.dtype}, not bfloat16 (or its bits as int16 or uint16)")
-        if len(shape) != 3 or shape[0] != rows or shape[2] != self.head_dim or (heads is not None and shape[1] != heads):
-            raise ValueError(f"{name} is {tuple(shape)}, not ({rows}, {'heads' if heads is None else heads}, {self.head_dim})")
+        if len(shape) != 3 or shape[0] != rows or shape[2] != D or (heads is not None and shape[1] != heads):
+            raise ValueError(f"{name} is {tuple(shape)}, not ({rows}, {'heads' if heads is None else heads}, {D})")
         if stride[2] != 1:
             raise ValueError(f"{name} has stride {stride[2]} along a head's values, not 1")
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
         # (the stride of a dimension of one is never used, and torch allows it any value)
         n = shape[1]
-        return n, stride[0] if rows > 1 else n * self.head_dim, stride[1] if n > 1 else self.head_dim
+        token, head = stride[0] if rows > 1 else n * D, stride[1] if n > 1 else D
+        if token < D or head < D or token % 8 or head % 8:
+            raise ValueError(f"{name} has strides {token} from token to token and {head} from head to head, not multiples "
+                             f"of 8 that are at least {D}")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} does not begin on 16 bytes")
+        if out and token < (n - 1) * head + D and head < (rows - 1) * token + D:
+            raise ValueError(f"{name} has strides {token} from token to token and {head} from head to head: heads overlap")
+        return n, token, head
 
     def _ints(self, t, name: str, dims: int):
         import torch
@@ -104,8 +115,8 @@ class KVCache:
             with _allocating_on(stream):
                 k = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if k is None else k
                 v = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if v is None else v
-        _, kt, kh = self._heads(k, "k", M, self.kv_heads)
-        _, vt, vh = self._heads(v, "v", M, self.kv_heads)
+        _, kt, kh = self._heads(k, "k", M, self.kv_heads, out=True)
+        _, vt, vh = self._heads(v, "v", M, self.kv_heads, out=True)
         self._check_device()
         B.fq_kv_read(self.k, self.v, self.k_scale, self.v_scale, self.bits, self.pages, self.page_size, slots, M,
                      self.kv_heads, self.head_dim, k, kt, kh, v, vt, vh, stream)
@@ -124,7 +135,7 @@ class KVCache:
             import torch
             with _allocating_on(stream):
                 o = torch.empty((seqs, H, self.head_dim), dtype=q.dtype, device=self.device)
-        _, ot, oh = self._heads(o, "o", seqs, H)
+        _, ot, oh = self._heads(o, "o", seqs, H, out=True)
         self._check_device()
         if workspace is None:
             workspace = self.workspace(seqs, H, max_pages, stream)
