@@ -473,9 +473,9 @@ fq_status fq_kv_read(const void* k_cache, const void* v_cache, const float* k_sc
  *   cu_q, cu_k  device int32 [seqs + 1], not decreasing, within [0, M] and [0, M_k] (what
  *               lies outside is cut off)
  * head_dim is a multiple of 16, at most 256; kv_heads divides q_heads; k_token and
- * v_token are at most 2^24; scale is finite.  Scores, maximum and sums are float32, the weights p of a product are
- * rounded to bf16, as its operand; one rounding to bf16 at the end.  k and v must be
- * finite within a sequence; rows outside of it may hold anything. */
+ * v_token are at most 2^24; scale is finite.  Scores, maximum and sums are float32; the weights p, operands of a bf16
+ * product, are rounded to bf16 or (few rows) to two bf16 pieces, 2^-16 of themselves; one rounding to
+ * bf16 at the end.  k and v must be finite within a sequence; rows outside of it may hold anything. */
 fq_status fq_attn_prefill(const void* q_bf16, int64_t q_token, int64_t q_head, const void* k_bf16, int64_t k_token,
                           int64_t k_head, const void* v_bf16, int64_t v_token, int64_t v_head, int32_t M, int32_t M_k,
                           const int32_t* cu_q, const int32_t* cu_k, int32_t seqs, int32_t q_heads, int32_t kv_heads,
@@ -489,8 +489,9 @@ fq_status fq_attn_prefill(const void* q_bf16, int64_t q_token, int64_t q_head, c
  *   lens        device int32 [seqs]; more than max_pages * page_size counts as that, fewer than 1 as none
  * A row that sees no token gets zeros.  What the cache holds behind a sequence's
  * last token does not matter.  max_pages * page_size <= 2^30; other rules as in
- * fq_attn_prefill and fq_kv_write.  A code's value times its scale is never rounded:
- * the key's scale multiplies the score, the value's the weight p.
+ * fq_attn_prefill and fq_kv_write.  A code's value times its scale is never rounded to bf16:
+ * the key's scale multiplies the score, the value's the weight p, in float32.  Weights
+ * (times that scale) enter their product as two bf16 pieces, off by at most 2^-16 of themselves.
  * workspace: at least fq_attn_decode_workspace_bytes(seqs, q_heads, kv_heads, head_dim,
  * max_pages * page_size) bytes (never fewer for more sequences or tokens), 256-byte
  * aligned; the parts of a long sequence meet there.  It belongs to one call at a time,
