@@ -177,7 +177,8 @@ __global__ __launch_bounds__(SH::THREADS) void attn_prefill_kernel(PrefillArgs a
             q[i] = as_bf(make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
         }
     }
-    const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);  // (0 times a masked score would be no number)
+    // (0 times a masked score would be no number; no score of float32 gets past 2^-21 times this one)
+    const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-149f);
 
     // addresses of the operands' reads in a stage
     constexpr int KA = CH == 8 ? 4 : 8;
