@@ -5,6 +5,7 @@ import pytest
 import attnref
 import blockref as ref
 from fqtest import bf16_to_f64
+from test_gpu_attn_decode import Batch
 from test_gpu_attn_prefill import call
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +39,9 @@ def test_prompts_of_scale_zero(scale, kernel, hook):
     got = call(q, k, v, [0, n], None, scale, 1)
     o, tol, _ = attnref.prefill(*(bf16_to_f64(t) for t in (q, k, v)), [0, n], [0, n], 0.0, 1)
     attnref.assert_attn(got, o, tol, "scale 0")
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("scale,q_scale", [(1e-33, 2.0 ** 106), (1e-38, 2.0 ** 120), (1e12, 2.0 ** -41), (0.0, 2.0 ** 110)])
+def test_tokens(scale, q_scale, bits):
+    Batch([200, 1, 33], 4, 2, 64, 16, bits, q_scale=q_scale, seed=3).check(float(np.float32(scale)))

@@ -30,11 +30,14 @@
 namespace fq {
 
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-// Two of a dword's four codes as bf16.
+// Two of a dword's four codes as bf16, times a power of two.
 template <bool HI>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, float times = 1.0f) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, times, HI));
 }
+// Codes of keys are multiplied as 2^-8 of themselves, 1.75 at most, and their scales as 2^8 of themselves (a bf16 key's
+// is below 2^120): sums that the key's scale meets only afterwards then stay within those of the query's own values.
+constexpr float kKeyCode = 0x1p-8f;
 
 // 8 keys of one d, for the d's of dword c of a lane's piece (bf16: two; codes: four), from rows of 8 keys.
 __device__ __forceinline__ void transpose_dword(const uint4 (&r)[8], int c, v8bf (&out)[2]) {
@@ -202,10 +205,12 @@ struct Columns {
             for (int j = 0; j < KL; ++j) {
                 const u32x4 k = keys[key_place(kDecodeUnit * i + col, 4 * j + g)];
                 if constexpr (FP8) {
-                    s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k[0]), codes_bf16<true>(k[0]),
-                                                         codes_bf16<false>(k[1]), codes_bf16<true>(k[1]))), query(lds, 2 * j, at), s[i]);
-                    s[i] = mfma_bf16_16(as_bf(make_uint4(codes_bf16<false>(k[2]), codes_bf16<true>(k[2]),
-                                                         codes_bf16<false>(k[3]), codes_bf16<true>(k[3]))), query(lds, 2 * j + 1, at), s[i]);
+                    auto half = [&](uint32_t a, uint32_t b) {
+                        return as_bf(make_uint4(codes_bf16<false>(a, kKeyCode), codes_bf16<true>(a, kKeyCode),
+                                                codes_bf16<false>(b, kKeyCode), codes_bf16<true>(b, kKeyCode)));
+                    };
+                    s[i] = mfma_bf16_16(half(k[0], k[1]), query(lds, 2 * j, at), s[i]);
+                    s[i] = mfma_bf16_16(half(k[2], k[3]), query(lds, 2 * j + 1, at), s[i]);
                 } else {
                     s[i] = mfma_bf16_16(__builtin_bit_cast(v8bf, k), query(lds, j, at), s[i]);
                 }
@@ -214,7 +219,8 @@ struct Columns {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float4 &kq = ks[i / 4], &vq = vs[i / 4];
-            x[i] = s[i / 4][i % 4] * (FP8 ? (i % 4 == 0 ? kq.x : i % 4 == 1 ? kq.y : i % 4 == 2 ? kq.z : kq.w) * c : c);
+            const float ki = i % 4 == 0 ? kq.x : i % 4 == 1 ? kq.y : i % 4 == 2 ? kq.z : kq.w;
+            x[i] = (FP8 ? s[i / 4][i % 4] * (ki * (1.0f / kKeyCode)) : s[i / 4][i % 4]) * c;
             w[i] = FP8 ? (i % 4 == 0 ? vq.x : i % 4 == 1 ? vq.y : i % 4 == 2 ? vq.z : vq.w) : 1.0f;
         }
     }
