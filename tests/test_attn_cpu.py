@@ -321,3 +321,69 @@ def test_a_forced_prompt_kernel_of_too_many_threads_is_refused(kernel, fits, hoo
     hook(f"attn_prefill={kernel}")
     code = prefill(M=10 ** 8)
     assert code == (5 if fits else SHAPE) and (fits or "too many for one launch" in fq.last_error()), fq.last_error()
+
+
+SEARCH = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+#include "fq_paged.h"
+using namespace fq;
+
+int main() {
+    long wrong = 0, most = 0;
+    srand(2);
+    for (int n : {1, 2, 63, 64, 65, 127, 128, 129, 1000, 4095, 4096, 4097, 5000, 100000, (1 << 18), (1 << 18) + 1, 1 << 20, (1 << 23) - 1}) {
+        std::vector<long> at(n);
+        long x = rand() % 3;
+        for (long& a : at) a = x, x += 1 + (rand() % 4 ? 0 : rand() % 50);
+        for (int k = 0; k < 300; ++k) {
+            const long b = k < 3 ? k - 1 : k == 3 ? x + 5 : k == 4 ? at[n - 1] : rand() % (x + 1);
+            long steps = 0;
+            const int got = last_not_past(n, [&](int first, int step, int probes) {
+                ++steps;
+                if (probes < 1 || probes > 64) ++wrong;
+                int c = 0;
+                for (int p = 0; p < probes; ++p) {
+                    const long i = first + long(p) * step;
+                    if (i < 0 || i >= n) { ++wrong; continue; }
+                    c += at[i] <= b;
+                }
+                return c;
+            });
+            // at[got] is not past b, the next one is
+            if (got < -1 || got >= n || (got >= 0 && at[got] > b) || (got + 1 < n && at[got + 1] <= b)) ++wrong;
+            if (n <= 64 ? steps != 1 : steps > (n <= 4096 ? 2 : n <= (1 << 18) ? 3 : 4)) ++wrong;
+            most = steps > most ? steps : most;
+        }
+        // entries in no order: inside 0 .. n - 1 all the same, and it ends
+        for (long& a : at) a = rand() % 1000 - 500;
+        for (int k = 0; k < 50; ++k) {
+            const int got = last_not_past(n, [&](int first, int step, int probes) {
+                int c = 0;
+                for (int p = 0; p < probes; ++p) {
+                    const long i = first + long(p) * step;
+                    if (i < 0 || i >= n) { ++wrong; continue; }
+                    c += at[i] <= k * 20 - 500;
+                }
+                return c;
+            });
+            if (got < -1 || got >= n) ++wrong;
+        }
+    }
+    printf("%ld %ld\n", most, wrong);
+    return 0;
+}
+"""
+
+
+def test_a_sequence_is_found_in_a_few_steps(tmp_path):
+    """However many there are: looking at all of them in every workgroup would take the square of their number."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no g++")
+    src, exe = tmp_path / "search.cpp", tmp_path / "search"
+    src.write_text(SEARCH)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", f"-I{CSRC}", str(src), "-o", str(exe)], check=True)
+    most, wrong = (int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split())
+    assert wrong == 0 and most == 4

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "fq_device.h"
+#include "fq_paged.h"
 
 namespace fq {
 
@@ -60,9 +61,9 @@ template <class First>
 __device__ __forceinline__ int find_sequence(int seqs, int64_t b, First first) {
     if (seqs == 1) return 0;
     const int lane = threadIdx.x & 63;
-    int n = 0;
-    for (int s0 = 0; s0 < seqs; s0 += 64) n += __popcll(__ballot(s0 + lane < seqs && first(s0 + lane) <= b));
-    return __builtin_amdgcn_readfirstlane(n - 1);
+    return __builtin_amdgcn_readfirstlane(last_not_past(seqs, [&](int at, int step, int probes) {
+        return __popcll(__ballot(lane < probes && first(at + lane * step) <= b));
+    }));
 }
 // Rows of sequence s, cut off at [0, M].
 struct Rows {

@@ -88,6 +88,21 @@ FQ_PAGED_FN int64_t paged_row(int32_t page, int32_t place, int32_t head, int32_t
     return (int64_t(page) * kv_heads + head) * page_size + place;
 }
 
+// The last of n sorted entries that is not past a wanted one (-1: none), 64 of them looked at in a step, so that n up to
+// 2^18 takes three steps; count(first, step, probes): how many of the entries first, first + step, ..., `probes` of
+// them and at most 64, are not past it.  Whatever the entries are, only those of 0 .. n - 1 are looked at, and the steps end.
+template <class Count>
+FQ_PAGED_FN int32_t last_not_past(int32_t n, Count count) {
+    int32_t first = 0;
+    while (n > 64) {
+        const int32_t step = (n + 63) / 64, k = count(first, step, (n + step - 1) / step);
+        if (k == 0) return -1;
+        first += (k - 1) * step;
+        n = step < n - (k - 1) * step ? step : n - (k - 1) * step;
+    }
+    return first + count(first, 1, n) - 1;
+}
+
 // Workspace of a decode call, never smaller for more sequences or tokens: the first part and the
 // parts of every sequence, then for every part and query head the maximum, the sum of weights and the output.
 struct DecodeWorkspace {
