@@ -38,6 +38,12 @@ __device__ __forceinline__ uint32_t lanes_scan(uint32_t v) {
     return v;
 }
 
+// Sequences up to which every workgroup goes through all lengths; more of them are gone through once, by a launch of
+// its own, since the workgroups grow with the sequences too.  (Graph-replayed us without / with that launch, 8 query heads of
+// 128, e4m3.  8 key heads: 192 sequences of 64 tokens 14.1 / 15.8, 256 18.9 / 19.4, 384 28.5 / 24.4, 1024 107 / 58;
+// 256 of 300 tokens 44.4 / 43.7, 384 67.6 / 59.4.  One key head: 256 of 300 17.4 / 19.1, 384 25.4 / 24.8, 768 43.9 / 34.1.)
+constexpr int kScanned = 256;
+
 // Part w of the batch: its sequence (-1: there are fewer parts), the number inside it and the
 // parts it has, the sequence's length and a part's.  Every wave finds it.
 struct Part {
@@ -45,6 +51,13 @@ struct Part {
 };
 __device__ __forceinline__ Part find_part(const DecodeArgs& a, int w, int target) {
     const int lane = threadIdx.x & 63, most = a.max_pages, size = a.cache.page_size;
+    if (a.seqs > kScanned) {
+        const int32_t* const plan = reinterpret_cast<const int32_t*>(a.plan);
+        const int seq = find_sequence(a.seqs, w, [&](int s) { return a.plan[s].x; });
+        const int first = scalar_load(plan, 2 * int64_t(seq)), count = scalar_load(plan, 2 * int64_t(seq) + 1);
+        return Part{w - first < count ? seq : -1, w - first, count, paged_len(scalar_load(a.lens, seq), most, size),
+                    scalar_load(plan, 2 * int64_t(a.seqs) + 1)};
+    }
     if (a.seqs == 1) {
         const int len = paged_len(scalar_load(a.lens, 0), most, size);
         const int per = decode_part_len(decode_units(len), target), count = decode_count(len, per);
@@ -71,6 +84,38 @@ __device__ __forceinline__ Part find_part(const DecodeArgs& a, int w, int target
     return Part{-1, 0, 0, 0, per};
 }
 
+// The plan of a batch, by one workgroup.
+constexpr int kPlanWaves = 16;
+__global__ __launch_bounds__(64 * kPlanWaves) void attn_plan_kernel(DecodeArgs a, int target) {
+    __shared__ uint64_t wave_units[kPlanWaves];
+    __shared__ uint32_t wave_parts[kPlanWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    auto length = [&](int s) { return paged_len(a.lens[s], a.max_pages, a.cache.page_size); };
+    unsigned long long units = 0;
+    for (int s = threadIdx.x; s < a.seqs; s += 64 * kPlanWaves) units += decode_units(length(s));
+    for (int d = 32; d; d >>= 1) units += __shfl_xor(units, d);
+    if (lane == 0) wave_units[wave] = units;
+    __syncthreads();
+    units = 0;
+    for (int i = 0; i < kPlanWaves; ++i) units += wave_units[i];
+    const int per = decode_part_len(units, target);
+    uint32_t before = 0;
+    for (int s0 = 0; s0 < a.seqs; s0 += 64 * kPlanWaves) {
+        const int s = s0 + threadIdx.x;
+        const uint32_t n = s < a.seqs ? decode_count(length(s), per) : 0, upto = lanes_scan(n);
+        if (lane == 63) wave_parts[wave] = upto;
+        __syncthreads();
+        uint32_t first = before + upto - n;
+        for (int i = 0; i < kPlanWaves; ++i) {
+            first += i < wave ? wave_parts[i] : 0;
+            before += wave_parts[i];
+        }
+        if (s < a.seqs) a.plan[s] = make_int2(first, n);
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) a.plan[a.seqs] = make_int2(before, per);
+}
+
 template <int DP, bool FP8>
 __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a, uint64_t magic, int target, int head_tiles) {
     using Cols = Columns<DP, FP8, true>;
@@ -92,7 +137,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a, uint6
     const Part part = find_part(a, w, target);
     if (part.seq < 0) return;
     const int seq = part.seq, len = part.len;
-    if (part.index == 0 && kvh == 0 && ht == 0 && threadIdx.x == 0) a.plan[seq] = make_int2(w, part.count);
+    if (a.seqs <= kScanned && part.index == 0 && kvh == 0 && ht == 0 && threadIdx.x == 0) a.plan[seq] = make_int2(w, part.count);
     const int begin = part.index * part.part_len, end = min(begin + part.part_len, len);
     const int32_t* const table = a.page_table + int64_t(seq) * a.max_pages;
     const uint32_t row_bytes = uint32_t(D * Cols::ES);
@@ -231,6 +276,7 @@ void launch_bits(const DecodeArgs& a, hipStream_t st) {
     const int tiles = decode_head_tiles(a.q_heads, a.cache.kv_heads), target = decode_target(a.cache.kv_heads, tiles);
     const dim3 grid(uint32_t(int64_t(a.parts) * a.cache.kv_heads * tiles));
     const uint64_t magic = paged_magic(a.cache.page_size);
+    if (a.seqs > kScanned) hipLaunchKernelGGL(attn_plan_kernel, dim3(1), dim3(64 * kPlanWaves), 0, st, a, target);
     if (a.cache.k_scale)
         hipLaunchKernelGGL((attn_decode_kernel<DP, true>), grid, dim3(64 * kDecodeWaves), 0, st, a, magic, target, tiles);
     else

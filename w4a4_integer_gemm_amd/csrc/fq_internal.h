@@ -285,7 +285,7 @@ struct DecodeArgs {
     const int32_t* lens;
     uint16_t* o;
     int64_t o_token, o_head;
-    int2* plan;    // [seqs] first part and parts of each
+    int2* plan;    // [seqs] first part and parts of each; [seqs]: parts of the batch, tokens of one
     float2* stats; // [parts][q_heads] maximum and sum of weights
     float* sums;   // [parts][q_heads][head_dim]
     int32_t parts; // (at most)

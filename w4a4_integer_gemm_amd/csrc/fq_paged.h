@@ -104,14 +104,15 @@ FQ_PAGED_FN int32_t last_not_past(int32_t n, Count count) {
 }
 
 // Workspace of a decode call, never smaller for more sequences or tokens: the first part and the
-// parts of every sequence, then for every part and query head the maximum, the sum of weights and the output.
+// parts of every sequence, and of the batch all parts and the tokens of one; then for every part and query head the
+// maximum, the sum of weights and the output.
 struct DecodeWorkspace {
     size_t stats, sums, bytes;  // offsets of the two, and the size
 };
 FQ_PAGED_FN DecodeWorkspace decode_workspace(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                              int32_t max_len) {
     const size_t rows = size_t(decode_parts(seqs, q_heads, kv_heads, max_len)) * size_t(q_heads);
-    const size_t stats = (size_t(seqs) * 8 + 255) / 256 * 256, sums = stats + (rows * 8 + 255) / 256 * 256;
+    const size_t stats = (size_t(seqs) * 8 + 8 + 255) / 256 * 256, sums = stats + (rows * 8 + 255) / 256 * 256;
     return DecodeWorkspace{stats, sums, (sums + rows * size_t(head_dim) * 4 + 255) / 256 * 256};
 }
 
