@@ -14,9 +14,10 @@
 //
 // Both products are the matrix instruction's bf16 ones with float32 sums.  Its operand holds 8 bits of a weight, so
 // that a weight goes in as two of them, its rounding to bf16 and that of what is left: off by 2^-16 of itself at most,
-// where one would be off by 2^-8, as much as the output's own rounding.  The second product reads nothing more, and the matrix
-// unit is idle for nine cycles of ten here: with it / without, decode of 64 ragged sequences 25.6 / 25.0 us, of
-// 131071 tokens 102.3 / 102.4, of 1024 8.8 / 8.6; 50 rows on 866 keys 13.6 / 13.3.
+// where one would be off by 2^-8, as much as the output's own rounding.  The second product reads nothing more, and the
+// matrix unit is idle for nine cycles of ten here: without / with it, decode of 64 ragged sequences 25.0 / 25.6 us, of
+// 131071 tokens 102.4 / 102.3, of 1024 8.6 / 8.8; 50 rows on 866 keys 13.3 / 13.6, on 8050 69.3 / 71.4 (28 heads of 128
+// 47.1 / 50.2).
 #pragma once
 
 #include <hip/hip_runtime.h>

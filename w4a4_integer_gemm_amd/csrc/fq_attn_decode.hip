@@ -6,15 +6,15 @@
 // query heads of one key head, so that they share the reading, and one part of a
 // sequence; its four waves take tiles of 32 tokens in turn, each with its own
 // running maximum, sum and output, and join at the end.  All parts of a batch have
-// one length, found from its lengths by every workgroup, so that sequences of any lengths keep
-// the chip equally busy.  Parts of a sequence meet in the workspace and are joined by a
-// second launch.
+// one length, found from its lengths by every workgroup (those of many sequences by a launch
+// before), so that sequences of any lengths keep the chip equally busy.  Parts of a sequence
+// meet in the workspace and are joined by a launch behind.
 // (The products, and how a tile's operands are laid out, are in fq_attn_columns.h.)
 //
-// One sequence of 131071 tokens, 8 key heads of 128, bf16: 93 us and 5 to join its parts, 537 MB at 5.7 TB/s.  64
-// sequences of 0 to 8191 tokens, 4 key heads of 128, e4m3: 18.6 to 19.1 us and 5 for 88 MB, 4.7 TB/s.  One of 1024
-// tokens: 4.9 us and 3.8, latencies in a chain (lengths, page, keys, values, the meeting of the waves, and the
-// parts again).
+// One sequence of 131071 tokens, 8 key heads of 128, bf16: 94 us and 5 to join its parts, 537 MB at 5.7 TB/s.  64
+// sequences of 0 to 8191 tokens, 4 key heads of 128, e4m3: 19.8 us and 5 for 88 MB, 4.5 TB/s.  1024 of 500 tokens, 2 key
+// heads, e4m3: 4.6 us for their plan and 54 for 275 MB, 5.1 TB/s.  One of 1024 tokens: 5.0 us and 3.6, latencies in a
+// chain (lengths, page, keys, values, the meeting of the waves, and the parts again).
 #include <hip/hip_runtime.h>
 
 #include "fq_attn.h"

@@ -20,11 +20,17 @@
 // A wave's loop is a software pipeline, so that the matrix unit has work while the vector unit makes
 // weights: the products of the next tile's scores are issued with this tile's scalings, powers and
 // packings between them, and those of the output with the next tile's maximum.  Operands are
-// read four products ahead.  Rounded: the weights, to bf16 (the sum takes them as rounded), and the output.
+// read four products ahead.
 //
-// 16384 rows, 28 heads on 4 of 128, causal: 1.70 ms, 1.13 PFLOP/s, where a bf16 product of 8192^3 by the library
-// runs at 1.2; the products keep the matrix unit busy for 64 % of the cycles, at the 1.65 to 1.8 GHz that the
-// power limit leaves it (the same loop of products alone: 1.74 PFLOP/s at 1.67 GHz).  4580 rows of eight
+// Rounded: the output, and before it the weights, to bf16, as the product's operand (2^-8 of each at most; the
+// sum takes them as rounded, so that they still add up to one).  Multiplying what the rounding leaves of them
+// too, as decode and the kernel of few rows do, is half as many products again where products are the bound: without / with
+// it, 28 heads on 4 of 128, 1024 rows 22.2 / 25.4 us, 4096 rows 134 / 196, 16384 rows 1757 / 2729; 16 heads of 64,
+// 8192 rows 175 / 234; 8 on 1 of 256, 16384 rows 1103 / 1464.
+//
+// 16384 rows, 28 heads on 4 of 128, causal: 1.70 to 1.77 ms, 1.09 to 1.13 PFLOP/s, where a bf16 product of 8192^3 by
+// the library runs at 1.26 and the matrix unit alone, on random operands in registers, at 1.69 to 1.75; the products keep
+// it busy for 65 % of the cycles, at the 1.65 to 1.8 GHz that the power limit leaves it.  4580 rows of eight
 // sequences: 59.7 us, 44 % busy: the last blocks, and a block's first loads and its epilogue (about 5 us).  1024 rows:
 // 19.2 us, 24 % busy: two blocks to a CU, whose 16 tiles follow one another.
 #include <hip/hip_runtime.h>
@@ -90,7 +96,8 @@ __global__ __launch_bounds__(SH::THREADS) void attn_prefill_kernel(PrefillArgs a
     __shared__ __attribute__((aligned(1024))) uint8_t lds[SH::LDS];
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wq = wave % SH::WQ, wk = wave / SH::WQ;
-    // heads in turn, the blocks that see most keys first
+    // heads in turn, from the last sequence to the first, and of a sequence the blocks that see most keys first (that
+    // a long sequence in front has its blocks behind those of short ones is not looked at)
     const int head = blockIdx.x % a.q_heads, b = blocks - 1 - int(blockIdx.x / a.q_heads);
     // (those of sequence s are cu[s] / BQ + s and on, which leaves at least as many as it has)
     auto first = [&](int s) { return max(0, min(a.cu_q[s], a.M)) / BQ + s; };
@@ -436,17 +443,17 @@ auto with_shape(int head_dim, Blocks blocks, F f) {
 hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t stream) {
     const int forced = hooks().attn_prefill.load(std::memory_order_relaxed);
     // Few rows: as long as its workgroups are about one to a CU (graph-replayed, us, rows / blocks of 64 / of 128:
-    // 28 heads on 4 of 128, 128 rows 5.9 / 7.8 / 8.0, 256 rows 10.2 / 9.2 / 10.1; 16 heads of 64, 256 rows 5.8 /
-    // 6.7 / 7.6, 384 rows 8.5 / 7.5 / 9.0; 8 heads on 1 of 256, 512 rows 12.4 / 17.9 / 23.1, 1024 rows 26.2 / 26.7 /
-    // 39.0; 16 heads on 2 of 256 with 8 sequences of 64 rows 16.0 / 12.1 at two to a CU).  Blocks of 64 rows with the
+    // 28 heads on 4 of 128, 128 rows 6.6 / 8.2 / 8.4, 256 rows 11.1 / 9.7 / 10.5; 16 heads of 64, 256 rows 6.4 /
+    // 7.1 / 7.9, 384 rows 9.3 / 7.9 / 9.4; 8 heads on 1 of 256, 512 rows 13.6 / 18.1 / 23.4, 1024 rows 28.0 / 26.6 /
+    // 38.4; 16 heads on 2 of 256 with 8 sequences of 64 rows 16.8 / 11.6 at two to a CU).  Blocks of 64 rows with the
     // keys shared by two groups of waves: where blocks of 128 would be fewer than three to two CUs (28 on 4 of
     // 128, 1024 rows 20.2 / 23.2, 2048 rows 46.3 / 46.2, 4096 rows 149 / 129; 40 on 8 of 128, 1024 rows 24.2 / 25.0;
     // 16 heads of 64, 2048 rows 21.7 / 29.5, 8192 rows 177 / 175; 8 on 1 of 256, 4096 rows 92 / 128, 8192 rows 324 /
     // 289).
     // Long keys move both bounds, since a block then passes over them in as many more steps: few rows up to seven
-    // workgroups to four CUs (one head of 128, 6466 rows 37 / 77; 4 on 2 of 64, 2000 rows 16.2 / 17.4), and four
-    // groups of waves instead of two where a CU has one block of 64 rows at most, or two of the longest (four / two
-    // groups: 7 heads on 1 of 80, 1500 rows 17.1 / 19.3; 2 heads of 128, 8000 rows 71.7 / 94.5; 7 on 1 of 96, 3500 rows
+    // workgroups to four CUs (one head of 128, 6466 rows 43 / 78; 4 on 2 of 64, 1700 rows 15.1 / 16.0, but 2000 rows, just
+    // past that, 18.5 / 17.8), and four groups of waves instead of two where a CU has one block of 64 rows at
+    // most, or two of the longest (four / two groups: 7 heads on 1 of 80, 1500 rows 17.1 / 19.3; 2 heads of 128, 8000 rows 71.7 / 94.5; 7 on 1 of 96, 3500 rows
     // 34.1 / 44.0; 8 on 1 of 128, 4000 rows 50.7 / 54.9, 10000 rows 257 / 241; but 28 on 4 of 128, 512 rows 14.0 /
     // 12.9, 1024 rows 27.7 / 21.7).
     const int64_t groups = attn_rows_groups(a), blocks = (int64_t(a.M) / kPrefillRows + a.seqs) * a.q_heads;

@@ -7,7 +7,7 @@
 //
 // Bound by what a CU is given of the keys and values (about 90 GB/s: a tile is requested
 // while the one before is worked on, and more do not fit the registers).  50 rows of 8 heads of 256 on one key head,
-// 866 keys: 25 groups of columns, 12.9 us.  More workgroups along the keys would need a workspace for their
+// 866 keys: 25 groups of columns, 13.2 us.  More workgroups along the keys would need a workspace for their
 // parts, which the call does not have; along the values (PARTS) they only read all keys each.
 #include <hip/hip_runtime.h>
 
@@ -30,7 +30,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_rows_kernel(PrefillArgs a, in
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = int(blockIdx.x / PARTS) % a.kv_heads, group = a.q_heads / a.kv_heads;
-    const int64_t b = blocks - 1 - int64_t(blockIdx.x / PARTS / a.kv_heads);  // (the blocks that see most keys first)
+    const int64_t b = blocks - 1 - int64_t(blockIdx.x / PARTS / a.kv_heads);  // (of a sequence, those that see most keys first)
     const int d0 = PARTS == 1 ? 0 : 128 * int(blockIdx.x % PARTS);             // the workgroup's first value,
     const int Dv = PARTS == 1 ? a.head_dim : min(a.head_dim - d0, 128);        // and how many it takes
     auto first = [&](int s) { return int64_t(max(0, min(a.cu_q[s], a.M))) * group / kColumns + s; };
@@ -128,8 +128,8 @@ void launch_parts(const PrefillArgs& a, hipStream_t st) {
 template <int DP>
 void launch_waves(const PrefillArgs& a, const DeviceInfo& dev, hipStream_t st) {
     // Two workgroups for a group of columns, each with half of the values, where both get a CU of their own (8
-    // heads on 1 of 256, graph-replayed, us, one / two: 1 row on 817 keys 14.2 / 11.8, 50 on 866 15.8 / 12.9, 50 on
-    // 3050 39.1 / 31.8, 200 rows 9.2 / 7.9).
+    // heads on 1 of 256, graph-replayed, us, one / two: 1 row on 817 keys 15.3 / 12.6, 50 on 866 16.8 / 13.6, 50 on
+    // 3050 40.2 / 33.3, 200 rows 9.9 / 8.3).
     if constexpr (DP > 128) {
         if (2 * attn_rows_groups(a) <= dev.cus) return launch_parts<DP, 2>(a, st);
     }

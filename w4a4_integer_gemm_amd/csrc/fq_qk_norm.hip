@@ -146,7 +146,7 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(QkNormArgs a, int share) {
 
 // Any even rot_dim: an element's partner may be in any lane, so a head's normed values pass
 // through LDS.  A thread owns 8 consecutive elements of one token, L lanes a head.  20000 tokens of 18
-// heads of 80, 40 of them rotated in halves: 56.2 us for 115 MB (2.0 TB/s); with 32 in halves, which the kernel
+// heads of 80, 40 of them rotated in halves: 54 to 56 us for 115 MB (2.1 TB/s); with 32 in halves, which the kernel
 // above takes, 25.2.
 template <int L>
 __global__ __launch_bounds__(256) void qk_norm_any_kernel(QkNormArgs a, int share) {
