@@ -253,11 +253,12 @@ struct Columns {
             if constexpr (FP8) x[i] *= w[i];
         }
         // p: the weights in bf16; rest: what that leaves of them, in bf16 again
-        const uint32_t w0[4] = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
-        uint32_t w1[4];
+        uint32_t w0[4], w1[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            w0[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
             w1[i] = pack_bf16x2(x[2 * i] - __uint_as_float(w0[i] << 16), x[2 * i + 1] - __uint_as_float(w0[i] & 0xFFFF0000u));
+        }
         const v8bf p = as_bf(make_uint4(w0[0], w0[1], w0[2], w0[3])), rest = as_bf(make_uint4(w1[0], w1[1], w1[2], w1[3]));
 #pragma unroll
         for (int hv = 0; hv < HV; ++hv) {

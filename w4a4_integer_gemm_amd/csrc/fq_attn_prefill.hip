@@ -453,9 +453,9 @@ hipError_t launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& dev, hipS
     // Long keys move both bounds, since a block then passes over them in as many more steps: few rows up to seven
     // workgroups to four CUs (one head of 128, 6466 rows 43 / 78; 4 on 2 of 64, 1700 rows 15.1 / 16.0, but 2000 rows, just
     // past that, 18.5 / 17.8), and four groups of waves instead of two where a CU has one block of 64 rows at
-    // most, or two of the longest (four / two groups: 7 heads on 1 of 80, 1500 rows 17.1 / 19.3; 2 heads of 128, 8000 rows 71.7 / 94.5; 7 on 1 of 96, 3500 rows
-    // 34.1 / 44.0; 8 on 1 of 128, 4000 rows 50.7 / 54.9, 10000 rows 257 / 241; but 28 on 4 of 128, 512 rows 14.0 /
-    // 12.9, 1024 rows 27.7 / 21.7).
+    // most, or two of the longest (four / two groups: 7 heads on 1 of 80, 1500 rows 17.1 / 19.3; 2 heads of 128, 8000
+    // rows 71.7 / 94.5; 7 on 1 of 96, 3500 rows 34.1 / 44.0; 8 on 1 of 128, 4000 rows 50.7 / 54.9, 10000 rows 257 / 241;
+    // but 28 on 4 of 128, 512 rows 14.0 / 12.9, 1024 rows 27.7 / 21.7).
     const int64_t groups = attn_rows_groups(a), blocks = (int64_t(a.M) / kPrefillRows + a.seqs) * a.q_heads;
     const int64_t blocks_64 = (int64_t(a.M) / 64 + a.seqs) * a.q_heads, cus = dev.cus;
     const bool long_keys = a.M_k >= 1024 && a.M_k >= 512 * int64_t(a.seqs), longest = a.M_k >= 2048 * int64_t(a.seqs);

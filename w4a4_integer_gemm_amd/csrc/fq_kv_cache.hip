@@ -12,8 +12,9 @@
 // e4m3: s = max|h| / 448 in float32, q = e4m3(h / s) with one rounding to nearest even; read back as
 // bf16(s q), one rounding more.  A row's scale is one store of the lane that holds its first piece.
 // 32768 tokens, 8 heads of 128, e4m3: written in 39 us, read in 34 to 39 (204 MB, 5.2 and 5.3 to 5.9 TB/s; with a
-// thread each for key and value 46.5 and 43.1); bf16 53 and 41 (269 MB, 5.1 and 6.5 TB/s, the Infinity Cache helping).  4571 tokens read in 6.9 us, 4580 of 4 heads written in
-// 5.1: one round of waves, slot, row and store three latencies in a chain.
+// thread each for key and value 46.5 and 43.1); bf16 53 and 41 (269 MB, 5.1 and 6.5 TB/s, the Infinity Cache
+// helping).  4571 tokens read in 6.9 us, 4580 of 4 heads written in 5.1: one round of waves, slot, row and store three
+// latencies in a chain.
 #include <hip/hip_runtime.h>
 
 #include "fq_device.h"
